@@ -51,7 +51,9 @@ typedef enum {
 
 typedef enum {
   PKV_BF16 = 0,     /* bfloat16                                                            */
-  PKV_FP8_E4M3 = 1  /* OCP FP8 E4M3 ("fn"): code bytes; real value = decode(code) * scale     */
+  PKV_FP8_E4M3 = 1, /* OCP FP8 E4M3 ("fn"): code bytes; real value = decode(code) * scale     */
+  PKV_NVFP4 = 2     /* microscaled 4-bit floating point: E2M1 codes, one E4M3 scale per 16 of them
+                     * (see pkv_cache); real value = code * block scale * scale                  */
 } pkv_dtype;
 
 typedef enum {
@@ -80,7 +82,7 @@ typedef enum {
 /* Device error codes a kernel may record (read with pkv_device_error). */
 enum {
   PKV_DEVERR_NONE = 0,
-  PKV_DEVERR_SLOT_RANGE = 1,   /* kv_store: slot_mapping entry >= num_pages * page_size           */
+  PKV_DEVERR_SLOT_RANGE = 1,   /* kv_store, kv_load: slot_mapping entry >= num_pages * page_size  */
   PKV_DEVERR_PAGE_RANGE = 2,   /* attention: a page id outside [0, num_pages)                     */
   PKV_DEVERR_TIMEOUT = 3       /* a bounded wait inside a kernel ran out; the kernel returned     */
 };
@@ -101,6 +103,19 @@ enum {
  * one uniform row space (stride_page == page_size * stride_token) and head_dim == 128.
  * FP8 pools hold E4M3 codes; k_scale / v_scale (> 0, finite) define real = code * scale on both the
  * write and the read side ("SGLang 源码完全拆解(八)：Attention Backend", section «层与后端的边界»).
+ *
+ * NVFP4 pools (an addition of this library; the pages' caches stop at FP8) hold 72 bytes per (token,
+ * head) row of 128 values: 64 code bytes in k / v and 8 block-scale bytes in k_sf / v_sf.
+ *   - code byte b of a row: element 2b in the low nibble, element 2b + 1 in the high one; a nibble is
+ *     E2M1 (sign, 2 exponent bits, 1 mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives);
+ *   - block-scale byte c: the E4M3 scale of elements 16 c .. 16 c + 15 (never negative as written here);
+ *   - value = code * block scale * k_scale (v_scale), k_scale / v_scale > 0 and finite; amax / 2688 uses
+ *     the whole range of the two factors (6 * 448).
+ * The sf_* fields are read for this dtype only: a caller of the other dtypes may pass the struct
+ * without them.  An "element" of k / v is one code byte, of k_sf / v_sf one scale byte.
+ * Requirements: head_dim == 128, k_sf and v_sf 8-byte aligned, sf strides positive multiples of 8.
+ * Any strides are accepted; the tokens of one head next to each other inside a page (stride_token =
+ * 64, sf_stride_token = 8) keep the 8-byte scales of neighbouring tokens in one memory sector.
  */
 typedef struct pkv_cache {
   void* k;
@@ -113,8 +128,13 @@ typedef struct pkv_cache {
   int64_t stride_page;
   int64_t stride_token;
   int64_t stride_head;
-  float k_scale; /* FP8 only */
-  float v_scale; /* FP8 only */
+  float k_scale; /* FP8 and NVFP4 */
+  float v_scale; /* FP8 and NVFP4 */
+  void* k_sf;              /* NVFP4 only, like every field below */
+  void* v_sf;
+  int64_t sf_stride_page;
+  int64_t sf_stride_token;
+  int64_t sf_stride_head;
 } pkv_cache;
 
 /* ---------------------------------------------------------------------------------------------- */
@@ -132,12 +152,36 @@ typedef struct pkv_cache {
  *                 PKV_DEVERR_SLOT_RANGE in the device error word.
  *   cache         host pointer to the pool description (read during the call only).
  * BF16 pools receive a bit-exact copy.  FP8 pools receive code = E4M3_RNE_satfinite(float(x) *
- * inv_scale) with inv_scale = 1.0f / scale computed once in float32 on the host.
+ * inv_scale) with inv_scale = 1.0f / scale computed once in float32 on the host.  NVFP4 pools receive,
+ * per block of 16 with t = float(x) * inv_scale (one float32 product), the block scale
+ * s = E4M3_RNE_satfinite(max |t| / 6) and the codes E2M1_RNE_satfinite(t / s), all 0 where s is 0; a
+ * block holding a NaN gets the NaN scale (its 16 values read as NaN), an infinity saturates.
  * Two tokens mapped to the same slot in one call race; the caller must not do that.
  * num_tokens == 0 is a no-op.
  */
 int pkv_kv_store(const void* k, const void* v, const int64_t* slot_mapping, int64_t num_tokens,
                  const pkv_cache* cache, void* stream);
+
+/*
+ * pkv_kv_store_scored: pkv_kv_store that also starts the accumulated attention weight of every slot it
+ * writes at zero (scores: see pkv_attn_decode_run_scored), in the same launch.
+ *   scores  device float32 [num_pages, num_kv_heads, page_size], contiguous; NULL = pkv_kv_store.
+ */
+int pkv_kv_store_scored(const void* k, const void* v, const int64_t* slot_mapping, int64_t num_tokens,
+                        const pkv_cache* cache, float* scores, void* stream);
+
+/*
+ * pkv_kv_load: the inverse of pkv_kv_store: read the rows at slot_mapping back as contiguous bf16, e.g.
+ * the cached prefix of an extend whose pool is FP8 or NVFP4 (the prefill runs read bf16 K / V: load the
+ * prefix, then attend to it with a PKV_MODE_RAGGED plan).
+ *   slot_mapping  device int64 [num_tokens], in any order, repeats allowed.  A negative entry gives a
+ *                 row of zeros; an entry >= num_pages * page_size too, recorded as PKV_DEVERR_SLOT_RANGE.
+ *   k, v          device bf16 [num_tokens, num_kv_heads, head_dim], contiguous, 16-byte aligned (out).
+ * BF16 pools give a bit-exact copy; FP8 and NVFP4 values are formed in float32 (code times block scale is
+ * exact there) and rounded to bf16 once.  num_tokens == 0 is a no-op.
+ */
+int pkv_kv_load(const int64_t* slot_mapping, int64_t num_tokens, const pkv_cache* cache, void* k, void* v,
+                void* stream);
 
 /* ---------------------------------------------------------------------------------------------- */
 /* the plan                                                                                       */
@@ -185,7 +229,7 @@ typedef struct pkv_plan_args {
   int32_t window_left;   /* -1: no window; w >= 0 keeps keys P - w .. P                       */
   float sm_scale;        /* <= 0 selects 1 / sqrt(head_dim)                                  */
   int32_t q_dtype;       /* PKV_BF16                                                         */
-  int32_t kv_dtype;      /* PKV_BF16 or PKV_FP8_E4M3 (FP8 KV: decode mode only)               */
+  int32_t kv_dtype;      /* PKV_BF16, PKV_FP8_E4M3 or PKV_NVFP4 (the latter two: decode only) */
   int32_t max_splits;    /* split-KV chunks per (request, KV head): 0 = planner's choice,    */
                          /* 1 = never split, k > 1 = at most k.  Prefill items are split only */
                          /* when there are fewer of them than SMs (at most 64 chunks each)    */
@@ -248,6 +292,52 @@ int pkv_attn_decode_run(const pkv_plan* plan, const void* q, const pkv_cache* ca
                         void* stream);
 int pkv_attn_prefill_run(const pkv_plan* plan, const void* q, const pkv_cache* cache, void* o, float* lse,
                          void* stream);
+
+/*
+ * pkv_attn_decode_run_scored: pkv_attn_decode_run that also accumulates every key's attention weight, the
+ * statistic pkv_kv_evict ranks keys by.  (The pages have no counterpart: an addition of this library.)
+ * For every request with one new token, every KV head h and every visible key j of it,
+ *   scores[page(j), h, offset(j)] += sum over the query heads g of KV head h of exp(scale q_g.k_j - lse_g),
+ * in float32; keys outside a sliding window gain nothing.  o and lse (NULL allowed) as
+ * pkv_attn_decode_run.  Each score is updated by one thread: the sums do not depend on an order.
+ *   scores   device float32 [num_pages, num_kv_heads, page_size], contiguous: one score per slot and KV
+ *            head of this layer's pool (start a slot's score with pkv_kv_store_scored).
+ *   scratch  device, 256-byte aligned, >= pkv_attn_scored_scratch_size() bytes: the scaled scores of the
+ *            visible keys, written and read within the call; under the same rules as the plan workspace.
+ * No page may be listed twice in the plan's kv_indices (a shared page would be updated by two requests
+ * at once): PKV_EINVAL.
+ */
+int pkv_attn_decode_run_scored(const pkv_plan* plan, const void* q, const pkv_cache* cache, void* o, float* lse,
+                               float* scores, void* scratch, size_t scratch_bytes, void* stream);
+
+/* Scratch bytes of pkv_attn_decode_run_scored for this plan (PKV_MODE_DECODE or PKV_MODE_MIXED).  Checks
+ * that no page is listed twice (PKV_EINVAL otherwise). */
+int pkv_attn_scored_scratch_size(const pkv_plan* plan, size_t* bytes);
+
+/*
+ * pkv_kv_evict: cut the planned requests' caches down to `budget` keys by accumulated attention weight, in
+ * place.  (The pages have no counterpart: an addition of this library.)
+ * For every request of the plan with L > budget keys and every KV head separately, the first num_sink
+ * and the last num_recent keys stay, and of the others the budget - num_sink - num_recent with the
+ * largest scores (equal scores: the lower position; a NaN ranks below everything).  The pages are then
+ * compacted so that the fewest rows move, K, V (and block scales) and scores together:
+ *   - survivors at positions < budget - num_recent stay where they are;
+ *   - the others, ascending, fill the evicted positions < budget - num_recent, ascending;
+ *   - the last num_recent keys move, in order, to budget - num_recent .. budget - 1.
+ * The request then has min(L, budget) keys (known on the host: nothing is read back), its pages past
+ * ceil(budget / page_size) are free, and the next step re-plans with the new lengths.  Rows at positions
+ * >= budget, and requests with L <= budget, are left as they are.  Attention over every key does not
+ * depend on the keys' order (their positions are in their values); a sliding window does, so a plan
+ * with window_left >= 0 is refused.
+ *   plan        PKV_MODE_DECODE, PKV_MODE_PREFILL or PKV_MODE_MIXED; its page table says which slots hold
+ *               which keys; no page may be listed twice (PKV_EINVAL).  The plan itself is stale afterwards.
+ *   budget      1 .. 2^21 (as is the longest request); num_sink, num_recent >= 0 with num_sink + num_recent <= budget.
+ *   scores      as pkv_attn_decode_run_scored.
+ *   kept        device int32 [batch_size, num_kv_heads, budget] (out, required): the old position of the
+ *               key now at each position; -1 behind the request's end.
+ */
+int pkv_kv_evict(const pkv_plan* plan, const pkv_cache* cache, float* scores, int32_t budget, int32_t num_sink,
+                 int32_t num_recent, int32_t* kept, void* stream);
 
 /*
  * pkv_attn_prefill_run_merge: pkv_attn_prefill_run whose result is merged into a state the caller

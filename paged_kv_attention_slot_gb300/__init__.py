@@ -21,6 +21,15 @@ through the page table with every prefix key visible, the two states merged by t
     o1, s1 = rag.run_ragged(q, k_new, v_new, return_lse=True)
     o2, s2 = pre.run(q, cache, return_lse=True)
     out, lse = merge_state(o1, s1, o2, s2)
+
+Long contexts in less memory: a 4-bit pool, and eviction by accumulated attention weight:
+
+    cache = KVCache.nvfp4(num_pages, page_size, num_kv_heads, 128, k_scale, v_scale)
+    scores = torch.zeros(num_pages, num_kv_heads, page_size, device="cuda")         # one per slot and KV head
+    kv_store(k_new, v_new, slot_mapping, cache, scores=scores)                     # new slots start at 0
+    plan = Plan().plan(..., mode="decode", kv_dtype="nvfp4", scored=True)
+    out = plan.run(q, cache, scores=scores)                                        # adds each key's weight
+    kept = plan.evict(cache, scores, budget=4096, num_sink=4, num_recent=64)       # then re-plan: min(L, 4096) keys
 """
 
 from __future__ import annotations
@@ -34,7 +43,7 @@ from . import _lib
 from ._lib import PkvError, check, lib
 
 __all__ = [
-    "KVCache", "Plan", "CascadePlan", "PkvError", "kv_store", "merge_state", "device_error", "block_table_to_csr",
+    "KVCache", "Plan", "CascadePlan", "PkvError", "kv_store", "kv_load", "merge_state", "device_error", "block_table_to_csr",
     "token_table_to_page_table", "library_path",
 ]
 
@@ -80,18 +89,38 @@ class KVCache:
     """One layer's K and V pools, [num_pages, page_size, num_kv_heads, head_dim].
 
     bf16 pools are torch.bfloat16 tensors; FP8 pools are torch.uint8 (or float8_e4m3fn) tensors of
-    E4M3 codes with k_scale / v_scale (real value = code * scale).  The last dimension must be
-    contiguous; other strides are passed through as they are.
+    E4M3 codes with k_scale / v_scale (real value = code * scale).  NVFP4 pools are torch.uint8 tensors
+    of E2M1 code pairs, [..., head_dim / 2] (element 2b in the low nibble of byte b), with the E4M3
+    scales of their blocks of 16 in k_sf / v_sf, [..., head_dim / 16] (uint8 or float8_e4m3fn): real
+    value = code * block scale * k_scale / v_scale; giving k_sf and v_sf makes the pool NVFP4.  The
+    last dimension must be contiguous; other strides are passed through as they are.
     """
 
-    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: float = 1.0, v_scale: float = 1.0):
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: float = 1.0, v_scale: float = 1.0,
+                 k_sf: torch.Tensor | None = None, v_sf: torch.Tensor | None = None):
         if k.shape != v.shape or k.dim() != 4:
             raise ValueError("k and v pools must both be [num_pages, page_size, num_kv_heads, head_dim]")
         if k.stride() != v.stride():
             raise ValueError("k and v pools must share strides")
         if k.stride(3) != 1:
             raise ValueError("head_dim must be the contiguous dimension")
-        if k.dtype == torch.bfloat16:
+        byte_types = (torch.uint8, getattr(torch, "float8_e4m3fn", None))
+        if (k_sf is None) != (v_sf is None):
+            raise ValueError("k_sf and v_sf must be given together")
+        if k_sf is not None:
+            if k.dtype != torch.uint8:
+                raise ValueError("the code pools of an NVFP4 cache must be uint8 tensors")
+            if k_sf.dtype not in byte_types or v_sf.dtype != k_sf.dtype:
+                raise ValueError("k_sf and v_sf must be uint8 or float8_e4m3fn tensors")
+            want = tuple(k.shape[:3]) + (k.shape[3] // 8,)
+            if tuple(k_sf.shape) != want or tuple(v_sf.shape) != want or k.shape[3] % 8:
+                raise ValueError("k_sf and v_sf must be [num_pages, page_size, num_kv_heads, head_dim / 16]")
+            if k_sf.stride() != v_sf.stride() or k_sf.stride(3) != 1:
+                raise ValueError("k_sf and v_sf must share strides, with the last dimension contiguous")
+            if any(t.device != k.device for t in (v, k_sf, v_sf)):
+                raise ValueError("the pools and their block scales must be on one device")
+            dtype = _lib.PKV_NVFP4
+        elif k.dtype == torch.bfloat16:
             dtype = _lib.PKV_BF16
         elif k.dtype in (torch.uint8, getattr(torch, "float8_e4m3fn", None)):
             dtype = _lib.PKV_FP8_E4M3
@@ -101,10 +130,24 @@ class KVCache:
             raise ValueError("k and v pools must have the same dtype")
         self.k, self.v = k, v
         self.k_scale, self.v_scale = float(k_scale), float(v_scale)
+        self.k_sf, self.v_sf = k_sf, v_sf
         self.dtype = dtype
+        sf = (None, None, 0, 0, 0) if k_sf is None else (k_sf.data_ptr(), v_sf.data_ptr(), *k_sf.stride()[:3])
         self.struct = _lib.pkv_cache(
-            k.data_ptr(), v.data_ptr(), k.shape[0], k.shape[1], k.shape[2], k.shape[3], dtype,
-            k.stride(0), k.stride(1), k.stride(2), self.k_scale, self.v_scale)
+            k.data_ptr(), v.data_ptr(), k.shape[0], k.shape[1], k.shape[2], self.head_dim, dtype,
+            k.stride(0), k.stride(1), k.stride(2), self.k_scale, self.v_scale, *sf)
+
+    @classmethod
+    def nvfp4(cls, num_pages: int, page_size: int, num_kv_heads: int, head_dim: int, k_scale: float = 1.0,
+              v_scale: float = 1.0, device="cuda") -> "KVCache":
+        """A zeroed NVFP4 cache (72 bytes per key, KV head and tensor at head_dim 128) whose pages hold the
+        tokens of one head next to each other, the layout the reads are fastest on.  k_scale and v_scale:
+        amax / 2688 uses the whole range of code and block scale."""
+        if head_dim % 16:
+            raise ValueError("head_dim must be a multiple of 16")
+        pools = [torch.zeros((num_pages, num_kv_heads, page_size, w), dtype=torch.uint8, device=device).transpose(1, 2)
+                 for w in (head_dim // 2, head_dim // 2, head_dim // 16, head_dim // 16)]
+        return cls(pools[0], pools[1], k_scale, v_scale, k_sf=pools[2], v_sf=pools[3])
 
     @property
     def num_pages(self):
@@ -120,11 +163,42 @@ class KVCache:
 
     @property
     def head_dim(self):
-        return self.k.shape[3]
+        return self.k.shape[3] if self.k_sf is None else 2 * self.k.shape[3]
 
 
-def kv_store(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor, cache: KVCache, stream=None) -> None:
-    """Write k, v ([T, num_kv_heads, head_dim] bf16, contiguous) at slot_mapping ([T] int64, device)."""
+def _check_device(t: torch.Tensor, name: str) -> None:
+    """The library launches on the current device."""
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device, not on {t.device}")
+
+
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """An output tensor whose memory belongs to the stream that will write it."""
+    if isinstance(stream, torch.cuda.Stream):
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=device)
+    return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _check_scores(scores: torch.Tensor, cache: KVCache) -> int:
+    """Address of an accumulated-weight tensor of the cache's slots."""
+    if scores.dtype != torch.float32 or not scores.is_contiguous():
+        raise ValueError("scores must be a contiguous float32 tensor")
+    if tuple(scores.shape) != (cache.num_pages, cache.num_kv_heads, cache.page_size):
+        raise ValueError(f"scores must be [{cache.num_pages}, {cache.num_kv_heads}, {cache.page_size}]: "
+                         "[num_pages, num_kv_heads, page_size]")
+    if scores.device != cache.k.device:
+        raise ValueError("scores must be on the cache's device")
+    _check_device(scores, "scores")
+    return scores.data_ptr()
+
+
+def kv_store(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor, cache: KVCache, stream=None,
+             scores: torch.Tensor | None = None) -> None:
+    """Write k, v ([T, num_kv_heads, head_dim] bf16, contiguous) at slot_mapping ([T] int64, device).
+
+    scores: float32 [num_pages, num_kv_heads, page_size] accumulated attention weights of the slots
+    (see Plan.run); those of the written slots are set to 0 in the same launch."""
     if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
         raise ValueError("k and v must be bf16")
     if not (k.is_contiguous() and v.is_contiguous() and slot_mapping.is_contiguous()):
@@ -134,8 +208,42 @@ def kv_store(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor, cache
     T = k.shape[0]
     if v.shape != k.shape or slot_mapping.shape[0] != T or tuple(k.shape[1:]) != (cache.num_kv_heads, cache.head_dim):
         raise ValueError("shape mismatch between k, v, slot_mapping and the cache")
+    if scores is not None or cache.dtype == _lib.PKV_NVFP4:
+        if any(t.device != cache.k.device for t in (k, v, slot_mapping)):
+            raise ValueError("k, v and slot_mapping must be on the cache's device")
+        _check_device(cache.k, "the cache")
+    if scores is not None:
+        check(lib().pkv_kv_store_scored(k.data_ptr(), v.data_ptr(), slot_mapping.data_ptr(), T, C.byref(cache.struct),
+                                        _check_scores(scores, cache), _stream_ptr(stream)))
+        return
     check(lib().pkv_kv_store(k.data_ptr(), v.data_ptr(), slot_mapping.data_ptr(), T, C.byref(cache.struct),
                              _stream_ptr(stream)))
+
+
+def kv_load(slot_mapping: torch.Tensor, cache: KVCache, k: torch.Tensor | None = None, v: torch.Tensor | None = None,
+            stream=None):
+    """Read the rows at slot_mapping ([T] int64, device) back as contiguous bf16 k, v [T, num_kv_heads, head_dim].
+
+    The way from an FP8 or NVFP4 pool to the prefill runs, which read bf16: load the cached prefix and
+    attend to it with a "ragged" plan.  A negative slot gives a row of zeros.  Returns (k, v)."""
+    if slot_mapping.dtype != torch.int64 or slot_mapping.dim() != 1 or not slot_mapping.is_contiguous():
+        raise ValueError("slot_mapping must be a contiguous one-dimensional int64 tensor")
+    if slot_mapping.device != cache.k.device:
+        raise ValueError("slot_mapping must be on the cache's device")
+    shape = (slot_mapping.shape[0], cache.num_kv_heads, cache.head_dim)
+    for name, t in (("k", k), ("v", v)):
+        if t is None:
+            continue
+        if t.dtype != torch.bfloat16 or not t.is_contiguous() or tuple(t.shape) != shape or t.device != cache.k.device:
+            raise ValueError(f"{name} must be a contiguous bf16 tensor {list(shape)} on the cache's device")
+    _check_device(cache.k, "the cache")
+    if k is None:
+        k = _new(shape, torch.bfloat16, cache.k.device, stream)
+    if v is None:
+        v = _new(shape, torch.bfloat16, cache.k.device, stream)
+    check(lib().pkv_kv_load(slot_mapping.data_ptr(), shape[0], C.byref(cache.struct), k.data_ptr(), v.data_ptr(),
+                            _stream_ptr(stream)))
+    return k, v
 
 
 def device_error(reset: bool = True, stream=None) -> int:
@@ -156,7 +264,7 @@ def set_wait_limit(clock_cycles: int = 0) -> None:
 
 _MODES = {"decode": _lib.PKV_MODE_DECODE, "prefill": _lib.PKV_MODE_PREFILL, "extend": _lib.PKV_MODE_PREFILL,
           "mixed": _lib.PKV_MODE_MIXED, "ragged": _lib.PKV_MODE_RAGGED, "paged_ragged": _lib.PKV_MODE_PAGED_RAGGED}
-_KV_DTYPES = {"bf16": _lib.PKV_BF16, "e4m3": _lib.PKV_FP8_E4M3, "fp8": _lib.PKV_FP8_E4M3}
+_KV_DTYPES = {"bf16": _lib.PKV_BF16, "e4m3": _lib.PKV_FP8_E4M3, "fp8": _lib.PKV_FP8_E4M3, "nvfp4": _lib.PKV_NVFP4}
 
 
 class Plan:
@@ -167,6 +275,8 @@ class Plan:
         check(lib().pkv_plan_create(C.byref(h)))
         self._h = h
         self.workspace = None
+        self.scratch = None  # of scored runs
+        self.scored = False
         self.mode = None
         self._keep = None
 
@@ -202,12 +312,15 @@ class Plan:
 
     def plan(self, qo_indptr, kv_indptr, kv_indices, last_page_len, *, num_qo_heads, num_kv_heads, head_dim,
              page_size=1, mode="decode", window_left=-1, sm_scale=0.0, kv_dtype="bf16", max_splits=0, num_sms=0,
-             causal=True, workspace: torch.Tensor | None = None, host_only: bool = False, stream=None) -> "Plan":
+             causal=True, workspace: torch.Tensor | None = None, host_only: bool = False, stream=None,
+             scored: bool = False) -> "Plan":
         """Plan a batch.  Host int arrays in; the binding keeps a device workspace (grown on demand).
 
         mode "ragged": kv_indptr holds row offsets into contiguous k / v tensors (run with
         run_ragged); kv_indices, last_page_len and page_size are ignored.  causal=False: every query
-        sees all keys of its request (prefill / ragged plans)."""
+        sees all keys of its request (prefill / ragged plans).  scored=True (decode and mixed plans):
+        reserve the scratch of run(..., scores=...) and check that no page is listed twice.  A workspace
+        or scratch that a captured graph uses must not grow: plan the largest batch first."""
         a, keep = self._args(qo_indptr, kv_indptr, kv_indices, last_page_len, num_qo_heads, num_kv_heads, head_dim,
                              page_size, mode, window_left, sm_scale, kv_dtype, max_splits, num_sms, causal)
         if host_only:
@@ -227,13 +340,24 @@ class Plan:
                 st = lib().pkv_attn_plan(self._h, C.byref(a), self.workspace.data_ptr(), self.workspace.numel(),
                                          _stream_ptr(stream))
             check(st)
+        self.scored = False
         self.mode = mode
         self.num_qo_heads = num_qo_heads
         self.head_dim = head_dim
+        self.batch_size = max(0, len(keep[0]) - 1)
         self.total_tokens = int(keep[0][-1]) if len(keep[0]) else 0
         self.kv_rows = int(keep[1][-1]) if (mode == "ragged" and len(keep[1])) else 0
         self.num_kv_heads = num_kv_heads
         self._keep = keep
+        if scored:
+            n = C.c_size_t(0)
+            check(lib().pkv_attn_scored_scratch_size(self._h, C.byref(n)))
+            if not host_only and (self.scratch is None or self.scratch.numel() < n.value
+                                  or self.scratch.device != self.workspace.device):
+                self._scratch_stream = _stream_ptr(None)
+                self.scratch = torch.empty(int(n.value) + (int(n.value) >> 2), dtype=torch.uint8,
+                                           device=self.workspace.device)
+            self.scored = True
         return self
 
     def info(self) -> dict:
@@ -293,15 +417,25 @@ class Plan:
         return (out, lse) if (return_lse or lse is not None) else out
 
     def run(self, q: torch.Tensor, cache: KVCache, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
-            return_lse: bool = False, merge_into: bool = False, stream=None):
+            return_lse: bool = False, merge_into: bool = False, stream=None, scores: torch.Tensor | None = None):
         """Attention for every planned token row; q is [total_tokens, num_qo_heads, head_dim] bf16.
 
         merge_into=True (prefill plans): out / lse hold a state on entry (e.g. from run_ragged over the
-        new tokens) and receive the merge of that state with this pass's (pkv_attn_prefill_run_merge)."""
+        new tokens) and receive the merge of that state with this pass's (pkv_attn_prefill_run_merge).
+
+        scores (plans made with scored=True): float32 [num_pages, num_kv_heads, page_size]; every visible
+        key of a request with one new token gains its attention weight, summed over the query heads of
+        its KV head (pkv_attn_decode_run_scored).  Rows of longer requests add nothing."""
         if self.mode == "ragged":
             raise ValueError("a ragged plan runs with run_ragged(q, k, v)")
         if self.mode == "paged_ragged":
             raise ValueError("a paged_ragged plan runs with run_paged_ragged(q, cache, k_new, v_new)")
+        if scores is not None:
+            if not self.scored or merge_into:
+                raise ValueError("scores need a plan made with scored=True (decode or mixed) and no merge_into")
+            addr = _check_scores(scores, cache)
+            if self.scratch is None or q.device != scores.device:
+                raise ValueError("a scored run needs a plan with a workspace and q on the cache's device")
         if merge_into:
             if self.mode not in ("prefill", "extend") or out is None or lse is None:
                 raise ValueError("merge_into needs a prefill plan and the held state in out and lse")
@@ -310,7 +444,16 @@ class Plan:
                                                    lse.data_ptr(), _stream_ptr(stream)))
             return out, lse
         out, lse = self._outputs(q, out, lse, return_lse)
-        if self.mode == "decode":
+        if scores is not None:
+            s = _stream_ptr(stream)
+            if s != self._scratch_stream and not torch.cuda.is_current_stream_capturing():
+                # used off the stream it was allocated on: its memory is not reused before this run is done
+                self.scratch.record_stream(stream or torch.cuda.current_stream())
+            check(lib().pkv_attn_decode_run_scored(
+                self._h, q.data_ptr(), C.byref(cache.struct), out.data_ptr(), lse.data_ptr() if lse is not None else None,
+                addr, self.scratch.data_ptr(), self.scratch.numel(), s))
+            fns = [lib().pkv_attn_prefill_run] if self.mode == "mixed" else []
+        elif self.mode == "decode":
             fns = [lib().pkv_attn_decode_run]
         elif self.mode == "mixed":  # one-token rows on the decode kernel, the rest on the prefill kernel
             fns = [lib().pkv_attn_decode_run, lib().pkv_attn_prefill_run]
@@ -320,6 +463,34 @@ class Plan:
             check(fn(self._h, q.data_ptr(), C.byref(cache.struct), out.data_ptr(),
                      lse.data_ptr() if lse is not None else None, _stream_ptr(stream)))
         return (out, lse) if (return_lse or lse is not None) else out
+
+
+    def evict(self, cache: KVCache, scores: torch.Tensor, budget: int, num_sink: int = 0, num_recent: int = 0,
+              kept: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """Cut every planned request down to `budget` keys per KV head by its accumulated weights, in place.
+
+        The first num_sink and last num_recent keys stay, and of the others those with the largest
+        scores (equal scores: the lower position).  K, V and scores are compacted to positions
+        0 .. min(L, budget) - 1 of the request's own pages, moving as few rows as possible (survivors
+        past the budget fill the evicted places; the recent keys keep their order at the end); plan again
+        with the new lengths.  Returns kept, int32 [batch, num_kv_heads, budget]: the old position of
+        the key now at each position, -1 behind the end."""
+        addr = _check_scores(scores, cache)
+        if self.mode is None or self.mode in ("ragged", "paged_ragged"):
+            raise ValueError("evict needs a decode, prefill or mixed plan")
+        budget, num_sink, num_recent = int(budget), int(num_sink), int(num_recent)
+        if not (1 <= budget <= 2 ** 21 and num_sink >= 0 and num_recent >= 0 and num_sink + num_recent <= budget):
+            raise ValueError("evict needs 1 <= budget <= 2**21, num_sink >= 0, num_recent >= 0 and "
+                             "num_sink + num_recent <= budget")
+        shape = (self.batch_size, cache.num_kv_heads, budget)
+        if kept is None:
+            kept = _new(shape, torch.int32, scores.device, stream)
+        elif (kept.dtype != torch.int32 or not kept.is_contiguous() or tuple(kept.shape) != shape
+              or kept.device != scores.device):
+            raise ValueError(f"kept must be a contiguous int32 tensor {list(shape)} on the cache's device")
+        check(lib().pkv_kv_evict(self._h, C.byref(cache.struct), addr, budget, num_sink, num_recent, kept.data_ptr(),
+                                 _stream_ptr(stream)))
+        return kept
 
 
 class CascadePlan:

@@ -22,6 +22,7 @@ PKV_EDEVICE = -5
 
 PKV_BF16 = 0
 PKV_FP8_E4M3 = 1
+PKV_NVFP4 = 2
 PKV_MODE_DECODE = 0
 PKV_MODE_PREFILL = 1
 PKV_MODE_MIXED = 2
@@ -53,6 +54,11 @@ class pkv_cache(C.Structure):
         ("stride_head", C.c_int64),
         ("k_scale", C.c_float),
         ("v_scale", C.c_float),
+        ("k_sf", C.c_void_p),
+        ("v_sf", C.c_void_p),
+        ("sf_stride_page", C.c_int64),
+        ("sf_stride_token", C.c_int64),
+        ("sf_stride_head", C.c_int64),
     ]
 
 
@@ -105,11 +111,19 @@ class pkv_plan_info(C.Structure):
 
 _SIGS = {
     "pkv_kv_store": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64, C.POINTER(pkv_cache), C.c_void_p]),
+    "pkv_kv_store_scored": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64, C.POINTER(pkv_cache), C.c_void_p,
+                                      C.c_void_p]),
+    "pkv_kv_load": (C.c_int, [C.c_void_p, C.c_int64, C.POINTER(pkv_cache), C.c_void_p, C.c_void_p, C.c_void_p]),
+    "pkv_kv_evict": (C.c_int, [C.c_void_p, C.POINTER(pkv_cache), C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_void_p,
+                               C.c_void_p]),
     "pkv_plan_create": (C.c_int, [C.POINTER(C.c_void_p)]),
     "pkv_plan_destroy": (None, [C.c_void_p]),
     "pkv_plan_workspace_size": (C.c_int, [C.POINTER(pkv_plan_args), C.POINTER(C.c_size_t)]),
     "pkv_attn_plan": (C.c_int, [C.c_void_p, C.POINTER(pkv_plan_args), C.c_void_p, C.c_size_t, C.c_void_p]),
     "pkv_attn_decode_run": (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(pkv_cache), C.c_void_p, C.c_void_p, C.c_void_p]),
+    "pkv_attn_decode_run_scored": (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(pkv_cache), C.c_void_p, C.c_void_p,
+                                             C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "pkv_attn_scored_scratch_size": (C.c_int, [C.c_void_p, C.POINTER(C.c_size_t)]),
     "pkv_attn_decode_run_noalloc": (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(pkv_cache), C.c_void_p, C.c_void_p, C.c_void_p]),
     "pkv_attn_prefill_run": (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(pkv_cache), C.c_void_p, C.c_void_p, C.c_void_p]),
     "pkv_attn_prefill_run_merge": (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(pkv_cache), C.c_void_p, C.c_void_p, C.c_void_p]),

@@ -21,6 +21,7 @@
 #include <cmath>
 #include <cstdio>
 #include <cstring>
+#include <new>
 #include <string>
 #include <vector>
 
@@ -226,9 +227,10 @@ int build_plan(const pkv_plan_args* a, pkv_plan* P) {
   if (!causal && a->window_left >= 0) return fail(PKV_EINVAL, "a sliding window needs causal == 1");
   if (!(std::isfinite(a->sm_scale))) return fail(PKV_EINVAL, "sm_scale is not finite");
   if (a->q_dtype != PKV_BF16) return fail(PKV_EUNSUPPORTED, "q_dtype must be PKV_BF16");
-  if (a->kv_dtype != PKV_BF16 && a->kv_dtype != PKV_FP8_E4M3) return fail(PKV_EINVAL, "unknown kv_dtype");
-  if (a->kv_dtype == PKV_FP8_E4M3 && a->head_dim != 128)
-    return fail(PKV_EUNSUPPORTED, "FP8 KV needs head_dim 128");
+  if (a->kv_dtype != PKV_BF16 && a->kv_dtype != PKV_FP8_E4M3 && a->kv_dtype != PKV_NVFP4)
+    return fail(PKV_EINVAL, "unknown kv_dtype");
+  if (a->kv_dtype != PKV_BF16 && a->head_dim != 128)
+    return fail(PKV_EUNSUPPORTED, a->kv_dtype == PKV_NVFP4 ? "NVFP4 KV needs head_dim 128" : "FP8 KV needs head_dim 128");
   if (a->max_splits < 0) return fail(PKV_EINVAL, "max_splits < 0");
   const int32_t G = a->num_qo_heads / a->num_kv_heads;
   // requests with more than one new token go to the prefill kernel (all of them in prefill mode)
@@ -253,6 +255,7 @@ int build_plan(const pkv_plan_args* a, pkv_plan* P) {
 
   P->req.assign(B, ReqInfo{});
   P->max_page_id = -1;
+  P->pages_unique.store(-1, std::memory_order_relaxed);
   int64_t total_tokens = B > 0 ? a->qo_indptr[B] : 0;
   for (int32_t i = 0; i < B; ++i) {
     const int64_t n = (int64_t)a->qo_indptr[i + 1] - a->qo_indptr[i];
@@ -575,6 +578,25 @@ int build_plan(const pkv_plan_args* a, pkv_plan* P) {
   return PKV_OK;
 }
 
+// The scales of a quantised pool and, for NVFP4, its block-scale pools.
+int check_scales(const pkv_cache* c) {
+  if (c->dtype == PKV_BF16) return PKV_OK;
+  const bool fp4 = c->dtype == PKV_NVFP4;
+  if (!(c->k_scale > 0.f) || !(c->v_scale > 0.f) || !std::isfinite(c->k_scale) || !std::isfinite(c->v_scale))
+    return fail(PKV_EINVAL, fp4 ? "NVFP4 cache scales must be finite and > 0" : "FP8 cache scales must be finite and > 0");
+  if (!fp4) return PKV_OK;
+  if (!std::isfinite(1.0f / c->k_scale) || !std::isfinite(1.0f / c->v_scale))
+    return fail(PKV_EINVAL, "NVFP4 cache scales must have finite reciprocals");
+  if (c->head_dim != 128) return fail(PKV_EUNSUPPORTED, "an NVFP4 cache needs head_dim 128");
+  if (!c->k_sf || !c->v_sf) return fail(PKV_EINVAL, "an NVFP4 cache needs k_sf and v_sf");
+  if (((uintptr_t)c->k_sf | (uintptr_t)c->v_sf) & 7) return fail(PKV_EINVAL, "k_sf and v_sf must be 8-byte aligned");
+  if (c->sf_stride_page <= 0 || c->sf_stride_token <= 0 || c->sf_stride_head <= 0)
+    return fail(PKV_EINVAL, "block-scale strides must be positive");
+  if (c->sf_stride_page % 8 || c->sf_stride_token % 8 || c->sf_stride_head % 8)
+    return fail(PKV_EINVAL, "block-scale strides must be multiples of 8 bytes");
+  return PKV_OK;
+}
+
 }  // namespace
 
 int pkv::check_cache(const pkv_plan* P, const pkv_cache* c) {
@@ -585,18 +607,37 @@ int pkv::check_cache(const pkv_plan* P, const pkv_cache* c) {
   if (c->num_pages <= P->max_page_id)
     return fail(PKV_EINVAL, "the plan references page " + std::to_string(P->max_page_id) + " but the pool has " +
                                 std::to_string(c->num_pages) + " pages");
-  const int64_t esz = c->dtype == PKV_FP8_E4M3 ? 1 : 2;
-  const int64_t vec = 16 / esz;
+  const int64_t vec = 16 / pool_elem_bytes(c->dtype);
   if (((uintptr_t)c->k | (uintptr_t)c->v) & 15) return fail(PKV_EINVAL, "cache k/v must be 16-byte aligned");
   if (c->stride_page % vec || c->stride_token % vec || c->stride_head % vec)
     return fail(PKV_EINVAL, "cache strides must be multiples of 16 bytes");
   if (c->stride_page <= 0 || c->stride_token <= 0 || c->stride_head <= 0)
     return fail(PKV_EINVAL, "cache strides must be positive");
-  if (c->dtype == PKV_FP8_E4M3) {
-    if (!(c->k_scale > 0.f) || !(c->v_scale > 0.f) || !std::isfinite(c->k_scale) || !std::isfinite(c->v_scale))
-      return fail(PKV_EINVAL, "FP8 cache scales must be finite and > 0");
+  return check_scales(c);
+}
+
+void pkv::set_cache_params(RunParams& p, const pkv_plan* P, const pkv_cache* c) {
+  const int64_t esz = pool_elem_bytes(c->dtype);
+  p.k_pool = (const char*)c->k;
+  p.v_pool = (const char*)c->v;
+  p.stride_page_b = c->stride_page * esz;
+  p.stride_token_b = c->stride_token * esz;
+  p.stride_head_b = c->stride_head * esz;
+  p.k_sf = p.v_sf = nullptr;
+  p.sf_page_b = p.sf_token_b = p.sf_head_b = 0;
+  if (c->dtype == PKV_NVFP4) {
+    p.k_sf = (const char*)c->k_sf;
+    p.v_sf = (const char*)c->v_sf;
+    p.sf_page_b = c->sf_stride_page;
+    p.sf_token_b = c->sf_stride_token;
+    p.sf_head_b = c->sf_stride_head;
   }
-  return PKV_OK;
+  p.num_pages = c->num_pages;
+  p.page_size = P->ps;
+  const float log2e = 1.4426950408889634f;
+  const bool scaled = c->dtype != PKV_BF16;
+  p.scale_log2 = P->sm_scale * log2e * (scaled ? c->k_scale : 1.0f);
+  p.out_scale = scaled ? c->v_scale : 1.0f;
 }
 
 namespace {
@@ -619,14 +660,7 @@ pkv::RunParams make_params(const pkv_plan* P, const void* q, const pkv_cache* c,
   p.q = q;
   p.o = o;
   p.lse = lse;
-  const int64_t esz = c->dtype == PKV_FP8_E4M3 ? 1 : 2;
-  p.k_pool = (const char*)c->k;
-  p.v_pool = (const char*)c->v;
-  p.stride_page_b = c->stride_page * esz;
-  p.stride_token_b = c->stride_token * esz;
-  p.stride_head_b = c->stride_head * esz;
-  p.num_pages = c->num_pages;
-  p.page_size = P->ps;
+  set_cache_params(p, P, c);
   p.num_qo_heads = P->Hq;
   p.num_kv_heads = P->Hkv;
   p.group = P->Hq / P->Hkv;
@@ -638,9 +672,6 @@ pkv::RunParams make_params(const pkv_plan* P, const void* q, const pkv_cache* c,
   p.ext_row_b = 0;
   p.wait_limit_k = (int32_t)((g_wait_limit.load(std::memory_order_relaxed) + 1023) >> 10);
   p.hold_wait = g_hold_wait.load(std::memory_order_relaxed);
-  const float log2e = 1.4426950408889634f;
-  p.scale_log2 = P->sm_scale * log2e * (c->dtype == PKV_FP8_E4M3 ? c->k_scale : 1.0f);
-  p.out_scale = c->dtype == PKV_FP8_E4M3 ? c->v_scale : 1.0f;
   p.num_work = count;
   p.num_merge = (int64_t)P->merge.size();
   return p;
@@ -796,32 +827,94 @@ int pkv_attn_plan(pkv_plan* plan, const pkv_plan_args* args, void* workspace, si
   return PKV_OK;
 }
 
-int pkv_kv_store(const void* k, const void* v, const int64_t* slot_mapping, int64_t num_tokens, const pkv_cache* cache,
-                 void* stream) {
+}  // extern "C"
+
+namespace {
+
+// The pool checks kv_store and kv_load share.
+int check_pool(const pkv_cache* cache) {
+  if (cache->head_dim != 64 && cache->head_dim != 128) return fail(PKV_EUNSUPPORTED, "head_dim must be 64 or 128");
+  if (cache->dtype != PKV_BF16 && cache->dtype != PKV_FP8_E4M3 && cache->dtype != PKV_NVFP4)
+    return fail(PKV_EINVAL, "unknown cache dtype");
+  if (cache->num_kv_heads <= 0 || cache->page_size < 1 || cache->num_pages < 0)
+    return fail(PKV_EINVAL, "bad cache geometry");
+  const int64_t esz = pkv::pool_elem_bytes(cache->dtype);
+  const int64_t vec = cache->dtype == PKV_BF16 ? 16 : 8;  // bytes of each pool access
+  if (((uintptr_t)cache->k | (uintptr_t)cache->v) & (vec - 1)) return fail(PKV_EINVAL, "cache k/v misaligned");
+  if ((cache->stride_page * esz) % vec || (cache->stride_token * esz) % vec || (cache->stride_head * esz) % vec)
+    return fail(PKV_EINVAL, "cache strides must be multiples of 16 bytes (bf16) or 8 bytes (fp8, nvfp4)");
+  return check_scales(cache);
+}
+
+int kv_store(const void* k, const void* v, const int64_t* slot_mapping, int64_t num_tokens, const pkv_cache* cache,
+             float* scores, void* stream) {
   if (num_tokens < 0) return fail(PKV_EINVAL, "num_tokens < 0");
   if (!cache) return fail(PKV_EINVAL, "cache is NULL");
   if (num_tokens == 0) return PKV_OK;
   if (!k || !v || !slot_mapping || !cache->k || !cache->v) return fail(PKV_EINVAL, "NULL pointer argument");
-  if (cache->head_dim != 64 && cache->head_dim != 128) return fail(PKV_EUNSUPPORTED, "head_dim must be 64 or 128");
-  if (cache->dtype != PKV_BF16 && cache->dtype != PKV_FP8_E4M3) return fail(PKV_EINVAL, "unknown cache dtype");
-  if (cache->num_kv_heads <= 0 || cache->page_size < 1 || cache->num_pages < 0)
-    return fail(PKV_EINVAL, "bad cache geometry");
-  const int64_t esz = cache->dtype == PKV_FP8_E4M3 ? 1 : 2;
-  const int64_t vec = cache->dtype == PKV_FP8_E4M3 ? 8 : 16;  // bytes each thread stores
+  int st = check_pool(cache);
+  if (st != PKV_OK) return st;
   if (((uintptr_t)k | (uintptr_t)v) & 15) return fail(PKV_EINVAL, "k and v must be 16-byte aligned");
-  if (((uintptr_t)cache->k | (uintptr_t)cache->v) & (vec - 1)) return fail(PKV_EINVAL, "cache k/v misaligned");
-  if ((cache->stride_page * esz) % vec || (cache->stride_token * esz) % vec || (cache->stride_head * esz) % vec)
-    return fail(PKV_EINVAL, "cache strides must be multiples of 16 bytes (bf16) or 8 bytes (fp8)");
+  if ((uintptr_t)scores & 3) return fail(PKV_EINVAL, "scores must be 4-byte aligned");
   float inv_k = 1.f, inv_v = 1.f;
-  if (cache->dtype == PKV_FP8_E4M3) {
-    if (!(cache->k_scale > 0.f) || !(cache->v_scale > 0.f) || !std::isfinite(cache->k_scale) ||
-        !std::isfinite(cache->v_scale))
-      return fail(PKV_EINVAL, "FP8 cache scales must be finite and > 0");
+  if (cache->dtype != PKV_BF16) {
     inv_k = 1.0f / cache->k_scale;
     inv_v = 1.0f / cache->v_scale;
   }
-  PKV_CUDA(pkv::launch_kv_store(k, v, slot_mapping, num_tokens, *cache, inv_k, inv_v, (cudaStream_t)stream),
+  PKV_CUDA(pkv::launch_kv_store(k, v, slot_mapping, num_tokens, *cache, inv_k, inv_v, scores, (cudaStream_t)stream),
            "kv_store launch");
+  return PKV_OK;
+}
+
+// No page id twice in the plan's page table (scores and eviction update each slot for one request).
+int check_pages_unique(const pkv_plan* P) {
+  int u = P->pages_unique.load(std::memory_order_relaxed);
+  if (u < 0) {
+    try {
+      u = 1;
+      if (P->max_page_id < 64 * (int64_t)P->indices.size()) {  // a bit per page of the pool's used range
+        std::vector<bool> seen((size_t)(P->max_page_id + 1), false);
+        for (int32_t id : P->indices) {
+          if (seen[(size_t)id]) u = 0;
+          seen[(size_t)id] = true;
+        }
+      } else {  // few pages of a large pool
+        std::vector<int32_t> ids(P->indices);
+        std::sort(ids.begin(), ids.end());
+        if (std::adjacent_find(ids.begin(), ids.end()) != ids.end()) u = 0;
+      }
+    } catch (const std::bad_alloc&) {
+      return fail(PKV_EUNSUPPORTED, "out of host memory while checking the page table");
+    }
+    P->pages_unique.store(u, std::memory_order_relaxed);
+  }
+  return u ? PKV_OK : fail(PKV_EINVAL, "a page is listed twice in kv_indices: accumulated scores and eviction need every "
+                                       "page to belong to one request");
+}
+
+}  // namespace
+
+extern "C" {
+
+int pkv_kv_store(const void* k, const void* v, const int64_t* slot_mapping, int64_t num_tokens, const pkv_cache* cache,
+                 void* stream) {
+  return kv_store(k, v, slot_mapping, num_tokens, cache, nullptr, stream);
+}
+
+int pkv_kv_store_scored(const void* k, const void* v, const int64_t* slot_mapping, int64_t num_tokens,
+                        const pkv_cache* cache, float* scores, void* stream) {
+  return kv_store(k, v, slot_mapping, num_tokens, cache, scores, stream);
+}
+
+int pkv_kv_load(const int64_t* slot_mapping, int64_t num_tokens, const pkv_cache* cache, void* k, void* v, void* stream) {
+  if (num_tokens < 0) return fail(PKV_EINVAL, "num_tokens < 0");
+  if (!cache) return fail(PKV_EINVAL, "cache is NULL");
+  if (num_tokens == 0) return PKV_OK;
+  if (!k || !v || !slot_mapping || !cache->k || !cache->v) return fail(PKV_EINVAL, "NULL pointer argument");
+  int st = check_pool(cache);
+  if (st != PKV_OK) return st;
+  if (((uintptr_t)k | (uintptr_t)v) & 15) return fail(PKV_EINVAL, "k and v must be 16-byte aligned");
+  PKV_CUDA(pkv::launch_kv_load(slot_mapping, num_tokens, *cache, k, v, (cudaStream_t)stream), "kv_load launch");
   return PKV_OK;
 }
 
@@ -832,6 +925,95 @@ int pkv_attn_decode_run(const pkv_plan* plan, const void* q, const pkv_cache* ca
   if (plan->num_decode_work == 0) return PKV_OK;
   pkv::RunParams p = make_params(plan, q, cache, o, lse, 0, plan->num_decode_work);
   PKV_CUDA(pkv::launch_decode(p, cache->dtype, (cudaStream_t)stream), "decode launch");
+  return PKV_OK;
+}
+
+int pkv_attn_scored_scratch_size(const pkv_plan* plan, size_t* bytes) {
+  if (!bytes) return fail(PKV_EINVAL, "bytes is NULL");
+  if (!plan || !plan->valid) return fail(PKV_EINVAL, "plan is NULL or has not been planned");
+  if (plan->mode != PKV_MODE_DECODE && plan->mode != PKV_MODE_MIXED)
+    return fail(PKV_EINVAL, "accumulated scores need a PKV_MODE_DECODE or PKV_MODE_MIXED plan");
+  int st = check_pages_unique(plan);
+  if (st != PKV_OK) return st;
+  *bytes = pkv::scored_lse_offset(plan) + (size_t)plan->total_tokens * plan->Hq * sizeof(float);
+  return PKV_OK;
+}
+
+int pkv_attn_decode_run_scored(const pkv_plan* plan, const void* q, const pkv_cache* cache, void* o, float* lse,
+                               float* scores, void* scratch, size_t scratch_bytes, void* stream) {
+  int st = check_run(plan, PKV_MODE_DECODE, q, cache, o);
+  if (st != PKV_OK) return st;
+  size_t need = 0;
+  st = pkv_attn_scored_scratch_size(plan, &need);
+  if (st != PKV_OK) return st;
+  if (plan->num_decode_work == 0) return PKV_OK;
+  if (!scores || (uintptr_t)scores & 3) return fail(PKV_EINVAL, "scores must be non-NULL and 4-byte aligned");
+  if ((uintptr_t)scratch & 255) return fail(PKV_EINVAL, "scratch must be 256-byte aligned");
+  if (!scratch || scratch_bytes < need)
+    return fail(PKV_EWORKSPACE, "scratch has " + std::to_string(scratch ? scratch_bytes : 0) + " bytes, the scored run needs " +
+                                    std::to_string(need));
+  pkv::RunParams p = make_params(plan, q, cache, o, lse, 0, plan->num_decode_work);
+  p.logits = (float*)scratch;
+  p.lse2 = (float*)((char*)scratch + pkv::scored_lse_offset(plan));
+  p.scores = scores;
+  PKV_CUDA(pkv::launch_decode_scored(p, cache->dtype, (cudaStream_t)stream), "scored decode launch");
+  return PKV_OK;
+}
+
+int pkv_kv_evict(const pkv_plan* plan, const pkv_cache* cache, float* scores, int32_t budget, int32_t num_sink,
+                 int32_t num_recent, int32_t* kept, void* stream) {
+  if (!plan || !plan->valid) return fail(PKV_EINVAL, "plan is NULL or has not been planned");
+  if (!plan->ws) return fail(PKV_EINVAL, "the plan is host-only (planned without a workspace)");
+  if (plan->mode != PKV_MODE_DECODE && plan->mode != PKV_MODE_PREFILL && plan->mode != PKV_MODE_MIXED)
+    return fail(PKV_EINVAL, "evict needs a PKV_MODE_DECODE, PKV_MODE_PREFILL or PKV_MODE_MIXED plan");
+  if (plan->window_left >= 0)
+    return fail(PKV_EINVAL, "evict changes the keys' order, which a sliding window depends on");
+  int st = pkv::check_cache(plan, cache);
+  if (st != PKV_OK) return st;
+  if (budget < 1 || num_sink < 0 || num_recent < 0 || (int64_t)num_sink + num_recent > budget)
+    return fail(PKV_EINVAL, "evict needs budget >= 1, num_sink >= 0, num_recent >= 0 and num_sink + num_recent <= budget");
+  if (budget > pkv::kEvictMaxLen)
+    return fail(PKV_EUNSUPPORTED, "evict covers budgets of up to " + std::to_string(pkv::kEvictMaxLen) + " keys");
+  st = check_pages_unique(plan);
+  if (st != PKV_OK) return st;
+  int dev = -1;
+  PKV_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
+  if (dev != plan->device) return fail(PKV_EINVAL, "the current device is not the device the plan was made on");
+  if (plan->batch == 0) return PKV_OK;
+  if (!scores || !kept || ((uintptr_t)scores | (uintptr_t)kept) & 3)
+    return fail(PKV_EINVAL, "scores and kept must be non-NULL and 4-byte aligned");
+  int32_t max_len = 0;
+  for (const ReqInfo& r : plan->req) max_len = std::max(max_len, r.kv_len);
+  if (max_len > pkv::kEvictMaxLen)
+    return fail(PKV_EUNSUPPORTED, "evict covers requests of up to " + std::to_string(pkv::kEvictMaxLen) + " keys");
+  int32_t sms = 0;
+  st = query_num_sms(0, &sms);
+  if (st != PKV_OK) return st;
+  pkv::RunParams rp{};
+  pkv::set_cache_params(rp, plan, cache);
+  pkv::EvictParams p{};
+  p.req = (const ReqInfo*)((char*)plan->ws + plan->off_req);
+  p.kv_indices = (const int32_t*)((char*)plan->ws + plan->off_idx);
+  p.k_pool = (char*)cache->k;
+  p.v_pool = (char*)cache->v;
+  p.k_sf = const_cast<char*>(rp.k_sf);
+  p.v_sf = const_cast<char*>(rp.v_sf);
+  p.stride_page_b = rp.stride_page_b;
+  p.stride_token_b = rp.stride_token_b;
+  p.stride_head_b = rp.stride_head_b;
+  p.sf_page_b = rp.sf_page_b;
+  p.sf_token_b = rp.sf_token_b;
+  p.sf_head_b = rp.sf_head_b;
+  p.num_pages = cache->num_pages;
+  p.scores = scores;
+  p.kept = kept;
+  p.page_size = plan->ps;
+  p.num_kv_heads = plan->Hkv;
+  p.row_chunks = (int32_t)(plan->D * pkv::pool_elem_bytes(cache->dtype) / (cache->dtype == PKV_NVFP4 ? 32 : 16));
+  p.budget = budget;
+  p.num_sink = num_sink;
+  p.num_recent = num_recent;
+  PKV_CUDA(pkv::launch_evict(p, plan->batch, max_len, sms, (cudaStream_t)stream), "evict launch");
   return PKV_OK;
 }
 

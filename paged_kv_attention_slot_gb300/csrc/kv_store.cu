@@ -8,7 +8,12 @@
 //
 // One thread moves one 16-byte chunk of one (token, head) row: for D = 128 bf16 a row is 16
 // chunks, so a warp writes two full rows and every global access is a full 16-byte vector.  The
-// kernel is a pure memory op; it is launched with enough CTAs to cover every chunk once.
+// kernel is a pure memory op; it is launched with enough CTAs to cover every chunk once.  An NVFP4 pool
+// takes one thread per 16-element block instead (two chunks in, one scale and 8 code bytes out).
+// kv_load is the way back: one thread per 8 (bf16, FP8) or 16 (NVFP4) elements of a row, widened and
+// rounded to bf16.
+
+#include <algorithm>
 
 #include "pkv_internal.h"
 #include "ptx.cuh"
@@ -58,6 +63,7 @@ struct StoreParams {
   int32_t heads;
   int32_t chunks;  // 16-byte source chunks per (token, head) row
   float inv_k, inv_v;
+  float* scores;  // nullable: [num_pages, heads, page_size] accumulated weights, zeroed at the written slots
   int32_t* err;
 };
 
@@ -79,6 +85,7 @@ __global__ void __launch_bounds__(256) kv_store_kernel(const StoreParams p) {
     }
     const int64_t page = slot / p.page_size;
     const int64_t off = slot - page * p.page_size;
+    if (p.scores && c == 0) p.scores[(page * p.heads + h) * p.page_size + off] = 0.f;
     const int64_t src = row * (int64_t)p.chunks * 16 + c * 16;
     const uint4 kx = __ldg(reinterpret_cast<const uint4*>(p.k + src));
     const uint4 vx = __ldg(reinterpret_cast<const uint4*>(p.v + src));
@@ -106,10 +113,225 @@ __global__ void __launch_bounds__(256) kv_store_kernel(const StoreParams p) {
   }
 }
 
+// ---- NVFP4: codes and block scales ----
+struct Fp4Pools {
+  uint8_t* k_sf;
+  uint8_t* v_sf;
+  int64_t sp_b, st_b, sh_b;  // strides of the scale pools in bytes
+};
+
+// Quotient t / s rounded to nearest (r = 1/s rounded): one Newton step on the quotient (Markstein's
+// correction).  |t| <= 2688 * 2^7 and s is an E4M3 value (2^-9 .. 448), so nothing over- or underflows
+// where the code is not 0 anyway.
+__device__ __forceinline__ float div_rn(float t, float s, float r) {
+  const float q = t * r;
+  return fmaf(fmaf(-q, s, t), r, q);
+}
+
+// One block of 16 bf16 values (two 16-byte vectors) to its E4M3 scale code and 8 bytes of E2M1 codes.
+__device__ __forceinline__ uint2 quant_block(const uint4 a, const uint4 b, float inv, uint32_t& sf) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  float t[16];
+  float amax = 0.f;
+  bool nan = false;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    t[2 * j] = __uint_as_float(w[j] << 16) * inv;
+    t[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u) * inv;
+    amax = fmaxf(amax, fmaxf(fabsf(t[2 * j]), fabsf(t[2 * j + 1])));
+    nan = nan || t[2 * j] != t[2 * j] || t[2 * j + 1] != t[2 * j + 1];
+  }
+  sf = nan ? 0x7fu : f32x2_to_e4m3x2(__fdiv_rn(amax, 6.f), 0.f) & 0xffu;
+  if (nan || sf == 0) return make_uint2(0u, 0u);
+  const float s = e4m3_to_f32(sf);
+  const float r = __fdiv_rn(1.f, s);
+  uint32_t c[2] = {0u, 0u};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    // beyond 2688 = 6 * 448 the scale is 448 and the code 6 for every value, infinities included
+    const float lo = div_rn(fminf(fmaxf(t[2 * j], -2688.f), 2688.f), s, r);
+    const float hi = div_rn(fminf(fmaxf(t[2 * j + 1], -2688.f), 2688.f), s, r);
+    c[j >> 2] |= f32x2_to_e2m1x2(lo, hi) << (8 * (j & 3));
+  }
+  return make_uint2(c[0], c[1]);
+}
+
+// One thread per (token, head, block of 16): the 8 threads of a row write its 64 code bytes and, packed
+// four to a word by shuffles, its 8 scale bytes.
+__global__ void __launch_bounds__(256) kv_store_fp4_kernel(const StoreParams p, const Fp4Pools f) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t n = p.T * p.heads * 8;  // a multiple of 8: the threads of a row stay together
+  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
+    const unsigned row_mask = 0xffu << (threadIdx.x & 24);
+    const int64_t row = i >> 3;
+    const int c = (int)(i & 7);
+    const int64_t tok = row / p.heads;
+    const int h = (int)(row - tok * p.heads);
+    const int64_t slot = __ldg(p.slots + tok);
+    if (slot < 0) continue;  // padding token (all 8 threads of the row)
+    if (slot >= p.total_slots) {
+      record_error(p.err, PKV_DEVERR_SLOT_RANGE);
+      continue;
+    }
+    const int64_t page = slot / p.page_size;
+    const int64_t off = slot - page * p.page_size;
+    if (p.scores && c == 0) p.scores[(page * p.heads + h) * p.page_size + off] = 0.f;
+    const uint4* ks = reinterpret_cast<const uint4*>(p.k + row * 256 + c * 32);
+    const uint4* vs = reinterpret_cast<const uint4*>(p.v + row * 256 + c * 32);
+    const uint4 k0 = __ldg(ks), k1 = __ldg(ks + 1), v0 = __ldg(vs), v1 = __ldg(vs + 1);
+    uint32_t fk, fv;
+    const uint2 ck = quant_block(k0, k1, p.inv_k, fk);
+    const uint2 cv = quant_block(v0, v1, p.inv_v, fv);
+    const int64_t dst = page * p.sp_b + off * p.st_b + h * p.sh_b + c * 8;
+    *reinterpret_cast<uint2*>(p.k_pool + dst) = ck;
+    *reinterpret_cast<uint2*>(p.v_pool + dst) = cv;
+    fk <<= 8 * (c & 3);
+    fv <<= 8 * (c & 3);
+#pragma unroll
+    for (int sh = 1; sh < 4; sh <<= 1) {
+      fk |= __shfl_xor_sync(row_mask, fk, sh);
+      fv |= __shfl_xor_sync(row_mask, fv, sh);
+    }
+    if ((c & 3) == 0) {
+      const int64_t sd = page * f.sp_b + off * f.st_b + h * f.sh_b + c;
+      *reinterpret_cast<uint32_t*>(f.k_sf + sd) = fk;
+      *reinterpret_cast<uint32_t*>(f.v_sf + sd) = fv;
+    }
+  }
+}
+
+// ---- the read back ----
+struct LoadParams {
+  const int64_t* slots;
+  const uint8_t* k_pool;
+  const uint8_t* v_pool;
+  const uint8_t* k_sf;
+  const uint8_t* v_sf;
+  uint4* k;
+  uint4* v;
+  int64_t T, total_slots;
+  int64_t sp_b, st_b, sh_b, fp_b, ft_b, fh_b;
+  int32_t page_size, heads, units;  // units: threads per (token, head) row
+  float k_scale, v_scale;
+  int32_t* err;
+};
+
+template <int KV>
+__device__ __forceinline__ void load_unit(const uint8_t* pool, const uint8_t* sf, int64_t at, int64_t sat, int c, float scale,
+                                          uint4* out) {
+  if constexpr (KV == PKV_BF16) {
+    out[0] = __ldg(reinterpret_cast<const uint4*>(pool + at + c * 16));
+  } else {
+    // 8 code bytes: 8 E4M3 values, or 16 E2M1 values under one block scale
+    const uint2 x = __ldg(reinterpret_cast<const uint2*>(pool + at + c * 8));
+    uint32_t h[8];
+    float f = scale;
+    if constexpr (KV == PKV_NVFP4) {
+      // code * block scale has 6 significant bits; the tensor's scale is the first rounding, bf16 the last
+      const float s = e4m3_to_f32(__ldg(sf + sat + c));
+      uint32_t a[4], b[4];
+      e2m1x8_to_f16x2x4(x.x, a);
+      e2m1x8_to_f16x2x4(x.y, b);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        h[j] = a[j];
+        h[4 + j] = b[j];
+      }
+      uint32_t r[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float2 y = f16x2_to_f32x2(h[j]);
+        r[j] = pack_bf16(y.x * s * f, y.y * s * f);
+      }
+      out[0] = make_uint4(r[0], r[1], r[2], r[3]);
+      out[1] = make_uint4(r[4], r[5], r[6], r[7]);
+    } else {
+      e4m3x4_to_f16x2x2(x.x, h[0], h[1]);
+      e4m3x4_to_f16x2x2(x.y, h[2], h[3]);
+      uint32_t r[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 y = f16x2_to_f32x2(h[j]);
+        r[j] = pack_bf16(y.x * f, y.y * f);
+      }
+      out[0] = make_uint4(r[0], r[1], r[2], r[3]);
+    }
+  }
+}
+
+template <int KV>
+__global__ void __launch_bounds__(256) kv_load_kernel(const LoadParams p) {
+  constexpr int OUT = KV == PKV_NVFP4 ? 2 : 1;  // 16-byte vectors written per thread and tensor
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t n = p.T * p.heads * p.units;
+  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t row = i / p.units;
+    const int c = (int)(i - row * p.units);
+    const int64_t tok = row / p.heads;
+    const int h = (int)(row - tok * p.heads);
+    const int64_t slot = __ldg(p.slots + tok);
+    uint4 ko[2], vo[2];
+    ko[0] = ko[1] = vo[0] = vo[1] = make_uint4(0u, 0u, 0u, 0u);
+    if (slot >= p.total_slots) {
+      record_error(p.err, PKV_DEVERR_SLOT_RANGE);
+    } else if (slot >= 0) {
+      const int64_t page = slot / p.page_size;
+      const int64_t off = slot - page * p.page_size;
+      const int64_t at = page * p.sp_b + off * p.st_b + h * p.sh_b;
+      const int64_t sat = page * p.fp_b + off * p.ft_b + h * p.fh_b;
+      load_unit<KV>(p.k_pool, p.k_sf, at, sat, c, p.k_scale, ko);
+      load_unit<KV>(p.v_pool, p.v_sf, at, sat, c, p.v_scale, vo);
+    }
+#pragma unroll
+    for (int j = 0; j < OUT; ++j) {
+      p.k[i * OUT + j] = ko[j];
+      p.v[i * OUT + j] = vo[j];
+    }
+  }
+}
+
+cudaError_t launch_kv_load(const int64_t* slots, int64_t T, const pkv_cache& c, void* k, void* v, cudaStream_t s) {
+  const bool fp4 = c.dtype == PKV_NVFP4;
+  const int64_t esz = pool_elem_bytes(c.dtype);
+  LoadParams p{};
+  p.slots = slots;
+  p.k_pool = static_cast<const uint8_t*>(c.k);
+  p.v_pool = static_cast<const uint8_t*>(c.v);
+  p.k = static_cast<uint4*>(k);
+  p.v = static_cast<uint4*>(v);
+  p.T = T;
+  p.total_slots = c.num_pages * (int64_t)c.page_size;
+  p.sp_b = c.stride_page * esz;
+  p.st_b = c.stride_token * esz;
+  p.sh_b = c.stride_head * esz;
+  if (fp4) {
+    p.k_sf = static_cast<const uint8_t*>(c.k_sf);
+    p.v_sf = static_cast<const uint8_t*>(c.v_sf);
+    p.fp_b = c.sf_stride_page;
+    p.ft_b = c.sf_stride_token;
+    p.fh_b = c.sf_stride_head;
+  }
+  p.page_size = c.page_size;
+  p.heads = c.num_kv_heads;
+  p.units = fp4 ? c.head_dim / 16 : c.head_dim / 8;
+  p.k_scale = c.k_scale;
+  p.v_scale = c.v_scale;
+  p.err = device_error_ptr();
+  if (!p.err) return cudaErrorInvalidDevice;
+  const int64_t blocks = std::min<int64_t>((T * p.heads * p.units + 255) / 256, 152 * 16);
+  const dim3 g((unsigned)blocks), b(256);
+  if (fp4) return launch_pdl(kv_load_kernel<PKV_NVFP4>, g, b, 0, s, p);
+  if (c.dtype == PKV_FP8_E4M3) return launch_pdl(kv_load_kernel<PKV_FP8_E4M3>, g, b, 0, s, p);
+  return launch_pdl(kv_load_kernel<PKV_BF16>, g, b, 0, s, p);
+}
+
 cudaError_t launch_kv_store(const void* k, const void* v, const int64_t* slots, int64_t T, const pkv_cache& c,
-                            float inv_k, float inv_v, cudaStream_t s) {
+                            float inv_k, float inv_v, float* scores, cudaStream_t s) {
+  const bool fp4 = c.dtype == PKV_NVFP4;
   const bool fp8 = c.dtype == PKV_FP8_E4M3;
-  const int64_t esz = fp8 ? 1 : 2;
+  const int64_t esz = pool_elem_bytes(c.dtype);
   StoreParams p;
   p.k = static_cast<const uint8_t*>(k);
   p.v = static_cast<const uint8_t*>(v);
@@ -123,7 +345,8 @@ cudaError_t launch_kv_store(const void* k, const void* v, const int64_t* slots, 
   p.sh_b = c.stride_head * esz;
   p.page_size = c.page_size;
   p.heads = c.num_kv_heads;
-  p.chunks = c.head_dim * 2 / 16;
+  p.chunks = fp4 ? c.head_dim / 16 : c.head_dim * 2 / 16;
+  p.scores = scores;
   p.inv_k = inv_k;
   p.inv_v = inv_v;
   p.err = device_error_ptr();
@@ -131,6 +354,11 @@ cudaError_t launch_kv_store(const void* k, const void* v, const int64_t* slots, 
   const int64_t n = T * p.heads * p.chunks;
   int64_t blocks = (n + 255) / 256;
   if (blocks > 152 * 16) blocks = 152 * 16;
+  if (fp4) {
+    const Fp4Pools f{static_cast<uint8_t*>(c.k_sf), static_cast<uint8_t*>(c.v_sf), c.sf_stride_page, c.sf_stride_token,
+                     c.sf_stride_head};
+    return launch_pdl(kv_store_fp4_kernel, dim3((unsigned)blocks), dim3(256), 0, s, p, f);
+  }
   return fp8 ? launch_pdl(kv_store_kernel<true>, dim3((unsigned)blocks), dim3(256), 0, s, p)
              : launch_pdl(kv_store_kernel<false>, dim3((unsigned)blocks), dim3(256), 0, s, p);
 }

@@ -76,7 +76,6 @@ extern "C" int pkv_attn_decode_run_noalloc(const pkv_plan* plan, const void* q, 
   // alignment, positive strides, FP8 scales)
   const int st = check_cache(plan, cache);
   if (st != PKV_OK) return st;
-  const int64_t esz = cache->dtype == PKV_FP8_E4M3 ? 1 : 2;
   if (plan->total_tokens > 0 && (!q || !o)) return noalloc_fail(PKV_EINVAL, "q and o must be non-NULL");
   if (((uintptr_t)q | (uintptr_t)o) & 15) return noalloc_fail(PKV_EINVAL, "q and o must be 16-byte aligned");
   if (plan->work.empty()) return PKV_OK;
@@ -116,20 +115,12 @@ extern "C" int pkv_attn_decode_run_noalloc(const pkv_plan* plan, const void* q, 
   p.q = q;
   p.o = o;
   p.lse = lse;
-  p.k_pool = static_cast<const char*>(cache->k);
-  p.v_pool = static_cast<const char*>(cache->v);
-  p.stride_page_b = cache->stride_page * esz;
-  p.stride_token_b = cache->stride_token * esz;
-  p.stride_head_b = cache->stride_head * esz;
-  p.num_pages = cache->num_pages;
-  p.page_size = plan->ps;
+  set_cache_params(p, plan, cache);
   p.num_qo_heads = plan->Hq;
   p.num_kv_heads = plan->Hkv;
   p.group = plan->Hq / plan->Hkv;
   p.head_dim = plan->D;
   p.window_left = plan->window_left;
-  p.scale_log2 = plan->sm_scale * 1.4426950408889634f * (cache->dtype == PKV_FP8_E4M3 ? cache->k_scale : 1.0f);
-  p.out_scale = cache->dtype == PKV_FP8_E4M3 ? cache->v_scale : 1.0f;
   p.num_work = (int64_t)plan->work.size();
   p.num_merge = (int64_t)plan->merge.size();
   e = launch_decode(p, cache->dtype, s);

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <vector>
 
 #include "pkv_attn.h"
@@ -82,6 +83,12 @@ struct RunParams {
   int64_t stride_page_b;   // bytes
   int64_t stride_token_b;  // bytes
   int64_t stride_head_b;   // bytes
+  const char* k_sf;        // NVFP4: block scales
+  const char* v_sf;
+  int64_t sf_page_b, sf_token_b, sf_head_b;  // bytes
+  float* logits;  // scored decode: scaled scores (log2 units) of the visible keys, see scored_lse_offset()
+  float* lse2;    // scored decode: [total_tokens, num_qo_heads] log2-sum-exp
+  float* scores;  // scored decode: [num_pages, num_kv_heads, page_size] accumulated weights
   int64_t num_pages;
   int32_t page_size;
   int32_t num_qo_heads;
@@ -105,9 +112,33 @@ struct RunParams {
 };
 
 // launchers (return cudaError_t of the launch)
+// scores: nullable, set to 0 at the written slots
 cudaError_t launch_kv_store(const void* k, const void* v, const int64_t* slots, int64_t T, const pkv_cache& c,
-                            float inv_k, float inv_v, cudaStream_t s);
+                            float inv_k, float inv_v, float* scores, cudaStream_t s);
+cudaError_t launch_kv_load(const int64_t* slots, int64_t T, const pkv_cache& c, void* k, void* v, cudaStream_t s);
+
+// Eviction of the plan's requests longer than `budget` (pkv_kv_evict), kernel parameters.
+struct EvictParams {
+  const ReqInfo* req;
+  const int32_t* kv_indices;
+  char* k_pool;
+  char* v_pool;
+  char* k_sf;  // null unless NVFP4
+  char* v_sf;
+  int64_t stride_page_b, stride_token_b, stride_head_b;
+  int64_t sf_page_b, sf_token_b, sf_head_b;
+  int64_t num_pages;
+  float* scores;
+  int32_t* kept;
+  int32_t page_size;
+  int32_t num_kv_heads;
+  int32_t row_chunks;  // 16-byte chunks of one K (or V) row
+  int32_t budget, num_sink, num_recent;
+};
+cudaError_t launch_evict(const EvictParams& p, int32_t batch, int32_t max_len, int num_sms, cudaStream_t s);
+constexpr int32_t kEvictMaxLen = 1 << 21;  // longest request the eviction kernel's shared memory covers
 cudaError_t launch_decode(const RunParams& p, int kv_dtype, cudaStream_t s);
+cudaError_t launch_decode_scored(const RunParams& p, int kv_dtype, cudaStream_t s);  // decode and the score update
 int decode_ctas_per_sm(int kv_dtype, int head_dim, int group);  // resident decode CTAs per SM
 cudaError_t launch_prefill(const RunParams& p, const void* tmap_q, const void* tmap_o, int64_t total_tokens,
                            cudaStream_t s);
@@ -119,6 +150,11 @@ cudaError_t launch_merge_state(const void* o_a, const float* lse_a, const void* 
                                float* lse, int64_t num_states, int head_dim, cudaStream_t s);
 
 cudaError_t read_device_error(int32_t* code, int reset, cudaStream_t s);
+
+// bytes per element of a pool's k / v (an NVFP4 element is one byte of two codes)
+inline int64_t pool_elem_bytes(int dtype) { return dtype == PKV_BF16 ? 2 : 1; }
+// The pool's part of the run parameters: pointers, byte strides, scales (sm_scale from the plan).
+void set_cache_params(RunParams& p, const pkv_plan* P, const pkv_cache* c);
 
 // record `msg` as this thread's pkv_last_error() text and return `code`
 int set_last_error(int code, const char* msg);
@@ -156,6 +192,15 @@ struct pkv_plan {
   size_t pinned_bytes = 0;
   cudaEvent_t copy_done = nullptr;
   bool copy_pending = false;
+  mutable std::atomic<int> pages_unique{-1};  // no page listed twice: 1, else 0; -1 = not looked at yet
   int device = -1;
 };
 
+namespace pkv {
+// Scratch of a scored run: the scaled scores, one float per (slot of the plan's pages, query head) --
+// request i's in the region that starts at page_base_i * page_size * num_qo_heads -- then lse2.
+inline size_t scored_lse_offset(const pkv_plan* P) {
+  const size_t n = P->indices.size() * (size_t)P->ps * (size_t)P->Hq * sizeof(float);
+  return (n + 255) / 256 * 256;
+}
+}  // namespace pkv

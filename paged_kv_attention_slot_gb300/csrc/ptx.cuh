@@ -1,6 +1,7 @@
 // Thin inline-PTX wrappers used by the kernels of this library (sm_103a).
 #pragma once
 
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -114,6 +115,46 @@ __device__ __forceinline__ void e4m3x4_to_f16x2x2(uint32_t four_codes, uint32_t&
       : "=r"(lo), "=r"(hi)
       : "r"(four_codes));
 }
+// ---- E2M1 (4-bit) codes ----
+// eight codes (nibble i = element i) to four f16x2, element 2i in the low half of out[i]; exact
+__device__ __forceinline__ void e2m1x8_to_f16x2x4(uint32_t x, uint32_t (&out)[4]) {
+  asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}\n"
+      : "=r"(out[0]), "=r"(out[1]), "=r"(out[2]), "=r"(out[3])
+      : "r"(x));
+}
+// two rows of four codes (row 0 in the low half-word) to four f16x2: out[i] = (row 0, row 1) of element i
+__device__ __forceinline__ void e2m1_2x4_to_f16x2x4(uint32_t x, uint32_t (&out)[4]) {
+  // pair the rows' nibbles into bytes first: {e0, e2} in one 16-bit word, {e1, e3} in another
+  const uint32_t even = (x & 0x0f0fu) | ((x >> 12) & 0xf0f0u);
+  const uint32_t odd = ((x >> 4) & 0x0f0fu) | ((x >> 16) & 0xf0f0u);
+  asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %2;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n}\n"
+      : "=r"(out[0]), "=r"(out[2])
+      : "r"(even));
+  asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %2;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n}\n"
+      : "=r"(out[1]), "=r"(out[3])
+      : "r"(odd));
+}
+// two floats to two E2M1 codes, round to nearest even, saturate to +-6; lo -> low nibble
+__device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
+  uint32_t r;
+  asm("{\n .reg .b8 t;\n cvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n cvt.u32.u8 %0, t;\n}\n"
+      : "=r"(r)
+      : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// one half of an f16x2 in both halves
+__device__ __forceinline__ uint32_t dup_lo(uint32_t x) { return __byte_perm(x, 0, 0x1010u); }
+__device__ __forceinline__ uint32_t dup_hi(uint32_t x) { return __byte_perm(x, 0, 0x3232u); }
+
 // two floats to two E4M3 codes, round to nearest even, saturate to finite; lo -> low byte
 __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
   uint32_t r;
@@ -121,6 +162,15 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
       : "=r"(r)
       : "f"(lo), "f"(hi));
   return r;
+}
+
+// one E4M3 code to f32 (exact)
+__device__ __forceinline__ float e4m3_to_f32(uint32_t code) {
+  return __half2float(__ushort_as_half((unsigned short)(e4m3x2_to_f16x2(code & 0xffu) & 0xffffu)));
+}
+__device__ __forceinline__ float2 f16x2_to_f32x2(uint32_t x) {
+  return make_float2(__half2float(__ushort_as_half((unsigned short)(x & 0xffffu))),
+                     __half2float(__ushort_as_half((unsigned short)(x >> 16))));
 }
 
 // hardware base-2 exponential (MUFU); ex2(-inf) = +0
