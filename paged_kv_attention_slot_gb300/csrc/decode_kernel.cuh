@@ -67,27 +67,31 @@ __device__ __forceinline__ void cp_async16_pol(uint32_t dst, const void* src, ui
                : "memory");
 }
 
-// KV: the pool's pkv_dtype.
-template <int D, int KV, int NB>
+// KV: the pool's pkv_dtype; NB: 8-column n-blocks; HPB: query heads per n-block, 8 or, for NVFP4, 4 in
+// "pair" form (every head in two neighbouring columns, see the V product in the kernel).
+template <int D, int KV, int NB, int HPB = 8>
 struct DecodeCfg {
   static constexpr bool FP4 = KV == PKV_NVFP4;
   static constexpr int ROWB = FP4 ? D / 2 : KV == PKV_FP8_E4M3 ? D : 2 * D;  // bytes per key row of one head
   static constexpr int CH = ROWB / 16;          // 16-byte chunks per row
-  static constexpr int KEYS = 16;               // keys per warp tile
+  static constexpr int KEYS = FP4 ? 32 : 16;    // keys per warp tile
+  static constexpr int SUBS = KEYS / 16;        // 16-key MMA tiles in it
   static constexpr int TILE_B = KEYS * ROWB;    // bytes of one K (or V) tile
   static constexpr int SF_B = FP4 ? KEYS * D / 16 : 0;    // bytes of the block scales of one K (or V) tile
   static constexpr int STAGE_B = 2 * TILE_B + 2 * SF_B;  // K, V, K scales, V scales
-  static constexpr int HEADS = 8 * NB;          // query heads per CTA (n dimension)
-  static constexpr int STAGES = FP4 ? 4 : 3;
+  static constexpr int HEADS = HPB * NB;        // query heads per CTA (n dimension)
+  static constexpr bool PAIR = HPB == 4;
+  static constexpr int STAGES = 3;
   static constexpr int WARPS = 4;
   // resident CTAs per SM: the 8-KB-per-stage bf16/D128 variant fits 2 (shared memory), the 4-KB
   // variants fit 4 when the accumulators are for 8 heads (registers)
-  static constexpr int CTAS = (2 * TILE_B > 4096 || NB > 1) ? 2 : 4;
+  static constexpr int CTAS = (2 * TILE_B > 4096 || (NB > 1 && !PAIR)) ? 2 : 4;
   static constexpr int WARP_SMEM = STAGES * STAGE_B;
   static constexpr int PIPE_SMEM = WARPS * WARP_SMEM;
   static constexpr int MERGE_SMEM = (WARPS * HEADS * D + 3 * WARPS * HEADS) * 4;
   static constexpr int SMEM = PIPE_SMEM > MERGE_SMEM ? PIPE_SMEM : MERGE_SMEM;
-  static constexpr int MB = D / 16;  // 16-row m-blocks of O^T
+  static constexpr int MB = PAIR ? D / 32 : D / 16;  // 16-row m-blocks of O^T (rows: dims, or pairs of dims)
+  static_assert(!PAIR || FP4, "the pair form is for 4-bit codes");
   static constexpr int KS = D / 16;  // k-steps of S^T
   static_assert(CH >= 8 || CH == 4, "the XOR swizzles below are for rows of 4 or at least 8 chunks");
   static_assert(SMEM * CTAS <= 232448, "shared memory per SM");
@@ -154,10 +158,11 @@ __device__ __forceinline__ void merge_accumulate(float4 (&acc)[NA], const int (&
 
 // SCORED: every visible key's scaled score (log2 units) goes to p.logits, each row's log2-sum-exp to
 // p.lse2 (for the accumulated attention weights, score_add.cu).
-template <int D, int KV, int NB, bool SCORED>
-__global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB>::CTAS) decode_kernel(const RunParams p, int32_t* err) {
-  using C = DecodeCfg<D, KV, NB>;
+template <int D, int KV, int NB, int HPB, bool SCORED>
+__global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB, HPB>::CTAS) decode_kernel(const RunParams p, int32_t* err) {
+  using C = DecodeCfg<D, KV, NB, HPB>;
   constexpr bool FP4 = KV == PKV_NVFP4;
+  constexpr bool PAIR = C::PAIR;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_stage_key[C::WARPS][C::STAGES];
 
@@ -174,7 +179,7 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB>::CTAS) decode_kernel
   uint32_t qb[C::KS][NB][2];
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
-    const int head = nb * 8 + g;
+    const int head = PAIR ? nb * 4 + (g >> 1) : nb * 8 + g;
     const bool valid = head < rows;
     const uint16_t* qr = static_cast<const uint16_t*>(p.q) + ((int64_t)w.q_row * p.num_qo_heads + qh0 + head) * D;
 #pragma unroll
@@ -196,12 +201,12 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB>::CTAS) decode_kernel
   // ---- per-warp cp.async ring ----
   uint8_t* wsm = smem + warp * C::WARP_SMEM;
   const uint32_t wsm_u = smem_u32(wsm);
-  const int lr = lane & 15;  // row whose page this lane resolves
+  const int lr = lane & (C::KEYS - 1);  // row whose page this lane resolves
   const int64_t head_off = (int64_t)w.kv_head * p.stride_head_b;
   const int64_t sf_head = FP4 ? (int64_t)w.kv_head * p.sf_head_b : 0;
   const uint64_t kv_policy = l2_evict_first();
 
-  // Lane lr (0..15) resolves the page of row lr of a tile; then every warp-wide cp.async covers
+  // Lane lr (0..15, NVFP4: 0..31) resolves the page of row lr of a tile; then every warp-wide cp.async covers
   // 32 / CH whole rows with consecutive lanes on consecutive 16-byte chunks (fully coalesced).
   constexpr int RPI = 32 / C::CH;  // rows per warp instruction
   const int lc = lane % C::CH;
@@ -209,6 +214,7 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB>::CTAS) decode_kernel
   const int ps = p.page_size;
   const int ps_shift = (ps & (ps - 1)) == 0 ? __ffs(ps) - 1 : -1;  // page sizes are usually powers of 2
   auto page_of = [&](int key) -> int { return ps_shift >= 0 ? key >> ps_shift : key / ps; };
+  const bool halves_paged = FP4 && (ps & 15) == 0 && (w.kv_begin & 15) == 0;  // tiles start on multiples of 16 then
   const int64_t row_step = (int64_t)RPI * p.stride_token_b;  // bytes between the rows of consecutive instructions
 
   // ---- the warp's tile sequence ----
@@ -218,7 +224,7 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB>::CTAS) decode_kernel
   // the warps of all the CTAs end within about one group of each other).  The claim for the next
   // group is sent when the warp starts loading a group, 2 tiles before it is needed.  A key >=
   // kv_end ends the sequence.
-  constexpr int GROUP_KEYS = 2 * C::KEYS;
+  constexpr int GROUP_KEYS = 2 * C::KEYS;  // (NVFP4: 64-key groups of two 32-key tiles)
   const bool shared_range = w.num_splits > 1;
   const int claim_base = w.num_splits * C::WARPS;
   int pending = 0;  // lane 0: value returned by the outstanding claim
@@ -252,6 +258,31 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB>::CTAS) decode_kernel
     nkey = nkey < w.kv_end ? next_key(nkey) : w.kv_end;
     const uint32_t dk = wsm_u + stage * C::STAGE_B;
     const uint32_t dv = dk + C::TILE_B;
+    if constexpr (FP4) {
+      // Common case: all 32 keys present and each half of them on one page (whole 16-key halves per page:
+      // halves_paged), so the row addresses follow from two pages and a stride.
+      const bool in_pool = (unsigned long long)(unsigned)page < (unsigned long long)p.num_pages;
+      if (halves_paged && key0 + C::KEYS <= w.kv_end && __all_sync(0xffffffffu, in_pool)) {
+        const int off = key0 + lr - page_of(key0 + lr) * ps;  // of this lane's row
+        const int64_t srow = (int64_t)page * p.sf_page_b + (int64_t)off * p.sf_token_b + sf_head;
+        cp_async8(dv + C::TILE_B + lane * 8, p.k_sf + srow, 8u);
+        cp_async8(dv + C::TILE_B + C::SF_B + lane * 8, p.v_sf + srow, 8u);
+        const int64_t crow = (int64_t)page * p.stride_page_b + (int64_t)off * p.stride_token_b + head_off;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const int64_t base = __shfl_sync(0xffffffffu, crow, 16 * hf) + (int64_t)lsub * p.stride_token_b + lc * 16;
+          const char* ks = p.k_pool + base;
+          const char* vs = p.v_pool + base;
+#pragma unroll
+          for (int j = 0; j < 16 / RPI; ++j) {
+            const uint32_t sw = C::at(16 * hf + j * RPI + lsub, lc);
+            cp_async16_pol(dk + sw, ks + j * row_step, 16u, kv_policy);
+            cp_async16_pol(dv + sw, vs + j * row_step, 16u, kv_policy);
+          }
+        }
+        return;
+      }
+    } else {
     // Common case: all 16 keys present and on one page (page size >= 16, chunk starts aligned), so
     // every lane has the same page id and the row addresses follow from one base and a stride.
     const bool one_page = key0 + C::KEYS <= w.kv_end && page_of(key0) == page_of(key0 + C::KEYS - 1) &&
@@ -261,10 +292,6 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB>::CTAS) decode_kernel
       const int64_t base = (int64_t)page * p.stride_page_b + (int64_t)(off0 + lsub) * p.stride_token_b + head_off + lc * 16;
       const char* ks = p.k_pool + base;
       const char* vs = p.v_pool + base;
-      if constexpr (FP4)  // lanes 0-15: the block scales of K row lr, lanes 16-31: of V row lr
-        cp_async8(dv + C::TILE_B + lane * 8,
-                  (lane < 16 ? p.k_sf : p.v_sf) + (int64_t)page * p.sf_page_b + (int64_t)(off0 + lr) * p.sf_token_b + sf_head,
-                  8u);
 #pragma unroll
       for (int j = 0; j < C::KEYS / RPI; ++j) {
         const int row = j * RPI + lsub;
@@ -273,6 +300,7 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB>::CTAS) decode_kernel
         cp_async16_pol(dv + sw, vs + j * row_step, 16u, kv_policy);
       }
       return;
+    }
     }
     int64_t roff = -1, soff = -1;
     if (key < w.kv_end) {
@@ -285,8 +313,8 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB>::CTAS) decode_kernel
         if (roff >= 0) soff = (int64_t)page * p.sf_page_b + (int64_t)off * p.sf_token_b + sf_head;
     }
     if constexpr (FP4) {
-      const char* sp = lane < 16 ? p.k_sf : p.v_sf;
-      cp_async8(dv + C::TILE_B + lane * 8, soff >= 0 ? sp + soff : sp, soff >= 0 ? 8u : 0u);
+      cp_async8(dv + C::TILE_B + lane * 8, soff >= 0 ? p.k_sf + soff : p.k_sf, soff >= 0 ? 8u : 0u);
+      cp_async8(dv + C::TILE_B + C::SF_B + lane * 8, soff >= 0 ? p.v_sf + soff : p.v_sf, soff >= 0 ? 8u : 0u);
     }
 #pragma unroll
     for (int j = 0; j < C::KEYS / RPI; ++j) {
@@ -377,10 +405,12 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB>::CTAS) decode_kernel
     const uint8_t* sfs = wsm + stage * C::STAGE_B + 2 * C::TILE_B;  // block scales of the K rows, then the V rows
     stage = stage + 1 == C::STAGES ? 0 : stage + 1;
 
-    // ---- S^T = K Q^T for 16 keys ----
-    float s[NB][4];
+    // ---- S^T = K Q^T for 16 keys (NVFP4: twice 16) ----
+    float s[C::SUBS][NB][4];
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.f;
+    for (int su = 0; su < C::SUBS; ++su)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) s[su][nb][0] = s[su][nb][1] = s[su][nb][2] = s[su][nb][3] = 0.f;
     if constexpr (KV == PKV_BF16) {
 #pragma unroll
       for (int ks = 0; ks < C::KS; ++ks) {
@@ -388,36 +418,37 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB>::CTAS) decode_kernel
         const int chunk = 2 * ks + (mi >> 1);
         ldsm_x4(a, kb + C::at(k_key, chunk));
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) mma_bf16(s[nb], a, qb[ks][nb][0], qb[ks][nb][1]);
+        for (int nb = 0; nb < NB; ++nb) mma_bf16(s[0][nb], a, qb[ks][nb][0], qb[ks][nb][1]);
       }
     } else if constexpr (FP4) {
       // This lane's codes of chunk c (8t .. 8t+7 of its 32) lie in block 2c + (t >> 1): one scale per
       // (key row, chunk), here for key rows g and g + 8
       const uint32_t sel = t < 2 ? 0x6420u : 0x7531u;
-      const uint2 f0 = *reinterpret_cast<const uint2*>(sfs + g * 8);
-      const uint2 f1 = *reinterpret_cast<const uint2*>(sfs + (g + 8) * 8);
-      uint32_t sg[2][2];  // [key row][chunk pair], f16x2
-      e4m3x4_to_f16x2x2(__byte_perm(f0.x, f0.y, sel), sg[0][0], sg[0][1]);
-      e4m3x4_to_f16x2x2(__byte_perm(f1.x, f1.y, sel), sg[1][0], sg[1][1]);
 #pragma unroll
-      for (int c = 0; c < C::CH; c += 2) {
-        uint32_t r[4];
-        const int chunk = c + (mi >> 1);
-        ldsm_x4(r, kb + C::at(k_key, chunk));
+      for (int su = 0; su < C::SUBS; ++su) {
+        const uint2 f0 = *reinterpret_cast<const uint2*>(sfs + (16 * su + g) * 8);
+        const uint2 f1 = *reinterpret_cast<const uint2*>(sfs + (16 * su + g + 8) * 8);
+        uint32_t sg[2][2];  // [key row][chunk pair], f16x2
+        e4m3x4_to_f16x2x2(__byte_perm(f0.x, f0.y, sel), sg[0][0], sg[0][1]);
+        e4m3x4_to_f16x2x2(__byte_perm(f1.x, f1.y, sel), sg[1][0], sg[1][1]);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {  // r[2h]: key g, chunk c + h; r[2h + 1]: key g + 8
-          const uint32_t s0 = h ? dup_hi(sg[0][c >> 1]) : dup_lo(sg[0][c >> 1]);
-          const uint32_t s1 = h ? dup_hi(sg[1][c >> 1]) : dup_lo(sg[1][c >> 1]);
-          uint32_t x[4], y[4];
-          e2m1x8_to_f16x2x4(r[2 * h], x);
-          e2m1x8_to_f16x2x4(r[2 * h + 1], y);
+        for (int c = 0; c < C::CH; c += 2) {
+          uint32_t r[4];
+          const int chunk = c + (mi >> 1);
+          ldsm_x4(r, kb + C::at(16 * su + k_key, chunk));
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t a[4] = {hmul2(x[2 * k], s0), hmul2(y[2 * k], s1), hmul2(x[2 * k + 1], s0),
-                                   hmul2(y[2 * k + 1], s1)};
+          for (int h = 0; h < 2; ++h) {  // r[2h]: key g, chunk c + h; r[2h + 1]: key g + 8
+            uint32_t x[4], y[4];
+            e2m1x8_to_f16x2x4(r[2 * h], x);
+            e2m1x8_to_f16x2x4(r[2 * h + 1], y);
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-              mma_f16(s[nb], a, qb[2 * (c + h) + k][nb][0], qb[2 * (c + h) + k][nb][1]);
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t a[4] = {hmul2_by(x[2 * k], sg[0][c >> 1], h), hmul2_by(y[2 * k], sg[1][c >> 1], h),
+                                     hmul2_by(x[2 * k + 1], sg[0][c >> 1], h), hmul2_by(y[2 * k + 1], sg[1][c >> 1], h)};
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+                mma_f16(s[su][nb], a, qb[2 * (c + h) + k][nb][0], qb[2 * (c + h) + k][nb][1]);
+            }
           }
         }
       }
@@ -435,7 +466,7 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB>::CTAS) decode_kernel
           e4m3x4_to_f16x2x2(r[2 * h], a[0], a[2]);
           e4m3x4_to_f16x2x2(r[2 * h + 1], a[1], a[3]);
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) mma_f16(s[nb], a, qb[c + h][nb][0], qb[c + h][nb][1]);
+          for (int nb = 0; nb < NB; ++nb) mma_f16(s[0][nb], a, qb[c + h][nb][0], qb[c + h][nb][1]);
         }
       }
     }
@@ -444,109 +475,169 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB>::CTAS) decode_kernel
     // The reference max m moves only when a column's tile max exceeds it by more than 2^8 (one
     // warp-wide decision), so most tiles skip the O rescale; probabilities stay below 2^8.
     const bool full = key0 + C::KEYS <= w.kv_end;
-    uint32_t pb[NB][2];
+    uint32_t pb[C::SUBS][NB][2];
+    // per head column: scaled scores of keys 16 su + g, 16 su + g + 8 (NCOL = 1: columns 2t and 2t + 1 hold
+    // the same head, one of them is enough)
+    constexpr int NCOL = PAIR ? 1 : 2;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      float x0 = s[nb][0] * sc;  // key g,     head 2t
-      float x1 = s[nb][1] * sc;  // key g,     head 2t+1
-      float x2 = s[nb][2] * sc;  // key g + 8, head 2t
-      float x3 = s[nb][3] * sc;  // key g + 8, head 2t+1
-      const bool lo_ok = full || key0 + g < w.kv_end, hi_ok = full || key0 + g + 8 < w.kv_end;
-      if constexpr (SCORED) {
-        // [key][query head of the group]: heads 2t, 2t + 1 of keys g and g + 8
-        const int head = nb * 8 + 2 * t;
-        float* lg = logits + (int64_t)(key0 + g) * p.group + head;
-        if (pair_rows) {  // every row of heads starts on 8 bytes
-          if (head < rows) {
-            if (lo_ok) *reinterpret_cast<float2*>(lg) = make_float2(x0, x1);
-            if (hi_ok) *reinterpret_cast<float2*>(lg + 8 * p.group) = make_float2(x2, x3);
+      float x[C::SUBS][2][NCOL];
+#pragma unroll
+      for (int su = 0; su < C::SUBS; ++su) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int k = 0; k < NCOL; ++k) x[su][r][k] = s[su][nb][2 * r + k] * sc;
+        const int kl = key0 + 16 * su + g;
+        const bool lo_ok = full || kl < w.kv_end, hi_ok = full || kl + 8 < w.kv_end;
+        if constexpr (SCORED) {
+          // [key][query head of the group]
+          const int head = PAIR ? nb * 4 + t : nb * 8 + 2 * t;
+          float* lg = logits + (int64_t)kl * p.group + head;
+          if (!PAIR && pair_rows) {  // two heads at once: every row of heads starts on 8 bytes
+            if (head < rows) {
+              if (lo_ok) *reinterpret_cast<float2*>(lg) = make_float2(x[su][0][0], x[su][0][NCOL - 1]);
+              if (hi_ok) *reinterpret_cast<float2*>(lg + 8 * p.group) = make_float2(x[su][1][0], x[su][1][NCOL - 1]);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < NCOL; ++k) {
+              if (lo_ok && head + k < rows) lg[k] = x[su][0][k];
+              if (hi_ok && head + k < rows) lg[8 * p.group + k] = x[su][1][k];
+            }
           }
-        } else {
-          if (lo_ok && head < rows) lg[0] = x0;
-          if (lo_ok && head + 1 < rows) lg[1] = x1;
-          if (hi_ok && head < rows) lg[8 * p.group] = x2;
-          if (hi_ok && head + 1 < rows) lg[8 * p.group + 1] = x3;
+        }
+        if (!full) {
+#pragma unroll
+          for (int k = 0; k < NCOL; ++k) {
+            x[su][0][k] = lo_ok ? x[su][0][k] : -INFINITY;
+            x[su][1][k] = hi_ok ? x[su][1][k] : -INFINITY;
+          }
         }
       }
-      if (!full) {
-        x0 = lo_ok ? x0 : -INFINITY;
-        x1 = lo_ok ? x1 : -INFINITY;
-        x2 = hi_ok ? x2 : -INFINITY;
-        x3 = hi_ok ? x3 : -INFINITY;
-      }
-      float mx0 = fmaxf(x0, x2), mx1 = fmaxf(x1, x3);
+      float mx[NCOL];
 #pragma unroll
-      for (int sh = 4; sh < 32; sh <<= 1) {
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, sh));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, sh));
+      for (int k = 0; k < NCOL; ++k) {
+        mx[k] = fmaxf(x[0][0][k], x[0][1][k]);
+        if constexpr (C::SUBS == 2) mx[k] = fmax3(mx[k], x[1][0][k], x[1][1][k]);
       }
+#pragma unroll
+      for (int sh = 4; sh < 32; sh <<= 1)
+#pragma unroll
+        for (int k = 0; k < NCOL; ++k) mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], sh));
       // every tile holds at least one visible key, so the tile maxima are finite
-      if (__any_sync(0xffffffffu, mx0 > m[nb][0] + 8.f || mx1 > m[nb][1] + 8.f)) {
-        const float mn0 = fmaxf(m[nb][0], mx0), mn1 = fmaxf(m[nb][1], mx1);
-        const float c0 = ex2(m[nb][0] - mn0), c1 = ex2(m[nb][1] - mn1);
-        m[nb][0] = mn0;
-        m[nb][1] = mn1;
-        l[nb][0] *= c0;
-        l[nb][1] *= c1;
+      if (__any_sync(0xffffffffu, mx[0] > m[nb][0] + 8.f || mx[NCOL - 1] > m[nb][NCOL - 1] + 8.f)) {
+        float cf[NCOL];
 #pragma unroll
-        for (int mb = 0; mb < C::MB; ++mb) {
-          o[mb][nb][0] *= c0;
-          o[mb][nb][1] *= c1;
-          o[mb][nb][2] *= c0;
-          o[mb][nb][3] *= c1;
+        for (int k = 0; k < NCOL; ++k) {
+          const float mn = fmaxf(m[nb][k], mx[k]);
+          cf[k] = ex2(m[nb][k] - mn);
+          m[nb][k] = mn;
+          l[nb][k] *= cf[k];
         }
+#pragma unroll
+        for (int mb = 0; mb < C::MB; ++mb)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[mb][nb][j] *= cf[PAIR ? 0 : (j & 1)];
       }
-      x0 = ex2(x0 - m[nb][0]);
-      x1 = ex2(x1 - m[nb][1]);
-      x2 = ex2(x2 - m[nb][0]);
-      x3 = ex2(x3 - m[nb][1]);
-      l[nb][0] += x0 + x2;
-      l[nb][1] += x1 + x3;
-      // P^T in accumulator layout (row = key, column pair = heads) -> B operand (k = keys, n = head)
-      if constexpr (KV == PKV_BF16) {
-        pb[nb][0] = movmatrix_trans(pack_bf16(x0, x1));
-        pb[nb][1] = movmatrix_trans(pack_bf16(x2, x3));
-      } else {
-        pb[nb][0] = movmatrix_trans(pack_f16(x0, x1));
-        pb[nb][1] = movmatrix_trans(pack_f16(x2, x3));
+#pragma unroll
+      for (int su = 0; su < C::SUBS; ++su) {
+#pragma unroll
+        for (int k = 0; k < NCOL; ++k) {
+          x[su][0][k] = ex2(x[su][0][k] - m[nb][k]);
+          x[su][1][k] = ex2(x[su][1][k] - m[nb][k]);
+          l[nb][k] += x[su][0][k] + x[su][1][k];
+        }
+        // P^T in accumulator layout (row = key, column pair = heads) -> B operand (k = keys, n = head)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          if constexpr (KV == PKV_BF16)
+            pb[su][nb][r] = movmatrix_trans(pack_bf16(x[su][r][0], x[su][r][NCOL - 1]));
+          else
+            pb[su][nb][r] = movmatrix_trans(pack_f16(x[su][r][0], x[su][r][NCOL - 1]));
+        }
       }
     }
 
     // ---- O^T += V^T P^T ----
-    if constexpr (FP4) {
+    if constexpr (PAIR) {
+      // A byte holds two neighbouring dims of one key, and an A operand register wants two values that are
+      // neighbours in k.  So k runs over (key, parity of the dim): the A rows are pairs of dims, the 8
+      // columns are (head, parity), and B[(key, parity), (head, parity')] is P where the parities agree and
+      // 0 elsewhere.  One ldmatrix.trans register (key 2t: dims 4g .. 4g+3, key 2t + 1: the same) is then
+      // the A fragment of a whole 8-key x 32-dim MMA, byte by byte, with no bit of it moved; half of the
+      // tensor work is spent on zeros, which 4 heads in 8 columns would leave idle anyway.
+      const uint32_t sel = g < 4 ? 0x6420u : 0x7531u;
+#pragma unroll
+      for (int su = 0; su < C::SUBS; ++su) {
+        uint32_t sv[2][2][2];   // [keys 0-7 | 8-15][key 2t | 2t + 1][chunk pair], f16x2
+        uint32_t bb[NB][2][2];  // [..][keys 0-7 | 8-15][key 2t | 2t + 1]: (P, 0) in even columns, (0, P) in odd ones
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 f = *reinterpret_cast<const uint4*>(sfs + C::SF_B + (16 * su + 2 * t + 8 * h) * 8);
+          e4m3x4_to_f16x2x2(__byte_perm(f.x, f.y, sel), sv[h][0][0], sv[h][0][1]);
+          e4m3x4_to_f16x2x2(__byte_perm(f.z, f.w, sel), sv[h][1][0], sv[h][1][1]);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            bb[nb][h][0] = __byte_perm(pb[su][nb][h], 0, (g & 1) ? 0x1044u : 0x4410u);
+            bb[nb][h][1] = __byte_perm(pb[su][nb][h], 0, (g & 1) ? 0x3244u : 0x4432u);
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < C::CH; c += 2) {
+          uint32_t r[4];
+          const int chunk = c + (mi & 1);
+          ldsm_x4_t(r, vb + C::at(16 * su + v_key, chunk));  // r[2h + u]: keys 8h + 0-7, chunk c + u
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t x[4];
+              e2m1x8_to_f16x2x4(r[2 * h + u], x);
+              const uint32_t s0 = sv[h][0][c >> 1], s1 = sv[h][1][c >> 1];
+              const uint32_t a[4] = {hmul2_by(x[0], s0, u), hmul2_by(x[1], s0, u), hmul2_by(x[2], s1, u), hmul2_by(x[3], s1, u)};
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) mma_f16(o[c + u][nb], a, bb[nb][h][0], bb[nb][h][1]);
+            }
+        }
+      }
+    } else if constexpr (FP4) {
       // The codes of this lane's ldmatrix.trans register (dims 4g .. 4g+3 of a 32-dim chunk, keys 2t and
       // 2t + 1) lie in block 2 chunk + (g >> 2).  Its scale differs between the two keys, and so does the
       // f16x2 of one dim: the pair of scales multiplies the pair of values.
       const uint32_t sel = g < 4 ? 0x6420u : 0x7531u;
-      uint32_t sv[2][C::CH];  // [keys 2t, 2t+1 | keys 2t+8, 2t+9][chunk], f16x2 (one key per half)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint4 f = *reinterpret_cast<const uint4*>(sfs + C::SF_B + (2 * t + 8 * h) * 8);
-        const uint32_t fa = __byte_perm(f.x, f.y, sel), fb = __byte_perm(f.z, f.w, sel);
-        e4m3x4_to_f16x2x2(__byte_perm(fa, fb, 0x5140u), sv[h][0], sv[h][1]);
-        e4m3x4_to_f16x2x2(__byte_perm(fa, fb, 0x7362u), sv[h][2], sv[h][3]);
-      }
+      for (int su = 0; su < C::SUBS; ++su) {
+        uint32_t sv[2][C::CH];  // [keys 2t, 2t+1 | keys 2t+8, 2t+9][chunk], f16x2 (one key per half)
 #pragma unroll
-      for (int c = 0; c < C::CH; c += 2) {
-        uint32_t r[4];
-        const int chunk = c + (mi & 1);
-        ldsm_x4_t(r, vb + C::at(v_key, chunk));
-        // r[u]: keys 2t (low half), 2t + 1 (high half) x dims 4g .. 4g+3 of chunk c + u; r[2 + u]: keys + 8
+        for (int h = 0; h < 2; ++h) {
+          const uint4 f = *reinterpret_cast<const uint4*>(sfs + C::SF_B + (16 * su + 2 * t + 8 * h) * 8);
+          const uint32_t fa = __byte_perm(f.x, f.y, sel), fb = __byte_perm(f.z, f.w, sel);
+          e4m3x4_to_f16x2x2(__byte_perm(fa, fb, 0x5140u), sv[h][0], sv[h][1]);
+          e4m3x4_to_f16x2x2(__byte_perm(fa, fb, 0x7362u), sv[h][2], sv[h][3]);
+        }
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          uint32_t x[4], y[4];
-          e2m1_2x4_to_f16x2x4(r[u], x);
-          e2m1_2x4_to_f16x2x4(r[2 + u], y);
+        for (int c = 0; c < C::CH; c += 2) {
+          uint32_t r[4];
+          const int chunk = c + (mi & 1);
+          ldsm_x4_t(r, vb + C::at(16 * su + v_key, chunk));
+          // r[u]: keys 2t (low half), 2t + 1 (high half) x dims 4g .. 4g+3 of chunk c + u; r[2 + u]: keys + 8
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            x[k] = hmul2(x[k], sv[0][c + u]);
-            y[k] = hmul2(y[k], sv[1][c + u]);
-          }
+          for (int u = 0; u < 2; ++u) {
+            uint32_t x[4], y[4];
+            e2m1_2x4_to_f16x2x4(r[u], x);
+            e2m1_2x4_to_f16x2x4(r[2 + u], y);
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t a[4] = {x[2 * k], x[2 * k + 1], y[2 * k], y[2 * k + 1]};
+            for (int k = 0; k < 4; ++k) {
+              x[k] = hmul2(x[k], sv[0][c + u]);
+              y[k] = hmul2(y[k], sv[1][c + u]);
+            }
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) mma_f16(o[2 * (c + u) + k][nb], a, pb[nb][0], pb[nb][1]);
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t a[4] = {x[2 * k], x[2 * k + 1], y[2 * k], y[2 * k + 1]};
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) mma_f16(o[2 * (c + u) + k][nb], a, pb[su][nb][0], pb[su][nb][1]);
+            }
           }
         }
       }
@@ -557,7 +648,7 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB>::CTAS) decode_kernel
         const int chunk = 2 * mb + (mi & 1);
         ldsm_x4_t(a, vb + C::at(v_key, chunk));
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) mma_bf16(o[mb][nb], a, pb[nb][0], pb[nb][1]);
+        for (int nb = 0; nb < NB; ++nb) mma_bf16(o[mb][nb], a, pb[0][nb][0], pb[0][nb][1]);
       }
     } else {
 #pragma unroll
@@ -575,8 +666,8 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB>::CTAS) decode_kernel
         for (int k = 0; k < 4; ++k) e4m3x4_to_f16x2x2(__byte_perm(r[k], 0, 0x3120u), ev[k], od[k]);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          mma_f16(o[c][nb], ev, pb[nb][0], pb[nb][1]);
-          mma_f16(o[c + 1][nb], od, pb[nb][0], pb[nb][1]);
+          mma_f16(o[c][nb], ev, pb[0][nb][0], pb[0][nb][1]);
+          mma_f16(o[c + 1][nb], od, pb[0][nb][0], pb[0][nb][1]);
         }
       }
     }
@@ -603,20 +694,31 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB>::CTAS) decode_kernel
   if (g == 0) {
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      sm[warp * C::HEADS + nb * 8 + 2 * t] = m[nb][0];
-      sm[warp * C::HEADS + nb * 8 + 2 * t + 1] = m[nb][1];
-      sl[warp * C::HEADS + nb * 8 + 2 * t] = l[nb][0];
-      sl[warp * C::HEADS + nb * 8 + 2 * t + 1] = l[nb][1];
+      if constexpr (PAIR) {
+        sm[warp * C::HEADS + nb * 4 + t] = m[nb][0];
+        sl[warp * C::HEADS + nb * 4 + t] = l[nb][0];
+      } else {
+        sm[warp * C::HEADS + nb * 8 + 2 * t] = m[nb][0];
+        sm[warp * C::HEADS + nb * 8 + 2 * t + 1] = m[nb][1];
+        sl[warp * C::HEADS + nb * 8 + 2 * t] = l[nb][0];
+        sl[warp * C::HEADS + nb * 8 + 2 * t + 1] = l[nb][1];
+      }
     }
   }
 #pragma unroll
   for (int mb = 0; mb < C::MB; ++mb) {
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
+      if constexpr (PAIR) {  // rows g, g + 8 x columns 2t, 2t + 1: dims 4g .. 4g+3 of chunk mb, head t
+        if (nb * 4 + t < rows)
+          *reinterpret_cast<float4*>(so + (warp * C::HEADS + nb * 4 + t) * D + mb * 32 + 4 * g) =
+              make_float4(o[mb][nb][0], o[mb][nb][1], o[mb][nb][2], o[mb][nb][3]);
+      } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int head = nb * 8 + 2 * t + (j & 1);
-        if (head < rows) so[(warp * C::HEADS + head) * D + o_dim<KV>(mb, j, g)] = o[mb][nb][j];
+        for (int j = 0; j < 4; ++j) {
+          const int head = nb * 8 + 2 * t + (j & 1);
+          if (head < rows) so[(warp * C::HEADS + head) * D + o_dim<KV>(mb, j, g)] = o[mb][nb][j];
+        }
       }
     }
   }
@@ -865,21 +967,21 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB>::CTAS) decode_kernel
   }
 }
 
-template <int D, int KV, int NB, bool SCORED>
+template <int D, int KV, int NB, int HPB, bool SCORED>
 static cudaError_t launch_decode_t(const RunParams& p, cudaStream_t s) {
-  using C = DecodeCfg<D, KV, NB>;
+  using C = DecodeCfg<D, KV, NB, HPB>;
   static bool attr_set[64] = {false};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 0 && dev < 64 && !attr_set[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, KV, NB, SCORED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, KV, NB, HPB, SCORED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          C::SMEM);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
   int32_t* err = device_error_ptr();
   if (!err) return cudaErrorInvalidDevice;
-  return launch_pdl(decode_kernel<D, KV, NB, SCORED>, dim3((unsigned)p.num_work), dim3(128), (size_t)C::SMEM, s, p, err);
+  return launch_pdl(decode_kernel<D, KV, NB, HPB, SCORED>, dim3((unsigned)p.num_work), dim3(128), (size_t)C::SMEM, s, p, err);
 }
 
 // The instance for the pool's type, head_dim and query heads per KV head.
@@ -889,13 +991,16 @@ static cudaError_t launch_decode_any(const RunParams& p, int kv_dtype, cudaStrea
   if (kv_dtype == PKV_FP8_E4M3 || kv_dtype == PKV_NVFP4) {
     if (p.head_dim != 128) return cudaErrorInvalidValue;
     if (kv_dtype == PKV_NVFP4)
-      return nb2 ? launch_decode_t<128, PKV_NVFP4, 2, SCORED>(p, s) : launch_decode_t<128, PKV_NVFP4, 1, SCORED>(p, s);
-    return nb2 ? launch_decode_t<128, PKV_FP8_E4M3, 2, SCORED>(p, s) : launch_decode_t<128, PKV_FP8_E4M3, 1, SCORED>(p, s);
+      return p.group <= 4 ? launch_decode_t<128, PKV_NVFP4, 1, 4, SCORED>(p, s)
+             : !nb2       ? launch_decode_t<128, PKV_NVFP4, 2, 4, SCORED>(p, s)
+                          : launch_decode_t<128, PKV_NVFP4, 2, 8, SCORED>(p, s);
+    return nb2 ? launch_decode_t<128, PKV_FP8_E4M3, 2, 8, SCORED>(p, s)
+               : launch_decode_t<128, PKV_FP8_E4M3, 1, 8, SCORED>(p, s);
   }
   if (p.head_dim == 128)
-    return nb2 ? launch_decode_t<128, PKV_BF16, 2, SCORED>(p, s) : launch_decode_t<128, PKV_BF16, 1, SCORED>(p, s);
+    return nb2 ? launch_decode_t<128, PKV_BF16, 2, 8, SCORED>(p, s) : launch_decode_t<128, PKV_BF16, 1, 8, SCORED>(p, s);
   if (p.head_dim == 64)
-    return nb2 ? launch_decode_t<64, PKV_BF16, 2, SCORED>(p, s) : launch_decode_t<64, PKV_BF16, 1, SCORED>(p, s);
+    return nb2 ? launch_decode_t<64, PKV_BF16, 2, 8, SCORED>(p, s) : launch_decode_t<64, PKV_BF16, 1, 8, SCORED>(p, s);
   return cudaErrorInvalidValue;
 }
 

@@ -127,14 +127,16 @@ __device__ __forceinline__ void e2m1x8_to_f16x2x4(uint32_t x, uint32_t (&out)[4]
 // two rows of four codes (row 0 in the low half-word) to four f16x2: out[i] = (row 0, row 1) of element i
 __device__ __forceinline__ void e2m1_2x4_to_f16x2x4(uint32_t x, uint32_t (&out)[4]) {
   // pair the rows' nibbles into bytes first: {e0, e2} in one 16-bit word, {e1, e3} in another
-  const uint32_t even = (x & 0x0f0fu) | ((x >> 12) & 0xf0f0u);
-  const uint32_t odd = ((x >> 4) & 0x0f0fu) | ((x >> 16) & 0xf0f0u);
+  // (one select per word; only left shifts, and the results in the two upper bytes)
+  const uint32_t a = x << 16, b = x << 4, c = x << 12;
+  const uint32_t even = (a & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
+  const uint32_t odd = (c & 0x0f0f0f0fu) | (x & 0xf0f0f0f0u);
   asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %2;\n"
-      " cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n}\n"
+      " cvt.rn.f16x2.e2m1x2 %0, b2;\n cvt.rn.f16x2.e2m1x2 %1, b3;\n}\n"
       : "=r"(out[0]), "=r"(out[2])
       : "r"(even));
   asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %2;\n"
-      " cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n}\n"
+      " cvt.rn.f16x2.e2m1x2 %0, b2;\n cvt.rn.f16x2.e2m1x2 %1, b3;\n}\n"
       : "=r"(out[1]), "=r"(out[3])
       : "r"(odd));
 }
@@ -151,9 +153,12 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// one half of an f16x2 in both halves
-__device__ __forceinline__ uint32_t dup_lo(uint32_t x) { return __byte_perm(x, 0, 0x1010u); }
-__device__ __forceinline__ uint32_t dup_hi(uint32_t x) { return __byte_perm(x, 0, 0x3232u); }
+// both halves of a times one half of s (the high one if hi)
+__device__ __forceinline__ uint32_t hmul2_by(uint32_t a, uint32_t s, bool hi) {
+  const __half2 h = *reinterpret_cast<const __half2*>(&s);
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), hi ? __high2half2(h) : __low2half2(h));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
 
 // two floats to two E4M3 codes, round to nearest even, saturate to finite; lo -> low byte
 __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
