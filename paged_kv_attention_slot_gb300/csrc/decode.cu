@@ -8,7 +8,7 @@ int decode_ctas_per_sm(int kv_dtype, int head_dim, int group) {
   const bool nb2 = group > 8;
   if (kv_dtype == PKV_NVFP4)
     return group <= 4 ? DecodeCfg<128, PKV_NVFP4, 1, 4>::CTAS
-           : !nb2     ? DecodeCfg<128, PKV_NVFP4, 2, 4>::CTAS
+           : !nb2     ? DecodeCfg<128, PKV_NVFP4, 1, 8>::CTAS
                       : DecodeCfg<128, PKV_NVFP4, 2, 8>::CTAS;
   if (kv_dtype == PKV_FP8_E4M3)
     return nb2 ? DecodeCfg<128, PKV_FP8_E4M3, 2>::CTAS : DecodeCfg<128, PKV_FP8_E4M3, 1>::CTAS;

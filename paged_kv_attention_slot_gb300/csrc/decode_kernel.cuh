@@ -72,6 +72,7 @@ __device__ __forceinline__ void cp_async16_pol(uint32_t dst, const void* src, ui
 template <int D, int KV, int NB, int HPB = 8>
 struct DecodeCfg {
   static constexpr bool FP4 = KV == PKV_NVFP4;
+  static constexpr bool PAIR = HPB == 4;
   static constexpr int ROWB = FP4 ? D / 2 : KV == PKV_FP8_E4M3 ? D : 2 * D;  // bytes per key row of one head
   static constexpr int CH = ROWB / 16;          // 16-byte chunks per row
   static constexpr int KEYS = FP4 ? 32 : 16;    // keys per warp tile
@@ -80,7 +81,6 @@ struct DecodeCfg {
   static constexpr int SF_B = FP4 ? KEYS * D / 16 : 0;    // bytes of the block scales of one K (or V) tile
   static constexpr int STAGE_B = 2 * TILE_B + 2 * SF_B;  // K, V, K scales, V scales
   static constexpr int HEADS = HPB * NB;        // query heads per CTA (n dimension)
-  static constexpr bool PAIR = HPB == 4;
   static constexpr int STAGES = 3;
   static constexpr int WARPS = 4;
   // resident CTAs per SM: the 8-KB-per-stage bf16/D128 variant fits 2 (shared memory), the 4-KB
@@ -214,7 +214,11 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB, HPB>::CTAS) decode_k
   const int ps = p.page_size;
   const int ps_shift = (ps & (ps - 1)) == 0 ? __ffs(ps) - 1 : -1;  // page sizes are usually powers of 2
   auto page_of = [&](int key) -> int { return ps_shift >= 0 ? key >> ps_shift : key / ps; };
-  const bool halves_paged = FP4 && (ps & 15) == 0 && (w.kv_begin & 15) == 0;  // tiles start on multiples of 16 then
+  // NVFP4: tiles start on multiples of 16 and pages hold whole 16-key halves (and the byte strides fit 32 bits)
+  const bool halves_paged = FP4 && (ps & 15) == 0 && (w.kv_begin & 15) == 0 &&
+                            ((p.stride_page_b | p.stride_token_b | p.sf_page_b | p.sf_token_b) >> 32) == 0;
+  const int64_t lane_off = head_off + lc * 16;
+  const int lane_sw = C::at(lsub, lc);
   const int64_t row_step = (int64_t)RPI * p.stride_token_b;  // bytes between the rows of consecutive instructions
 
   // ---- the warp's tile sequence ----
@@ -263,21 +267,20 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB, HPB>::CTAS) decode_k
       // halves_paged), so the row addresses follow from two pages and a stride.
       const bool in_pool = (unsigned long long)(unsigned)page < (unsigned long long)p.num_pages;
       if (halves_paged && key0 + C::KEYS <= w.kv_end && __all_sync(0xffffffffu, in_pool)) {
-        const int off = key0 + lr - page_of(key0 + lr) * ps;  // of this lane's row
-        const int64_t srow = (int64_t)page * p.sf_page_b + (int64_t)off * p.sf_token_b + sf_head;
+        const unsigned off = key0 + lr - page_of(key0 + lr) * ps;  // of this lane's row
+        const uint64_t srow = (uint64_t)(unsigned)page * (unsigned)p.sf_page_b + (uint64_t)off * (unsigned)p.sf_token_b + sf_head;
         cp_async8(dv + C::TILE_B + lane * 8, p.k_sf + srow, 8u);
         cp_async8(dv + C::TILE_B + C::SF_B + lane * 8, p.v_sf + srow, 8u);
-        const int64_t crow = (int64_t)page * p.stride_page_b + (int64_t)off * p.stride_token_b + head_off;
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          const int64_t base = __shfl_sync(0xffffffffu, crow, 16 * hf) + (int64_t)lsub * p.stride_token_b + lc * 16;
+          const unsigned hp = __shfl_sync(0xffffffffu, page, 16 * hf), ho = __shfl_sync(0xffffffffu, off, 16 * hf) + lsub;
+          const uint64_t base = (uint64_t)hp * (unsigned)p.stride_page_b + (uint64_t)ho * (unsigned)p.stride_token_b + lane_off;
           const char* ks = p.k_pool + base;
           const char* vs = p.v_pool + base;
 #pragma unroll
           for (int j = 0; j < 16 / RPI; ++j) {
-            const uint32_t sw = C::at(16 * hf + j * RPI + lsub, lc);
-            cp_async16_pol(dk + sw, ks + j * row_step, 16u, kv_policy);
-            cp_async16_pol(dv + sw, vs + j * row_step, 16u, kv_policy);
+            cp_async16_pol(dk + lane_sw + (16 * hf + j * RPI) * C::ROWB, ks + j * row_step, 16u, kv_policy);
+            cp_async16_pol(dv + lane_sw + (16 * hf + j * RPI) * C::ROWB, vs + j * row_step, 16u, kv_policy);
           }
         }
         return;
@@ -990,9 +993,12 @@ static cudaError_t launch_decode_any(const RunParams& p, int kv_dtype, cudaStrea
   const bool nb2 = p.group > 8;
   if (kv_dtype == PKV_FP8_E4M3 || kv_dtype == PKV_NVFP4) {
     if (p.head_dim != 128) return cudaErrorInvalidValue;
+    // NVFP4: up to 4 query heads the pair form fills the 8 columns (4 heads: 64 requests of 512-4096 keys
+    // 41.8 us against 48.8 in the 8-head form, 2 x 131072 keys 59.6 against 68.9); for 5 to 8 heads it
+    // needs a second n-block and loses (8 heads, 256 ragged requests: 119 against 106 us)
     if (kv_dtype == PKV_NVFP4)
       return p.group <= 4 ? launch_decode_t<128, PKV_NVFP4, 1, 4, SCORED>(p, s)
-             : !nb2       ? launch_decode_t<128, PKV_NVFP4, 2, 4, SCORED>(p, s)
+             : !nb2       ? launch_decode_t<128, PKV_NVFP4, 1, 8, SCORED>(p, s)
                           : launch_decode_t<128, PKV_NVFP4, 2, 8, SCORED>(p, s);
     return nb2 ? launch_decode_t<128, PKV_FP8_E4M3, 2, 8, SCORED>(p, s)
                : launch_decode_t<128, PKV_FP8_E4M3, 1, 8, SCORED>(p, s);
