@@ -982,8 +982,11 @@ int pkv_kv_evict(const pkv_plan* plan, const pkv_cache* cache, float* scores, in
   if (plan->batch == 0) return PKV_OK;
   if (!scores || !kept || ((uintptr_t)scores | (uintptr_t)kept) & 3)
     return fail(PKV_EINVAL, "scores and kept must be non-NULL and 4-byte aligned");
-  int32_t max_len = 0;
-  for (const ReqInfo& r : plan->req) max_len = std::max(max_len, r.kv_len);
+  int32_t max_len = 0, num_long = 0;
+  for (const ReqInfo& r : plan->req) {
+    max_len = std::max(max_len, r.kv_len);
+    num_long += r.kv_len > budget;
+  }
   if (max_len > pkv::kEvictMaxLen)
     return fail(PKV_EUNSUPPORTED, "evict covers requests of up to " + std::to_string(pkv::kEvictMaxLen) + " keys");
   int32_t sms = 0;
@@ -1013,7 +1016,7 @@ int pkv_kv_evict(const pkv_plan* plan, const pkv_cache* cache, float* scores, in
   p.budget = budget;
   p.num_sink = num_sink;
   p.num_recent = num_recent;
-  PKV_CUDA(pkv::launch_evict(p, plan->batch, max_len, sms, (cudaStream_t)stream), "evict launch");
+  PKV_CUDA(pkv::launch_evict(p, plan->batch, num_long, max_len, sms, (cudaStream_t)stream), "evict launch");
   return PKV_OK;
 }
 

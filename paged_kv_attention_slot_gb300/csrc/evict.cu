@@ -12,18 +12,25 @@
 // before it is written.
 //
 // What bounds it: reading the scores once (4 bytes per key) and moving the rows; there is no
-// arithmetic to speak of.  With few units the work of one has to be spread, so a unit belongs to a
-// thread-block cluster of C CTAs: each takes a contiguous slice of the positions, and histograms, prefix
-// counts and the list of moves go through distributed shared memory.  One launch does it all, and
-// nothing is read back: the new length is min(L, b).
+// arithmetic to speak of, but a chain of steps (scores, selection, prefix counts, moves).  One launch does
+// them all, and nothing is read back: the new length is min(L, b).  A unit belongs to a thread-block
+// cluster of C CTAs, in one of two forms:
+//   * requests of up to kMaxWhole keys: every CTA of the cluster selects on its own, from its own copy of
+//     the scores (C-fold reads, from L2), and moves its own columns of every row (C = 2: K and V).  The CTAs
+//     exchange nothing; one cluster barrier, long passed when it is waited for, keeps the scores from
+//     being rewritten before everyone has read them.
+//   * longer ones: each CTA takes a contiguous slice of the positions; histograms, prefix counts and
+//     the list of moves go through distributed shared memory.
 //
 // Selection: a radix select on the scores as order-preserving 32-bit keys, 11 + 11 + 10 bits from the
-// top; each pass histograms the keys that share the digits found so far.  It leaves the m-th largest
-// key and how many of the keys equal to it survive; those go by position.
+// top; each pass histograms the keys that share the digits found so far, and the passes end early when
+// all of those survive.  It leaves the smallest surviving key and how many of the keys equal to it
+// survive; those go by position.
 
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "pkv_internal.h"
 #include "ptx.cuh"
@@ -34,27 +41,33 @@ namespace pkv {
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 2048;       // 4 per thread
-constexpr int kListCap = 1024;    // moves one CTA holds at a time
-constexpr int kUnroll = 4;        // 16-byte chunks in flight per thread
-constexpr int kMaxKeys = 32768;   // scores of a slice kept in shared memory (128 KB); longer slices re-read them
-constexpr int kMaxSlice = 262144; // positions per CTA at most (12 bytes of shared memory per 32 of them)
+constexpr int kBins = 2048;
+constexpr int kUnroll = 4;         // 16-byte chunks in flight per thread
+constexpr int kScoreUnroll = 4;    // groups of four scores in flight per thread
+constexpr int kMaxWhole = 12288;   // longest request of the whole form (48 KB of scores)
+constexpr int kMaxKeys = 32768;    // scores of a slice kept in shared memory (128 KB); longer slices re-read them
+constexpr int kMaxSlice = 262144;  // positions per CTA at most (12 bytes of shared memory per 32 of them)
 constexpr int kMaxCluster = 8;
-
-static_assert(kBins == 4 * kThreads, "four bins per thread");
 static_assert((int64_t)kMaxSlice * kMaxCluster >= kEvictMaxLen, "a cluster covers the longest request");
 
-struct Shared {
-  uint32_t hist[2][kBins];
-  int2 move[kListCap];        // (destination position, source position)
-  int4 place[kListCap];       // their (page, offset): dst page, dst offset, src page, src offset
-  uint32_t warp_sum[kWarps];
-  unsigned long long warp_sum2[kWarps];
-  uint32_t digit, rest;       // of the radix pass: the digit found, how many keys to take inside it
-  uint32_t eq_total;          // this CTA's keys equal to the threshold
-  unsigned long long hm_total;  // this CTA's holes (high half) and movers (low half)
+template <bool SLICED>
+struct Form {
+  static constexpr int THREADS = SLICED ? 1024 : 256;
+  static constexpr int CTAS = SLICED ? 1 : 5;     // resident per SM
+  static constexpr int WARPS = THREADS / 32;
+  static constexpr int LIST = SLICED ? 2048 : 512;  // moves one CTA holds at a time
+  static constexpr int HISTS = SLICED ? 2 : 1;
+  static_assert(THREADS <= LIST, "the list holds a tile of the last rows");
+  static constexpr int GROUPS = SLICED ? kBins / 32 : 1;  // sliced: sums of 32 neighbouring bins
+  struct alignas(16) Shared {
+    uint32_t hist[HISTS][kBins];
+    uint32_t group[HISTS][GROUPS];
+    int2 move[LIST];         // (destination position, source position)
+    longlong2 place[LIST];   // byte offsets of their rows in the pools: (destination, source)
+    unsigned long long warp_sum[WARPS];
+    uint32_t digit, rest, count;  // of the radix pass: the digit found, the keys to take inside it, its keys
+    unsigned long long hm_total;  // sliced: this CTA's holes (high half) and movers (low half)
+  };
 };
 
 // scores in an order-preserving unsigned form; a NaN is the lowest, -0 equals +0
@@ -64,9 +77,9 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// exclusive prefix over the threads of `v`, and the total of the block
-template <typename V>
-__device__ __forceinline__ V block_prefix(V v, V* warp_sum, V& total) {
+// exclusive prefix over the block's threads of `v`, and the total of the block
+template <int WARPS, typename V>
+__device__ __forceinline__ V block_prefix(V v, unsigned long long* warp_sum, V& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   V inc = v;
 #pragma unroll
@@ -77,15 +90,16 @@ __device__ __forceinline__ V block_prefix(V v, V* warp_sum, V& total) {
   __syncthreads();  // the previous use of warp_sum is over
   if (lane == 31) warp_sum[warp] = inc;
   __syncthreads();
-  V before = 0, all = 0;
+  // every warp scans the warps' sums itself
+  V s = lane < WARPS ? (V)warp_sum[lane] : (V)0;
 #pragma unroll
-  for (int k = 0; k < kWarps; ++k) {
-    const V s = warp_sum[k];
-    before += k < warp ? s : 0;
-    all += s;
+  for (int o = 1; o < WARPS; o <<= 1) {
+    const V u = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += u;
   }
-  total = all;
-  return before + inc - v;
+  total = __shfl_sync(0xffffffffu, s, WARPS - 1);
+  const V before = __shfl_sync(0xffffffffu, s, warp > 0 ? warp - 1 : 0);
+  return (warp > 0 ? before : (V)0) + inc - v;
 }
 
 // bits [lo, hi) of the 32 positions that start at `first`
@@ -95,18 +109,28 @@ __device__ __forceinline__ uint32_t range_mask(int first, int lo, int hi) {
   return (b - a == 32 ? 0xffffffffu : ((1u << (b - a)) - 1u)) << a;
 }
 
-__global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p, int slice_cap, int key_cap) {
+template <bool SLICED>
+__global__ void __launch_bounds__(Form<SLICED>::THREADS, Form<SLICED>::CTAS) evict_kernel(const EvictParams p, int slice_cap,
+                                                                                         int key_cap) {
+  using F = Form<SLICED>;
+  constexpr int THREADS = F::THREADS, WARPS = F::WARPS;
   extern __shared__ __align__(16) uint8_t smem[];
-  Shared& sh = *reinterpret_cast<Shared*>(smem);
+  typename F::Shared& sh = *reinterpret_cast<typename F::Shared*>(smem);
   const int word_cap = slice_cap / 32;
-  uint32_t* lives = reinterpret_cast<uint32_t*>(smem + sizeof(Shared));  // survivors of the slice, a bit each
-  uint32_t* eqw = lives + word_cap;    // keys equal to the threshold; later the holes before each word
-  uint32_t* mov = eqw + word_cap;      // movers before each word
-  uint32_t* keys = mov + word_cap;     // [key_cap] order-preserving scores of the slice (key_cap = 0: not kept)
+  // [key_cap] order-preserving scores of the slice (a multiple of 32, or 0: not kept; 16-byte aligned)
+  uint32_t* keys = reinterpret_cast<uint32_t*>(smem + sizeof(typename F::Shared));
+  uint32_t* lives = keys + key_cap;  // survivors of the slice, a bit each
+  uint32_t* eqw = lives + word_cap;  // keys equal to the threshold; later the holes before each word
+  uint32_t* mov = eqw + word_cap;    // movers before each word
 
   cg::cluster_group cluster = cg::this_cluster();
-  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-  const int unit = blockIdx.x / C;
+  const int CN = (int)cluster.num_blocks(), CR = (int)cluster.block_rank();
+  const int C = SLICED ? CN : 1, rank = SLICED ? CR : 0;  // how positions and rows are shared out
+  auto unit_sync = [&]() {
+    if constexpr (SLICED) cluster.sync();
+    else __syncthreads();
+  };
+  const int unit = blockIdx.x / CN;
   const int h = unit % p.num_kv_heads, i = unit / p.num_kv_heads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
@@ -115,7 +139,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p, in
   const int L = rq.kv_len, b = p.budget, S = p.num_sink, R = p.num_recent;
   int32_t* kept = p.kept + (int64_t)unit * b;
   if (L <= b) {  // the whole cluster: nothing to evict
-    for (int j = rank * kThreads + tid; j < b; j += C * kThreads) kept[j] = j < L ? j : -1;
+    for (int j = CR * THREADS + tid; j < b; j += CN * THREADS) kept[j] = j < L ? j : -1;
     return;
   }
   const int32_t* pages = p.kv_indices + rq.page_base;
@@ -130,12 +154,15 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p, in
     return p.scores + ((int64_t)page * p.num_kv_heads + h) * ps + off;
   };
 
-  const int m = b - S - R;          // body keys that survive
+  const int m = b - S - R;  // body keys that survive
   const int front = b - R, tail = L - R;
   const int slice = ((L + C - 1) / C + 31) / 32 * 32;  // <= slice_cap
   const int base = rank * slice;
   const int n = max(0, min(slice, L - base));  // positions of this slice
   const int nw = (n + 31) / 32;
+
+  if (m > 0)
+    for (int k = tid; k < F::HISTS * kBins; k += THREADS) (&sh.hist[0][0])[k] = 0u;
 
   // ---- the scores of the body ----
   auto key_from_memory = [&](int pos) -> uint32_t {
@@ -143,69 +170,172 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p, in
     place_of(pos, page, off);
     return order_key(*score_at(page, off));
   };
-  const bool cached = key_cap > 0;
-  if (cached)
-    for (int k = tid; k < n; k += kThreads) {
-      const int pos = base + k;
-      keys[k] = pos >= S && pos < tail ? key_from_memory(pos) : 0u;
-    }
-  auto key_at = [&](int k) -> uint32_t { return cached ? keys[k] : key_from_memory(base + k); };
+  const bool cached = !SLICED || key_cap > 0;
   const int body_lo = min(max(S - base, 0), n), body_hi = min(max(tail - base, 0), n);
+  if (cached) {
+    // (positions outside the body get some key that no one looks at)
+    if ((ps & 3) == 0 && (reinterpret_cast<uintptr_t>(p.scores) & 15) == 0) {
+      // four positions of one page at a time; a last group may reach past L, but not past its page
+      const int groups = (n + 3) / 4;
+      for (int q0 = tid; q0 < groups; q0 += THREADS * kScoreUnroll) {
+        float4 x[kScoreUnroll];
+#pragma unroll
+        for (int u = 0; u < kScoreUnroll; ++u) {
+          const int q = q0 + u * THREADS;
+          if (q < groups) {
+            int page, off;
+            place_of(base + 4 * q, page, off);
+            x[u] = *reinterpret_cast<const float4*>(score_at(page, off));
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kScoreUnroll; ++u) {
+          const int q = q0 + u * THREADS;
+          if (q < groups)
+            *reinterpret_cast<uint4*>(keys + 4 * q) =
+                make_uint4(order_key(x[u].x), order_key(x[u].y), order_key(x[u].z), order_key(x[u].w));
+        }
+      }
+    } else {
+      for (int k0 = tid; k0 < n; k0 += THREADS * kScoreUnroll) {
+        uint32_t x[kScoreUnroll];
+#pragma unroll
+        for (int u = 0; u < kScoreUnroll; ++u) {
+          const int k = k0 + u * THREADS;
+          if (k < n) x[u] = key_from_memory(base + k);
+        }
+#pragma unroll
+        for (int u = 0; u < kScoreUnroll; ++u) {
+          const int k = k0 + u * THREADS;
+          if (k < n) keys[k] = x[u];
+        }
+      }
+    }
+  }
+  auto key_at = [&](int k) -> uint32_t { return cached ? keys[k] : key_from_memory(base + k); };
+  // whole form: this CTA has read every score it will read (waited for before scores are moved)
+  if constexpr (!SLICED) cluster.barrier_arrive();
 
   // ---- the m-th largest key of the unit's body ----
-  uint32_t T = 0xffffffffu;  // above every key: nothing survives
+  uint32_t T = 0xffffffffu;  // keys above T survive, and need_eq of those equal to it (m = 0: none is above)
   uint32_t need_eq = 0;
+  uint32_t eq_before = 0;  // keys equal to T in the slices before this one
+  __syncthreads();
   if (m > 0) {
-    for (int k = tid; k < 2 * kBins; k += kThreads) (&sh.hist[0][0])[k] = 0u;
-    __syncthreads();
     uint32_t prefix = 0, fixed = 0, rest = (uint32_t)m;
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
       const uint32_t bits = pass == 2 ? 0x3ffu : 0x7ffu;
-      uint32_t* hist = sh.hist[pass & 1];
-      for (int k = body_lo + tid; k < body_hi; k += kThreads) {
+      uint32_t* hist = sh.hist[SLICED ? pass & 1 : 0];
+      for (int k = body_lo + tid; k < body_hi; k += THREADS) {
         const uint32_t key = key_at(k);
         if ((key & fixed) == prefix) atomicAdd(&hist[(key >> shift) & bits], 1u);
       }
-      cluster.sync();
-      // this thread's four bins, over the cluster's slices; bins in descending order over the threads
-      const int bin0 = kBins - 4 - 4 * tid;
-      uint4 c = make_uint4(0u, 0u, 0u, 0u);
-      for (int r = 0; r < C; ++r) {
-        const uint4 x = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(hist, r) + bin0);
-        c.x += x.x;
-        c.y += x.y;
-        c.z += x.z;
-        c.w += x.w;
-      }
-      uint32_t total;
-      uint32_t above = block_prefix<uint32_t>(c.x + c.y + c.z + c.w, sh.warp_sum, total);
-      const uint32_t cnt[4] = {c.w, c.z, c.y, c.x};  // descending
+      if constexpr (SLICED) {
+        // the bin of the rest-th key from the top, over the cluster's slices: first its group of 32 bins,
+        // then the bin, so that two short rounds of remote reads do (one warp) instead of whole histograms
+        __syncthreads();
+        uint32_t* group = sh.group[pass & 1];
+        for (int g = tid / 16; g < F::GROUPS; g += THREADS / 16) {
+          uint32_t v = hist[32 * g + 2 * (tid & 15)] + hist[32 * g + 2 * (tid & 15) + 1];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (above < rest && above + cnt[k] >= rest) {  // exactly one (thread, bin) of the block
-          sh.digit = (uint32_t)(bin0 + 3 - k);
-          sh.rest = rest - above;
+          for (int o = 1; o < 16; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+          if ((tid & 15) == 0) group[g] = v;
         }
-        above += cnt[k];
+        cluster.sync();
+        if (warp == 0) {
+          uint32_t hi = 0, lo = 0;  // groups 63 - lane and 31 - lane
+#pragma unroll
+          for (int r = 0; r < kMaxCluster; ++r)
+            if (r < C) {
+              const uint32_t* gr = cluster.map_shared_rank(group, r);
+              hi += gr[63 - lane];
+              lo += gr[31 - lane];
+            }
+          uint32_t ihi = hi, ilo = lo;  // inclusive, from the top
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t a = __shfl_up_sync(0xffffffffu, ihi, o), c = __shfl_up_sync(0xffffffffu, ilo, o);
+            if (lane >= o) {
+              ihi += a;
+              ilo += c;
+            }
+          }
+          ilo += __shfl_sync(0xffffffffu, ihi, 31);
+          const uint32_t bh = __ballot_sync(0xffffffffu, ihi >= rest), bl = __ballot_sync(0xffffffffu, ilo >= rest);
+          const int src = __ffs(bh ? bh : bl) - 1;  // the body holds at least m keys, so one is set
+          const uint32_t above_g = __shfl_sync(0xffffffffu, bh ? ihi - hi : ilo - lo, src);
+          const int g = (bh ? 63 : 31) - src;
+          uint32_t c = 0;
+#pragma unroll
+          for (int r = 0; r < kMaxCluster; ++r)
+            if (r < C) c += cluster.map_shared_rank(hist, r)[32 * g + 31 - lane];
+          uint32_t inc = c;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t a = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += a;
+          }
+          inc += above_g;
+          if (inc >= rest && inc - c < rest) {  // exactly one lane
+            sh.digit = (uint32_t)(32 * g + 31 - lane);
+            sh.rest = rest - (inc - c);
+            sh.count = c;
+          }
+        }
+      } else {
+        __syncthreads();
+        // this thread's bins, in descending order over the threads
+        constexpr int BINS_PT = kBins / THREADS;
+        const int bin0 = kBins - BINS_PT * (tid + 1);
+        uint32_t cnt[BINS_PT];
+#pragma unroll
+        for (int k = 0; k < BINS_PT; k += 2) {
+          const uint2 x = *reinterpret_cast<const uint2*>(hist + bin0 + k);
+          cnt[k] = x.x;
+          cnt[k + 1] = x.y;
+        }
+        uint32_t mine = 0, total;
+#pragma unroll
+        for (int k = 0; k < BINS_PT; ++k) mine += cnt[k];
+        uint32_t above = block_prefix<WARPS, uint32_t>(mine, sh.warp_sum, total);
+#pragma unroll
+        for (int k = BINS_PT - 1; k >= 0; --k) {
+          if (above < rest && above + cnt[k] >= rest) {  // exactly one (thread, bin) of the block
+            sh.digit = (uint32_t)(bin0 + k);
+            sh.rest = rest - above;
+            sh.count = cnt[k];
+          }
+          above += cnt[k];
+        }
       }
+      // Sliced: pass 2 uses hist[0] again; every CTA read it before the cluster barrier of pass 1.
+      // Whole: every thread of this CTA has read it before the barriers of block_prefix.
+      if (SLICED ? pass == 1 : pass < 2)
+        for (int k = tid; k < kBins; k += THREADS) sh.hist[0][k] = 0u;
       __syncthreads();
       prefix |= sh.digit << shift;
       fixed |= bits << shift;
       rest = sh.rest;
-      // pass 2 uses hist[0] again: every CTA read it before the cluster barrier of pass 1
-      if (pass == 1)
-        for (int k = tid; k < kBins; k += kThreads) sh.hist[0][k] = 0u;
-      __syncthreads();
+      if (pass == 2) {
+        // the last pass counted every slice's keys equal to T
+        if constexpr (SLICED) {
+          const uint32_t x = lane < rank ? cluster.map_shared_rank(hist, lane)[sh.digit] : 0u;
+          eq_before = __reduce_add_sync(0xffffffffu, x);
+        }
+      } else if (sh.count == rest && prefix > 0) {
+        // every key with these digits survives: all keys from `prefix` up, none by position
+        prefix -= 1;
+        rest = 0;
+        break;
+      }
     }
     T = prefix;
     need_eq = rest;
-  } else {
-    __syncthreads();
   }
 
   // ---- survivors, a bit per position ----
-  for (int w = warp; w < nw; w += kWarps) {
+  for (int w = warp; w < nw; w += WARPS) {
     const int k = w * 32 + lane;
     const bool body = k >= body_lo && k < body_hi;
     const uint32_t key = body ? key_at(k) : 0u;
@@ -217,18 +347,16 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p, in
     }
   }
   __syncthreads();
-  const int per_thread = (nw + kThreads - 1) / kThreads;  // consecutive words per thread
+  const int per_thread = (nw + THREADS - 1) / THREADS;  // consecutive words per thread
   const int w0 = min(tid * per_thread, nw), w1 = min(w0 + per_thread, nw);
-  uint32_t eq_mine = 0;
-  for (int w = w0; w < w1; ++w) eq_mine += __popc(eqw[w]);
-  uint32_t total;
-  uint32_t eq_before = block_prefix<uint32_t>(eq_mine, sh.warp_sum, total);
-  if (tid == 0) sh.eq_total = total;
-  cluster.sync();
-  for (int r = 0; r < rank; ++r) eq_before += *cluster.map_shared_rank(&sh.eq_total, r);
+  if (need_eq > 0) {
+    uint32_t eq_mine = 0, total;
+    for (int w = w0; w < w1; ++w) eq_mine += __popc(eqw[w]);
+    eq_before += block_prefix<WARPS, uint32_t>(eq_mine, sh.warp_sum, total);
+  }
   unsigned long long hm = 0;
   for (int w = w0; w < w1; ++w) {
-    uint32_t e = eqw[w];
+    uint32_t e = need_eq > 0 ? eqw[w] : 0u;
     const uint32_t c = __popc(e);
     if (eq_before + c > need_eq) {  // only the lowest (need_eq - eq_before) of them
       uint32_t take = eq_before < need_eq ? need_eq - eq_before : 0u, out = 0u;
@@ -245,14 +373,15 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p, in
     hm += (unsigned long long)__popc(~alive & range_mask(first, S, front)) << 32 | __popc(alive & range_mask(first, front, tail));
   }
   unsigned long long hm_all;
-  unsigned long long hm_before = block_prefix<unsigned long long>(hm, sh.warp_sum2, hm_all);
-  if (tid == 0) sh.hm_total = hm_all;
-  cluster.sync();
-  uint32_t holes = 0;  // of the unit (= its movers)
-  for (int r = 0; r < C; ++r) {
-    const unsigned long long x = *cluster.map_shared_rank(&sh.hm_total, r);
-    if (r < rank) hm_before += x;
-    holes += (uint32_t)(x >> 32);
+  unsigned long long hm_before = block_prefix<WARPS, unsigned long long>(hm, sh.warp_sum, hm_all);
+  uint32_t holes = (uint32_t)(hm_all >> 32);  // of the unit (= its movers)
+  if constexpr (SLICED) {
+    if (tid == 0) sh.hm_total = hm_all;
+    cluster.sync();
+    const unsigned long long x = lane < C ? *cluster.map_shared_rank(&sh.hm_total, lane) : 0ull;
+    holes = __reduce_add_sync(0xffffffffu, (uint32_t)(x >> 32));
+    hm_before += (unsigned long long)__reduce_add_sync(0xffffffffu, lane < rank ? (uint32_t)(x >> 32) : 0u) << 32;
+    hm_before += __reduce_add_sync(0xffffffffu, lane < rank ? (uint32_t)x : 0u);
   }
   for (int w = w0; w < w1; ++w) {
     const int first = base + w * 32;
@@ -263,157 +392,187 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p, in
   }
   __syncthreads();
 
-  // ---- fill the holes, C * kListCap moves at a time ----
-  const int rc = p.row_chunks;                     // a power of two
-  const int item_shift = 31 - __clz(2 * rc);       // 16-byte chunks of a K and a V row
+  // ---- fill the holes, C * LIST moves at a time ----
+  // A CTA moves `cols` 16-byte chunks from chunk col0 on of every row pair it is given (K, then V).
+  const int rc = p.row_chunks;  // a power of two
+  const int cols = SLICED ? 2 * rc : 2 * rc / CN, col0 = SLICED ? 0 : CR * cols;
+  const int item_shift = 31 - __clz(cols);
+  // whole form: the first CTA moves scores, kept positions and K scales, the last one V scales
+  const bool with_k = SLICED || CR == 0, with_v = SLICED || CR == CN - 1;
   const int64_t head_off = (int64_t)h * p.stride_head_b, sf_head = (int64_t)h * p.sf_head_b;
-  auto chunk_ptr = [&](int page, int off, int c) -> uint4* {
-    char* pool = c < rc ? p.k_pool : p.v_pool;
-    return reinterpret_cast<uint4*>(pool + (int64_t)page * p.stride_page_b + (int64_t)off * p.stride_token_b + head_off) +
-           (c & (rc - 1));
+  auto row_off = [&](int page, int off) -> int64_t {
+    return (int64_t)page * p.stride_page_b + (int64_t)off * p.stride_token_b + head_off;
+  };
+  // chunk x of the CTA's columns of the row at byte offset `off`
+  auto chunk_ptr = [&](int64_t off, int x) -> uint4* {
+    const int c = col0 + x;
+    return reinterpret_cast<uint4*>((c < rc ? p.k_pool : p.v_pool) + off) + (c & (rc - 1));
   };
   auto sf_off = [&](int page, int off) -> int64_t {
     return (int64_t)page * p.sf_page_b + (int64_t)off * p.sf_token_b + sf_head;
   };
+  if constexpr (!SLICED) cluster.barrier_wait();  // all CTAs of the unit have read its scores
   const uint32_t lt = (1u << lane) - 1u;
   for (uint32_t t0 = 0, per = 0; t0 < holes || t0 == 0; t0 += per * C) {
-    per = min((uint32_t)kListCap, (holes - t0 + C - 1) / C);  // moves per CTA of this round
-    for (int w = warp; w < nw; w += kWarps) {
+    per = min((uint32_t)F::LIST, (holes - t0 + C - 1) / C);  // moves per CTA of this round
+    const float inv_per = 1.f / (float)max(per, 1u);
+    for (int w = warp; w < nw; w += WARPS) {
       const int first = base + w * 32, pos = first + lane;
       const uint32_t alive = lives[w];
       const uint32_t hb = ~alive & range_mask(first, S, front), mb = alive & range_mask(first, front, tail);
-      if (t0 == 0 && pos < front && !((hb >> lane) & 1)) kept[pos] = pos;
       const bool hole = (hb >> lane) & 1, mover = (mb >> lane) & 1;
+      if (with_k && t0 == 0 && pos < front && !hole) kept[pos] = pos;
       if (hole || mover) {
         const uint32_t t = (hole ? eqw[w] + __popc(hb & lt) : mov[w] + __popc(mb & lt)) - t0;  // wraps below t0
         if (t < per * C) {
-          int2* e = cluster.map_shared_rank(sh.move, t / per) + t % per;
+          int2* e;
+          if constexpr (SLICED) {
+            int r = (int)((float)t * inv_per);  // t / per, off by one at most (t < 2^14)
+            r += (uint32_t)(r + 1) * per <= t;
+            r -= (uint32_t)r * per > t;
+            e = cluster.map_shared_rank(sh.move, r) + (t - r * per);
+          } else {
+            e = sh.move + t;
+          }
           if (hole) e->x = pos;
           else e->y = pos;
         }
       }
     }
     if (holes == 0) break;
-    cluster.sync();  // the lists are complete
+    unit_sync();  // the lists are complete
     const int mine = (int)min((int64_t)per, max((int64_t)0, (int64_t)holes - t0 - (int64_t)rank * per));
-    for (int e = tid; e < mine; e += kThreads) {
+    for (int e = tid; e < mine; e += THREADS) {
       const int2 mv = sh.move[e];
-      int4 pl;
-      place_of(mv.x, pl.x, pl.y);
-      place_of(mv.y, pl.z, pl.w);
-      sh.place[e] = pl;
-      kept[mv.x] = mv.y;
-      *score_at(pl.x, pl.y) = *score_at(pl.z, pl.w);
+      int dp, dof, sp, sof;
+      place_of(mv.x, dp, dof);
+      place_of(mv.y, sp, sof);
+      sh.place[e] = make_longlong2(row_off(dp, dof), row_off(sp, sof));
+      if (with_k) {
+        kept[mv.x] = mv.y;
+        *score_at(dp, dof) = *score_at(sp, sof);
+      }
       if (p.k_sf) {
-        const int64_t d = sf_off(pl.x, pl.y), s = sf_off(pl.z, pl.w);
-        *reinterpret_cast<uint2*>(p.k_sf + d) = *reinterpret_cast<const uint2*>(p.k_sf + s);
-        *reinterpret_cast<uint2*>(p.v_sf + d) = *reinterpret_cast<const uint2*>(p.v_sf + s);
+        const int64_t d = sf_off(dp, dof), s = sf_off(sp, sof);
+        if (with_k) *reinterpret_cast<uint2*>(p.k_sf + d) = *reinterpret_cast<const uint2*>(p.k_sf + s);
+        if (with_v) *reinterpret_cast<uint2*>(p.v_sf + d) = *reinterpret_cast<const uint2*>(p.v_sf + s);
       }
     }
     __syncthreads();
     const int items = mine << item_shift;
-    for (int x0 = tid; x0 < items; x0 += kThreads * kUnroll) {
+    for (int x0 = tid; x0 < items; x0 += THREADS * kUnroll) {
       uint4 v[kUnroll];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        const int x = x0 + u * kThreads;
-        if (x < items) {
-          const int4 pl = sh.place[x >> item_shift];
-          v[u] = *chunk_ptr(pl.z, pl.w, x & (2 * rc - 1));
-        }
+        const int x = x0 + u * THREADS;
+        if (x < items) v[u] = *chunk_ptr(sh.place[x >> item_shift].y, x & (cols - 1));
       }
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        const int x = x0 + u * kThreads;
-        if (x < items) {
-          const int4 pl = sh.place[x >> item_shift];
-          *chunk_ptr(pl.x, pl.y, x & (2 * rc - 1)) = v[u];
-        }
+        const int x = x0 + u * THREADS;
+        if (x < items) *chunk_ptr(sh.place[x >> item_shift].x, x & (cols - 1)) = v[u];
       }
     }
-    cluster.sync();  // the lists may be rewritten; sources in [front, tail) may be overwritten
+    unit_sync();  // the lists may be rewritten; sources in [front, tail) may be overwritten
   }
 
   // ---- the last R keys move down by L - b, in order ----
-  const bool overlap = L - b < R;  // tiles are then read by the whole cluster before any is written
-  const int gtid = rank * kThreads + tid, gstride = C * kThreads;
-  for (int j0 = 0; j0 < R; j0 += gstride) {
-    const int j = j0 + gtid;
+  const bool overlap = L - b < R;  // tiles are then read by all who share them before any is written
+  const int rows = min(THREADS, (THREADS * kUnroll) >> item_shift);  // rows per CTA and tile
+  for (int j0 = 0; j0 < R; j0 += C * rows) {
+    const int first = j0 + rank * rows;
+    const int mine = max(0, min(rows, R - first));
     float sc = 0.f;
     uint2 fk = make_uint2(0u, 0u), fv = fk;
     int dp = 0, dof = 0;
-    if (j < R) {
-      int sp, so;
-      place_of(tail + j, sp, so);
+    if (tid < mine) {
+      const int j = first + tid;
+      int sp, sof;
+      place_of(tail + j, sp, sof);
       place_of(front + j, dp, dof);
-      sc = *score_at(sp, so);
-      if (p.k_sf) {
-        fk = *reinterpret_cast<const uint2*>(p.k_sf + sf_off(sp, so));
-        fv = *reinterpret_cast<const uint2*>(p.v_sf + sf_off(sp, so));
+      sh.place[tid] = make_longlong2(row_off(dp, dof), row_off(sp, sof));
+      if (with_k) {
+        sc = *score_at(sp, sof);
+        kept[front + j] = tail + j;
       }
-      kept[front + j] = tail + j;
-    }
-    if (overlap) cluster.sync();
-    if (j < R) {
-      *score_at(dp, dof) = sc;
       if (p.k_sf) {
-        *reinterpret_cast<uint2*>(p.k_sf + sf_off(dp, dof)) = fk;
-        *reinterpret_cast<uint2*>(p.v_sf + sf_off(dp, dof)) = fv;
+        if (with_k) fk = *reinterpret_cast<const uint2*>(p.k_sf + sf_off(sp, sof));
+        if (with_v) fv = *reinterpret_cast<const uint2*>(p.v_sf + sf_off(sp, sof));
       }
     }
-  }
-  const int64_t items = (int64_t)R << item_shift;
-  for (int64_t x0 = 0; x0 < items; x0 += (int64_t)gstride * kUnroll) {
+    __syncthreads();
+    const int items = mine << item_shift;
     uint4 v[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int64_t x = x0 + gtid + (int64_t)u * gstride;
-      if (x < items) {
-        int page, off;
-        place_of(tail + (int)(x >> item_shift), page, off);
-        v[u] = *chunk_ptr(page, off, (int)(x & (2 * rc - 1)));
+      const int x = tid + u * THREADS;
+      if (x < items) v[u] = *chunk_ptr(sh.place[x >> item_shift].y, x & (cols - 1));
+    }
+    if (overlap) unit_sync();
+    if (tid < mine) {
+      if (with_k) *score_at(dp, dof) = sc;
+      if (p.k_sf) {
+        if (with_k) *reinterpret_cast<uint2*>(p.k_sf + sf_off(dp, dof)) = fk;
+        if (with_v) *reinterpret_cast<uint2*>(p.v_sf + sf_off(dp, dof)) = fv;
       }
     }
-    if (overlap) cluster.sync();
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int64_t x = x0 + gtid + (int64_t)u * gstride;
-      if (x < items) {
-        int page, off;
-        place_of(front + (int)(x >> item_shift), page, off);
-        *chunk_ptr(page, off, (int)(x & (2 * rc - 1))) = v[u];
-      }
+      const int x = tid + u * THREADS;
+      if (x < items) *chunk_ptr(sh.place[x >> item_shift].x, x & (cols - 1)) = v[u];
     }
+    __syncthreads();  // the list is rewritten by the next tile
   }
-  cluster.sync();  // no CTA leaves while another may still read its shared memory
+  if constexpr (SLICED) cluster.sync();  // no CTA leaves while another may still read its shared memory
 }
 
-}  // namespace
+// Clusters of c CTAs of the sliced form (one CTA per SM) that the device runs at once.  Not SMs / c: a
+// cluster lives within one GPC (16 clusters of 8 were one too many for this part: the last one ran alone,
+// 79 us instead of 41 for 2 x 131072 keys and 8 KV heads).
+cudaError_t clusters_at_once(int dev, int c, int64_t* out) {
+  static std::atomic<int> known[64][kMaxCluster + 1];  // 0: not asked yet, else the answer + 1
+  int v = dev >= 0 && dev < 64 ? known[dev][c].load(std::memory_order_relaxed) : 0;
+  if (v == 0) {
+    cudaError_t e = cudaFuncSetAttribute(evict_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)c);
+    cfg.blockDim = dim3(Form<true>::THREADS);
+    cfg.dynamicSmemBytes = sizeof(typename Form<true>::Shared) + (size_t)kMaxKeys * 4 + (size_t)kMaxKeys / 32 * 12;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)c;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, evict_kernel<true>, &cfg);
+    if (e != cudaSuccess) return e;
+    v = n + 1;
+    if (dev >= 0 && dev < 64) known[dev][c].store(v, std::memory_order_relaxed);
+  }
+  *out = v - 1;
+  return cudaSuccess;
+}
 
-cudaError_t launch_evict(const EvictParams& p, int32_t batch, int32_t max_len, int num_sms, cudaStream_t s) {
-  const int64_t units = (int64_t)batch * p.num_kv_heads;
-  // CTAs per unit: enough to cover the longest request, then doubled while there are SMs without a
-  // CTA and slices longer than 1024 positions
-  int C = 1;
-  while (C < kMaxCluster && (max_len + C - 1) / C > kMaxSlice) C *= 2;
-  while (C < kMaxCluster && units * C * 2 <= 2 * (int64_t)num_sms && max_len / C > 1024) C *= 2;
+template <bool SLICED>
+cudaError_t launch_form(const EvictParams& p, int64_t units, int C, int slice_cap, int key_cap, cudaStream_t s) {
+  using F = Form<SLICED>;
   if (units * C > INT32_MAX) return cudaErrorInvalidValue;
-  const int slice_cap = ((max_len + C - 1) / C + 31) / 32 * 32;
-  const int key_cap = slice_cap <= kMaxKeys ? slice_cap : 0;
-  const size_t smem = sizeof(Shared) + (size_t)slice_cap / 32 * 12 + (size_t)key_cap * 4;
   static bool attr_set[64] = {false};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev >= 0 && dev < 64 && !attr_set[dev]) {
-    e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+    e = cudaFuncSetAttribute(evict_kernel<SLICED>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
     if (e != cudaSuccess) return e;
-    attr_set[dev] = true;
+    if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(units * C));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.blockDim = dim3(F::THREADS);
+  cfg.dynamicSmemBytes = sizeof(typename F::Shared) + (size_t)slice_cap / 32 * 12 + (size_t)key_cap * 4;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -424,7 +583,33 @@ cudaError_t launch_evict(const EvictParams& p, int32_t batch, int32_t max_len, i
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, evict_kernel, p, slice_cap, key_cap);
+  return cudaLaunchKernelEx(&cfg, evict_kernel<SLICED>, p, slice_cap, key_cap);
+}
+
+}  // namespace
+
+cudaError_t launch_evict(const EvictParams& p, int32_t batch, int32_t num_long, int32_t max_len, int num_sms, cudaStream_t s) {
+  const int64_t units = (int64_t)batch * p.num_kv_heads, busy = (int64_t)num_long * p.num_kv_heads;
+  int C = 1;
+  if (max_len <= kMaxWhole) {
+    // K and V to two CTAs while these are resident at once
+    if (busy * 2 <= Form<false>::CTAS * (int64_t)num_sms) C = 2;
+    const int cap = (max_len + 31) / 32 * 32;
+    return launch_form<false>(p, units, C, cap, cap, s);
+  }
+  // slices: enough to cover the longest request, then as many as let all busy units run at once
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  while ((max_len + C - 1) / C > kMaxSlice) ++C;
+  for (int c = kMaxCluster; c > C; --c) {
+    int64_t at_once = 0;
+    e = clusters_at_once(dev, c, &at_once);
+    if (e != cudaSuccess) return e;
+    if (busy <= at_once) C = c;
+  }
+  const int slice_cap = ((max_len + C - 1) / C + 31) / 32 * 32;
+  return launch_form<true>(p, units, C, slice_cap, slice_cap <= kMaxKeys ? slice_cap : 0, s);
 }
 
 }  // namespace pkv

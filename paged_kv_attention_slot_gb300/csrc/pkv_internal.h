@@ -135,7 +135,8 @@ struct EvictParams {
   int32_t row_chunks;  // 16-byte chunks of one K (or V) row
   int32_t budget, num_sink, num_recent;
 };
-cudaError_t launch_evict(const EvictParams& p, int32_t batch, int32_t max_len, int num_sms, cudaStream_t s);
+// num_long requests are longer than the budget, the longest has max_len keys
+cudaError_t launch_evict(const EvictParams& p, int32_t batch, int32_t num_long, int32_t max_len, int num_sms, cudaStream_t s);
 constexpr int32_t kEvictMaxLen = 1 << 21;  // longest request the eviction kernel's shared memory covers
 cudaError_t launch_decode(const RunParams& p, int kv_dtype, cudaStream_t s);
 cudaError_t launch_decode_scored(const RunParams& p, int kv_dtype, cudaStream_t s);  // decode and the score update
