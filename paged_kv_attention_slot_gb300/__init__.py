@@ -132,9 +132,14 @@ class KVCache:
         self.k_scale, self.v_scale = float(k_scale), float(v_scale)
         self.k_sf, self.v_sf = k_sf, v_sf
         self.dtype = dtype
+        P, ps, H, w = k.shape
+        self._geometry = (P, ps, H, w if k_sf is None else 2 * w)
+        self._score_shape = (P, H, ps)
+        self._device = k.device
+        self._device_index = k.get_device()  # -1: the host
         sf = (None, None, 0, 0, 0) if k_sf is None else (k_sf.data_ptr(), v_sf.data_ptr(), *k_sf.stride()[:3])
         self.struct = _lib.pkv_cache(
-            k.data_ptr(), v.data_ptr(), k.shape[0], k.shape[1], k.shape[2], self.head_dim, dtype,
+            k.data_ptr(), v.data_ptr(), *self._geometry, dtype,
             k.stride(0), k.stride(1), k.stride(2), self.k_scale, self.v_scale, *sf)
 
     @classmethod
@@ -151,30 +156,30 @@ class KVCache:
 
     @property
     def num_pages(self):
-        return self.k.shape[0]
+        return self._geometry[0]
 
     @property
     def page_size(self):
-        return self.k.shape[1]
+        return self._geometry[1]
 
     @property
     def num_kv_heads(self):
-        return self.k.shape[2]
+        return self._geometry[2]
 
     @property
     def head_dim(self):
-        return self.k.shape[3] if self.k_sf is None else 2 * self.k.shape[3]
+        return self._geometry[3]
 
 
-def _check_device(t: torch.Tensor, name: str) -> None:
+def _check_device(cache: "KVCache") -> None:
     """The library launches on the current device."""
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} must be on the current CUDA device, not on {t.device}")
+    if cache._device_index < 0 or cache._device_index != torch.cuda.current_device():
+        raise ValueError(f"the cache must be on the current CUDA device, not on {cache.k.device}")
 
 
 def _new(shape, dtype, device, stream) -> torch.Tensor:
     """An output tensor whose memory belongs to the stream that will write it."""
-    if isinstance(stream, torch.cuda.Stream):
+    if stream is not None and isinstance(stream, torch.cuda.Stream):
         with torch.cuda.stream(stream):
             return torch.empty(shape, dtype=dtype, device=device)
     return torch.empty(shape, dtype=dtype, device=device)
@@ -184,12 +189,11 @@ def _check_scores(scores: torch.Tensor, cache: KVCache) -> int:
     """Address of an accumulated-weight tensor of the cache's slots."""
     if scores.dtype != torch.float32 or not scores.is_contiguous():
         raise ValueError("scores must be a contiguous float32 tensor")
-    if tuple(scores.shape) != (cache.num_pages, cache.num_kv_heads, cache.page_size):
-        raise ValueError(f"scores must be [{cache.num_pages}, {cache.num_kv_heads}, {cache.page_size}]: "
-                         "[num_pages, num_kv_heads, page_size]")
-    if scores.device != cache.k.device:
+    if scores.shape != cache._score_shape:
+        raise ValueError(f"scores must be {list(cache._score_shape)}: [num_pages, num_kv_heads, page_size]")
+    if scores.get_device() != cache._device_index:
         raise ValueError("scores must be on the cache's device")
-    _check_device(scores, "scores")
+    _check_device(cache)
     return scores.data_ptr()
 
 
@@ -206,12 +210,13 @@ def kv_store(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor, cache
     if slot_mapping.dtype != torch.int64:
         raise ValueError("slot_mapping must be int64")
     T = k.shape[0]
-    if v.shape != k.shape or slot_mapping.shape[0] != T or tuple(k.shape[1:]) != (cache.num_kv_heads, cache.head_dim):
+    if v.shape != k.shape or slot_mapping.shape[0] != T or k.shape[1:] != cache._geometry[2:]:
         raise ValueError("shape mismatch between k, v, slot_mapping and the cache")
     if scores is not None or cache.dtype == _lib.PKV_NVFP4:
-        if any(t.device != cache.k.device for t in (k, v, slot_mapping)):
+        d = cache._device_index
+        if k.get_device() != d or v.get_device() != d or slot_mapping.get_device() != d:
             raise ValueError("k, v and slot_mapping must be on the cache's device")
-        _check_device(cache.k, "the cache")
+        _check_device(cache)
     if scores is not None:
         check(lib().pkv_kv_store_scored(k.data_ptr(), v.data_ptr(), slot_mapping.data_ptr(), T, C.byref(cache.struct),
                                         _check_scores(scores, cache), _stream_ptr(stream)))
@@ -228,19 +233,18 @@ def kv_load(slot_mapping: torch.Tensor, cache: KVCache, k: torch.Tensor | None =
     attend to it with a "ragged" plan.  A negative slot gives a row of zeros.  Returns (k, v)."""
     if slot_mapping.dtype != torch.int64 or slot_mapping.dim() != 1 or not slot_mapping.is_contiguous():
         raise ValueError("slot_mapping must be a contiguous one-dimensional int64 tensor")
-    if slot_mapping.device != cache.k.device:
+    if slot_mapping.get_device() != cache._device_index:
         raise ValueError("slot_mapping must be on the cache's device")
-    shape = (slot_mapping.shape[0], cache.num_kv_heads, cache.head_dim)
-    for name, t in (("k", k), ("v", v)):
-        if t is None:
-            continue
-        if t.dtype != torch.bfloat16 or not t.is_contiguous() or tuple(t.shape) != shape or t.device != cache.k.device:
-            raise ValueError(f"{name} must be a contiguous bf16 tensor {list(shape)} on the cache's device")
-    _check_device(cache.k, "the cache")
+    shape = (slot_mapping.shape[0], *cache._geometry[2:])
+    for t in (k, v):
+        if t is not None and (t.dtype != torch.bfloat16 or not t.is_contiguous() or t.shape != shape
+                              or t.get_device() != cache._device_index):
+            raise ValueError(f"k and v must be contiguous bf16 tensors {list(shape)} on the cache's device")
+    _check_device(cache)
     if k is None:
-        k = _new(shape, torch.bfloat16, cache.k.device, stream)
+        k = _new(shape, torch.bfloat16, cache._device, stream)
     if v is None:
-        v = _new(shape, torch.bfloat16, cache.k.device, stream)
+        v = _new(shape, torch.bfloat16, cache._device, stream)
     check(lib().pkv_kv_load(slot_mapping.data_ptr(), shape[0], C.byref(cache.struct), k.data_ptr(), v.data_ptr(),
                             _stream_ptr(stream)))
     return k, v
@@ -374,7 +378,7 @@ class Plan:
     def _outputs(self, q, out, lse, return_lse):
         if q.dtype != torch.bfloat16 or not q.is_contiguous():
             raise ValueError("q must be a contiguous bf16 tensor")
-        if tuple(q.shape) != (self.total_tokens, self.num_qo_heads, self.head_dim):
+        if q.shape != (self.total_tokens, self.num_qo_heads, self.head_dim):
             raise ValueError(f"q must be [{self.total_tokens}, {self.num_qo_heads}, {self.head_dim}]")
         if out is None:
             out = torch.empty_like(q)
@@ -434,7 +438,7 @@ class Plan:
             if not self.scored or merge_into:
                 raise ValueError("scores need a plan made with scored=True (decode or mixed) and no merge_into")
             addr = _check_scores(scores, cache)
-            if self.scratch is None or q.device != scores.device:
+            if self.scratch is None or q.get_device() != cache._device_index:
                 raise ValueError("a scored run needs a plan with a workspace and q on the cache's device")
         if merge_into:
             if self.mode not in ("prefill", "extend") or out is None or lse is None:
@@ -484,9 +488,9 @@ class Plan:
                              "num_sink + num_recent <= budget")
         shape = (self.batch_size, cache.num_kv_heads, budget)
         if kept is None:
-            kept = _new(shape, torch.int32, scores.device, stream)
-        elif (kept.dtype != torch.int32 or not kept.is_contiguous() or tuple(kept.shape) != shape
-              or kept.device != scores.device):
+            kept = _new(shape, torch.int32, cache._device, stream)
+        elif (kept.dtype != torch.int32 or not kept.is_contiguous() or kept.shape != shape
+              or kept.get_device() != cache._device_index):
             raise ValueError(f"kept must be a contiguous int32 tensor {list(shape)} on the cache's device")
         check(lib().pkv_kv_evict(self._h, C.byref(cache.struct), addr, budget, num_sink, num_recent, kept.data_ptr(),
                                  _stream_ptr(stream)))

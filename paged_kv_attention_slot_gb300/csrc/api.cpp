@@ -956,7 +956,7 @@ int pkv_attn_decode_run_scored(const pkv_plan* plan, const void* q, const pkv_ca
   p.logits = (float*)scratch;
   p.lse2 = (float*)((char*)scratch + pkv::scored_lse_offset(plan));
   p.scores = scores;
-  PKV_CUDA(pkv::launch_decode_scored(p, cache->dtype, (cudaStream_t)stream), "scored decode launch");
+  PKV_CUDA(pkv::launch_decode_scored(p, cache->dtype, plan->num_decode_merge > 0, (cudaStream_t)stream), "scored decode launch");
   return PKV_OK;
 }
 

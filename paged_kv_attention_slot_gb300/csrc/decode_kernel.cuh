@@ -67,6 +67,127 @@ __device__ __forceinline__ void cp_async16_pol(uint32_t dst, const void* src, ui
                : "memory");
 }
 
+// ---- accumulated attention weights (scored runs) ----
+// The weight of key j for KV head h, a_j = sum over its query heads g of 2^(x_gj - lse_g) (x: the scaled
+// scores in log2 units, [key][query head] at lg0), is added to scores[slot(j), h] for the keys
+// [lo, hi) of a unit.  The additions are reductions at L2, so no thread waits for a score's old value;
+// every score gets one per launch, so their order does not matter.  A thread takes four neighbouring keys
+// (of one page: one page id, one 16-byte reduction) where pages and scores allow it, UNROLL times in flight.
+// The page ids may be read at once; `ready` is called before the first look at lg0 and lse.
+template <int UNROLL, typename Ready>
+__device__ __forceinline__ void add_weights(const RunParams& p, const WorkItem& w, const float* lg0, const float* lse, int lo,
+                                            int hi, int tid, int threads, Ready ready) {
+  const int G = p.group, ps = p.page_size;
+  const int ps_shift = (ps & (ps - 1)) == 0 ? __ffs(ps) - 1 : -1;
+  const int32_t* pages = p.kv_indices + w.page_base;
+  auto score_at = [&](int page, int off) -> float* {
+    return p.scores + ((int64_t)page * p.num_kv_heads + w.kv_head) * ps + off;
+  };
+  auto in_pool = [&](int page) {  // (a page outside was recorded where its rows were read)
+    return (unsigned long long)(unsigned)page < (unsigned long long)p.num_pages;
+  };
+  bool waited = false;
+  if ((ps & 3) == 0 && (reinterpret_cast<uintptr_t>(p.scores) & 15) == 0) {
+    for (int base = lo & ~3; base < hi; base += 4 * UNROLL * threads) {  // block-uniform
+      int page[UNROLL], off[UNROLL];
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u) {
+        const int key = base + 4 * (tid + u * threads);
+        page[u] = -1;
+        off[u] = 0;
+        if (key < hi) {
+          const int pg = ps_shift >= 0 ? key >> ps_shift : key / ps;
+          page[u] = __ldg(pages + pg);
+          off[u] = key - pg * ps;
+        }
+      }
+      if (!waited) ready();
+      waited = true;
+      float a[UNROLL][4];
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u) a[u][0] = a[u][1] = a[u][2] = a[u][3] = 0.f;
+      // (a score outside [lo, hi) was not computed and is not read)
+      if ((G & 3) == 0) {
+        for (int g = 0; g < G; g += 4) {
+          float4 x[UNROLL][4];
+#pragma unroll
+          for (int u = 0; u < UNROLL; ++u)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int key = base + 4 * (tid + u * threads) + k;
+              x[u][k] = key >= lo && key < hi ? *reinterpret_cast<const float4*>(lg0 + (int64_t)key * G + g)
+                                              : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            }
+          const float l0 = lse[g], l1 = lse[g + 1], l2 = lse[g + 2], l3 = lse[g + 3];
+#pragma unroll
+          for (int u = 0; u < UNROLL; ++u)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              a[u][k] += (ex2(x[u][k].x - l0) + ex2(x[u][k].y - l1)) + (ex2(x[u][k].z - l2) + ex2(x[u][k].w - l3));
+        }
+      } else {
+        for (int g = 0; g < G; ++g) {
+          const float l0 = lse[g];
+#pragma unroll
+          for (int u = 0; u < UNROLL; ++u)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int key = base + 4 * (tid + u * threads) + k;
+              if (key >= lo && key < hi) a[u][k] += ex2(lg0[(int64_t)key * G + g] - l0);
+            }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u) {
+        const int key = base + 4 * (tid + u * threads);
+        if (key >= hi || !in_pool(page[u])) continue;
+        float* at = score_at(page[u], off[u]);
+        if (key >= lo && key + 4 <= hi) {
+          red_add_v4(at, a[u][0], a[u][1], a[u][2], a[u][3]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (key + k >= lo && key + k < hi) red_add(at + k, a[u][k]);
+        }
+      }
+    }
+    return;
+  }
+  constexpr int KU = 4;  // odd page sizes: single keys, four in flight
+  for (int base = lo; base < hi; base += KU * threads) {  // block-uniform
+    int page[KU], off[KU];
+#pragma unroll
+    for (int u = 0; u < KU; ++u) {
+      const int key = base + tid + u * threads;
+      page[u] = -1;
+      off[u] = 0;
+      if (key < hi) {
+        const int pg = ps_shift >= 0 ? key >> ps_shift : key / ps;
+        page[u] = __ldg(pages + pg);
+        off[u] = key - pg * ps;
+      }
+    }
+    if (!waited) ready();
+    waited = true;
+    float a[KU] = {0.f, 0.f, 0.f, 0.f};
+    for (int g = 0; g < G; ++g) {
+      const float l0 = lse[g];
+#pragma unroll
+      for (int u = 0; u < KU; ++u) {
+        const int key = base + tid + u * threads;
+        if (key < hi) a[u] += ex2(lg0[(int64_t)key * G + g] - l0);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < KU; ++u)
+      if (base + tid + u * threads < hi && in_pool(page[u])) red_add(score_at(page[u], off[u]), a[u]);
+  }
+}
+// Scores of the unit of work item w.
+__device__ __forceinline__ float* unit_logits(const RunParams& p, const WorkItem& w) {
+  return p.logits + (int64_t)w.page_base * p.page_size * p.num_qo_heads + (int64_t)w.kv_head * w.kv_end * p.group;
+}
+
 // KV: the pool's pkv_dtype; NB: 8-column n-blocks; HPB: query heads per n-block, 8 or, for NVFP4, 4 in
 // "pair" form (every head in two neighbouring columns, see the V product in the kernel).
 template <int D, int KV, int NB, int HPB = 8>
@@ -388,8 +509,7 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB, HPB>::CTAS) decode_k
   float* logits = nullptr;
   const bool pair_rows = (p.group & 1) == 0;
   if constexpr (SCORED)
-    logits = p.logits + (int64_t)w.page_base * ps * p.num_qo_heads +
-             (int64_t)w.kv_head * w.kv_end * p.group + w.head_group * kDecodeRows;
+    logits = unit_logits(p, w) + w.head_group * kDecodeRows;
 
   int stage = 0, fill = C::STAGES - 1;  // ring slot of the tile computed now and of the one loaded now
   while (true) {
@@ -756,8 +876,13 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB, HPB>::CTAS) decode_k
     }
     if (p.lse && threadIdx.x < rows)
       p.lse[(int64_t)w.q_row * p.num_qo_heads + qh0 + threadIdx.x] = s_lse2[threadIdx.x] * 0.69314718055994531f;
-    if constexpr (SCORED)
-      if (threadIdx.x < rows) p.lse2[(int64_t)w.q_row * p.num_qo_heads + qh0 + threadIdx.x] = s_lse2[threadIdx.x];
+    if constexpr (SCORED) {
+      if (p.group > kDecodeRows) {  // other CTAs hold the other query heads' sums: score_add_kernel
+        if (threadIdx.x < rows) p.lse2[(int64_t)w.q_row * p.num_qo_heads + qh0 + threadIdx.x] = s_lse2[threadIdx.x];
+      } else {  // every score of this unit was written by this CTA
+        add_weights<(C::CTAS >= 4 ? 2 : 4)>(p, w, unit_logits(p, w), s_lse2, w.kv_begin, w.kv_end, threadIdx.x, 128, [] {});
+      }
+    }
   } else {
     float* po = p.part_o + (int64_t)w.out_slot * kDecodeRows * D;
     for (int idx = threadIdx.x; idx < rows * D; idx += blockDim.x) {

@@ -139,7 +139,8 @@ struct EvictParams {
 cudaError_t launch_evict(const EvictParams& p, int32_t batch, int32_t num_long, int32_t max_len, int num_sms, cudaStream_t s);
 constexpr int32_t kEvictMaxLen = 1 << 21;  // longest request the eviction kernel's shared memory covers
 cudaError_t launch_decode(const RunParams& p, int kv_dtype, cudaStream_t s);
-cudaError_t launch_decode_scored(const RunParams& p, int kv_dtype, cudaStream_t s);  // decode and the score update
+// decode and the score update; any_split: some unit is shared by several CTAs
+cudaError_t launch_decode_scored(const RunParams& p, int kv_dtype, bool any_split, cudaStream_t s);
 int decode_ctas_per_sm(int kv_dtype, int head_dim, int group);  // resident decode CTAs per SM
 cudaError_t launch_prefill(const RunParams& p, const void* tmap_q, const void* tmap_o, int64_t total_tokens,
                            cudaStream_t s);
