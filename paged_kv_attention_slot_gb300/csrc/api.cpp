@@ -846,6 +846,13 @@ int check_pool(const pkv_cache* cache) {
   return check_scales(cache);
 }
 
+// The NVFP4 write and the read back index pages and rows with 32 bits.
+int check_indices(const pkv_cache* cache) {
+  if (cache->num_pages > INT32_MAX) return fail(PKV_EUNSUPPORTED, "num_pages must be below 2^31");
+  if (cache->num_kv_heads > 65536) return fail(PKV_EUNSUPPORTED, "num_kv_heads must be at most 65536");
+  return PKV_OK;
+}
+
 int kv_store(const void* k, const void* v, const int64_t* slot_mapping, int64_t num_tokens, const pkv_cache* cache,
              float* scores, void* stream) {
   if (num_tokens < 0) return fail(PKV_EINVAL, "num_tokens < 0");
@@ -853,6 +860,7 @@ int kv_store(const void* k, const void* v, const int64_t* slot_mapping, int64_t 
   if (num_tokens == 0) return PKV_OK;
   if (!k || !v || !slot_mapping || !cache->k || !cache->v) return fail(PKV_EINVAL, "NULL pointer argument");
   int st = check_pool(cache);
+  if (st == PKV_OK && cache->dtype == PKV_NVFP4) st = check_indices(cache);
   if (st != PKV_OK) return st;
   if (((uintptr_t)k | (uintptr_t)v) & 15) return fail(PKV_EINVAL, "k and v must be 16-byte aligned");
   if ((uintptr_t)scores & 3) return fail(PKV_EINVAL, "scores must be 4-byte aligned");
@@ -912,6 +920,7 @@ int pkv_kv_load(const int64_t* slot_mapping, int64_t num_tokens, const pkv_cache
   if (num_tokens == 0) return PKV_OK;
   if (!k || !v || !slot_mapping || !cache->k || !cache->v) return fail(PKV_EINVAL, "NULL pointer argument");
   int st = check_pool(cache);
+  if (st == PKV_OK) st = check_indices(cache);
   if (st != PKV_OK) return st;
   if (((uintptr_t)k | (uintptr_t)v) & 15) return fail(PKV_EINVAL, "k and v must be 16-byte aligned");
   PKV_CUDA(pkv::launch_kv_load(slot_mapping, num_tokens, *cache, k, v, (cudaStream_t)stream), "kv_load launch");

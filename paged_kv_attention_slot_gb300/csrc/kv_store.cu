@@ -10,7 +10,7 @@
 // chunks, so a warp writes two full rows and every global access is a full 16-byte vector.  The
 // kernel is a pure memory op; it is launched with enough CTAs to cover every chunk once.  An NVFP4 pool
 // takes one thread per 16-element block instead (two chunks in, one scale and 8 code bytes out).
-// kv_load is the way back: one thread per 8 (bf16, FP8) or 16 (NVFP4) elements of a row, widened and
+// kv_load is the way back: one thread per 8 elements of a row (one 16-byte vector out), widened and
 // rounded to bf16.
 
 #include <algorithm>
@@ -120,72 +120,102 @@ struct Fp4Pools {
   int64_t sp_b, st_b, sh_b;  // strides of the scale pools in bytes
 };
 
-// Quotient t / s rounded to nearest (r = 1/s rounded): one Newton step on the quotient (Markstein's
-// correction).  |t| <= 2688 * 2^7 and s is an E4M3 value (2^-9 .. 448), so nothing over- or underflows
-// where the code is not 0 anyway.
-__device__ __forceinline__ float div_rn(float t, float s, float r) {
-  const float q = t * r;
-  return fmaf(fmaf(-q, s, t), r, q);
+// Quotients rounded to nearest without a division: q = t r with r = 1 / s rounded, then one Newton step on
+// the quotient (Markstein's correction), two quotients at a time.  The caller keeps t / s away from over-
+// and underflow.
+__device__ __forceinline__ uint64_t div2_rn(uint64_t t2, uint64_t minus_s2, uint64_t r2) {
+  const uint64_t q2 = fmul2(t2, r2);
+  return ffma2(ffma2(q2, minus_s2, t2), r2, q2);
 }
 
-// One block of 16 bf16 values (two 16-byte vectors) to its E4M3 scale code and 8 bytes of E2M1 codes.
-__device__ __forceinline__ uint2 quant_block(const uint4 a, const uint4 b, float inv, uint32_t& sf) {
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  float t[16];
-  float amax = 0.f;
-  bool nan = false;
+// The 16 codes of a block of bf16 pairs w under the block scale s (r = 1 / s rounded).  CLAMP: values may be
+// beyond 2688 = 6 * 448, where the scale is 448 and the code 6, infinities included.
+template <bool CLAMP>
+__device__ __forceinline__ uint2 quant_codes(const uint32_t (&w)[8], float inv, float s, float r) {
+  const uint64_t inv2 = f2pack(inv, inv), r2 = f2pack(r, r), ms2 = f2pack(-s, -s);
+  uint32_t c[2];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    t[2 * j] = __uint_as_float(w[j] << 16) * inv;
-    t[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u) * inv;
-    amax = fmaxf(amax, fmaxf(fabsf(t[2 * j]), fabsf(t[2 * j + 1])));
-    nan = nan || t[2 * j] != t[2 * j] || t[2 * j + 1] != t[2 * j + 1];
-  }
-  sf = nan ? 0x7fu : f32x2_to_e4m3x2(__fdiv_rn(amax, 6.f), 0.f) & 0xffu;
-  if (nan || sf == 0) return make_uint2(0u, 0u);
-  const float s = e4m3_to_f32(sf);
-  const float r = __fdiv_rn(1.f, s);
-  uint32_t c[2] = {0u, 0u};
+  for (int v = 0; v < 2; ++v) {
+    float q[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    // beyond 2688 = 6 * 448 the scale is 448 and the code 6 for every value, infinities included
-    const float lo = div_rn(fminf(fmaxf(t[2 * j], -2688.f), 2688.f), s, r);
-    const float hi = div_rn(fminf(fmaxf(t[2 * j + 1], -2688.f), 2688.f), s, r);
-    c[j >> 2] |= f32x2_to_e2m1x2(lo, hi) << (8 * (j & 3));
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t x = w[4 * v + j];
+      uint64_t t2 = fmul2(f2pack(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)), inv2);
+      if constexpr (CLAMP) {
+        float lo, hi;
+        f2unpack(t2, lo, hi);
+        t2 = f2pack(fminf(fmaxf(lo, -2688.f), 2688.f), fminf(fmaxf(hi, -2688.f), 2688.f));
+      }
+      f2unpack(div2_rn(t2, ms2, r2), q[2 * j], q[2 * j + 1]);
+    }
+    c[v] = f32x8_to_e2m1x8(q);
   }
   return make_uint2(c[0], c[1]);
 }
 
+// One block of 16 bf16 values (two 16-byte vectors) to its E4M3 scale code and 8 bytes of E2M1 codes.
+// The largest magnitude is found on the bf16 bits (scaling is monotonic), two at a time; a NaN's are
+// above infinity's.
+__device__ __forceinline__ uint2 quant_block(const uint4 a, const uint4 b, float inv, uint32_t& sf) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t top = 0u;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) top = __vmaxu2(top, w[j] & 0x7fff7fffu);
+  top = max(top & 0xffffu, top >> 16);
+  const float amax = fminf(__uint_as_float(top << 16) * inv, 1e30f);  // (above 2688 the scale is 448 in any case)
+  const float sixth = 1.f / 6.f, q6 = amax * sixth;
+  sf = f32x2_to_e4m3x2(fmaf(fmaf(-q6, 6.f, amax), sixth, q6), 0.f) & 0xffu;
+  if (top > 0x7f80u) sf = 0x7fu;  // a NaN
+  if (sf == 0 || sf == 0x7fu) return make_uint2(0u, 0u);
+  // an E4M3 value's reciprocal is never near the middle of two floats, so one Newton step rounds it
+  const float s = e4m3_to_f32(sf), r0 = rcp_approx(s), r = fmaf(fmaf(-s, r0, 1.f), r0, r0);
+  if (amax > 1e6f) return quant_codes<true>(w, inv, s, r);
+  return quant_codes<false>(w, inv, s, r);
+}
+
+// Quotients by a number that is usually a power of two.
+struct Divider {
+  int32_t d, shift;  // shift >= 0: d == 1 << shift
+  __device__ __forceinline__ uint32_t div(uint32_t x) const { return shift >= 0 ? x >> shift : x / (uint32_t)d; }
+  __device__ __forceinline__ uint32_t div64(int64_t x) const {  // x >= 0, quotient below 2^32
+    if (shift >= 0) return (uint32_t)(x >> shift);
+    return x >> 32 ? (uint32_t)(x / d) : (uint32_t)x / (uint32_t)d;
+  }
+};
+Divider divider(int32_t d) {
+  int s = 0;
+  while ((1 << s) < d && s < 30) ++s;
+  return Divider{d, (1 << s) == d ? s : -1};
+}
+constexpr int64_t kMaxRows = (int64_t)1 << 26;  // (token, head) rows per launch: 32-bit indices
+
 // One thread per (token, head, block of 16): the 8 threads of a row write its 64 code bytes and, packed
-// four to a word by shuffles, its 8 scale bytes.
-__global__ void __launch_bounds__(256) kv_store_fp4_kernel(const StoreParams p, const Fp4Pools f) {
+// four to a word by shuffles, its 8 scale bytes.  The rows are read beside the slot, not after it.
+__global__ void __launch_bounds__(256) kv_store_fp4_kernel(const StoreParams p, const Fp4Pools f, const Divider heads,
+                                                           const Divider pages) {
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t n = p.T * p.heads * 8;  // a multiple of 8: the threads of a row stay together
-  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-    const unsigned row_mask = 0xffu << (threadIdx.x & 24);
-    const int64_t row = i >> 3;
-    const int c = (int)(i & 7);
-    const int64_t tok = row / p.heads;
-    const int h = (int)(row - tok * p.heads);
+  const uint32_t n = (uint32_t)(p.T * p.heads) * 8;  // a multiple of 8: the threads of a row stay together
+  const unsigned row_mask = 0xffu << (threadIdx.x & 24);
+  const int c = threadIdx.x & 7;
+  for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) {
+    const uint4* ks = reinterpret_cast<const uint4*>(p.k) + (int64_t)i * 2;
+    const uint4* vs = reinterpret_cast<const uint4*>(p.v) + (int64_t)i * 2;
+    const uint4 k0 = __ldg(ks), k1 = __ldg(ks + 1), v0 = __ldg(vs), v1 = __ldg(vs + 1);
+    const uint32_t row = i >> 3, tok = heads.div(row), h = row - tok * p.heads;
     const int64_t slot = __ldg(p.slots + tok);
     if (slot < 0) continue;  // padding token (all 8 threads of the row)
     if (slot >= p.total_slots) {
       record_error(p.err, PKV_DEVERR_SLOT_RANGE);
       continue;
     }
-    const int64_t page = slot / p.page_size;
-    const int64_t off = slot - page * p.page_size;
-    if (p.scores && c == 0) p.scores[(page * p.heads + h) * p.page_size + off] = 0.f;
-    const uint4* ks = reinterpret_cast<const uint4*>(p.k + row * 256 + c * 32);
-    const uint4* vs = reinterpret_cast<const uint4*>(p.v + row * 256 + c * 32);
-    const uint4 k0 = __ldg(ks), k1 = __ldg(ks + 1), v0 = __ldg(vs), v1 = __ldg(vs + 1);
-    uint32_t fk, fv;
-    const uint2 ck = quant_block(k0, k1, p.inv_k, fk);
-    const uint2 cv = quant_block(v0, v1, p.inv_v, fv);
+    const uint32_t page = pages.div64(slot);
+    const uint32_t off = (uint32_t)(slot - (int64_t)page * p.page_size);
+    if (p.scores && c == 0) p.scores[((int64_t)page * p.heads + h) * p.page_size + off] = 0.f;
     const int64_t dst = page * p.sp_b + off * p.st_b + h * p.sh_b + c * 8;
-    *reinterpret_cast<uint2*>(p.k_pool + dst) = ck;
-    *reinterpret_cast<uint2*>(p.v_pool + dst) = cv;
+    uint32_t fk, fv;
+    *reinterpret_cast<uint2*>(p.k_pool + dst) = quant_block(k0, k1, p.inv_k, fk);
+    *reinterpret_cast<uint2*>(p.v_pool + dst) = quant_block(v0, v1, p.inv_v, fv);
     fk <<= 8 * (c & 3);
     fv <<= 8 * (c & 3);
 #pragma unroll
@@ -212,84 +242,92 @@ struct LoadParams {
   uint4* v;
   int64_t T, total_slots;
   int64_t sp_b, st_b, sh_b, fp_b, ft_b, fh_b;
-  int32_t page_size, heads, units;  // units: threads per (token, head) row
+  int32_t page_size, heads, unit_shift;  // 1 << unit_shift 16-byte vectors of a bf16 row
   float k_scale, v_scale;
+  Divider by_heads, by_page;
   int32_t* err;
 };
 
+// Eight elements (unit c) of the row at byte offset `at` (block scales at `sat`) as one vector of bf16.
 template <int KV>
-__device__ __forceinline__ void load_unit(const uint8_t* pool, const uint8_t* sf, int64_t at, int64_t sat, int c, float scale,
-                                          uint4* out) {
+__device__ __forceinline__ uint4 load_unit(const uint8_t* pool, const uint8_t* sf, int64_t at, int64_t sat, int c, float scale) {
   if constexpr (KV == PKV_BF16) {
-    out[0] = __ldg(reinterpret_cast<const uint4*>(pool + at + c * 16));
+    return __ldg(reinterpret_cast<const uint4*>(pool + at + c * 16));
   } else {
-    // 8 code bytes: 8 E4M3 values, or 16 E2M1 values under one block scale
-    const uint2 x = __ldg(reinterpret_cast<const uint2*>(pool + at + c * 8));
-    uint32_t h[8];
-    float f = scale;
+    uint32_t h[4];
+    float s = 1.f;
     if constexpr (KV == PKV_NVFP4) {
       // code * block scale has 6 significant bits; the tensor's scale is the first rounding, bf16 the last
-      const float s = e4m3_to_f32(__ldg(sf + sat + c));
-      uint32_t a[4], b[4];
-      e2m1x8_to_f16x2x4(x.x, a);
-      e2m1x8_to_f16x2x4(x.y, b);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        h[j] = a[j];
-        h[4 + j] = b[j];
-      }
-      uint32_t r[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float2 y = f16x2_to_f32x2(h[j]);
-        r[j] = pack_bf16(y.x * s * f, y.y * s * f);
-      }
-      out[0] = make_uint4(r[0], r[1], r[2], r[3]);
-      out[1] = make_uint4(r[4], r[5], r[6], r[7]);
+      s = e4m3_to_f32(__ldg(sf + sat + (c >> 1)));
+      e2m1x8_to_f16x2x4(__ldg(reinterpret_cast<const uint32_t*>(pool + at + c * 4)), h);
     } else {
+      const uint2 x = __ldg(reinterpret_cast<const uint2*>(pool + at + c * 8));
       e4m3x4_to_f16x2x2(x.x, h[0], h[1]);
       e4m3x4_to_f16x2x2(x.y, h[2], h[3]);
-      uint32_t r[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 y = f16x2_to_f32x2(h[j]);
-        r[j] = pack_bf16(y.x * f, y.y * f);
-      }
-      out[0] = make_uint4(r[0], r[1], r[2], r[3]);
     }
+    uint32_t r[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 y = f16x2_to_f32x2(h[j]);
+      r[j] = KV == PKV_NVFP4 ? pack_bf16(y.x * s * scale, y.y * s * scale) : pack_bf16(y.x * scale, y.y * scale);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
   }
 }
 
 template <int KV>
 __global__ void __launch_bounds__(256) kv_load_kernel(const LoadParams p) {
-  constexpr int OUT = KV == PKV_NVFP4 ? 2 : 1;  // 16-byte vectors written per thread and tensor
+  constexpr int U = 2;  // units in flight per thread
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t n = p.T * p.heads * p.units;
-  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t row = i / p.units;
-    const int c = (int)(i - row * p.units);
-    const int64_t tok = row / p.heads;
-    const int h = (int)(row - tok * p.heads);
-    const int64_t slot = __ldg(p.slots + tok);
-    uint4 ko[2], vo[2];
-    ko[0] = ko[1] = vo[0] = vo[1] = make_uint4(0u, 0u, 0u, 0u);
-    if (slot >= p.total_slots) {
-      record_error(p.err, PKV_DEVERR_SLOT_RANGE);
-    } else if (slot >= 0) {
-      const int64_t page = slot / p.page_size;
-      const int64_t off = slot - page * p.page_size;
-      const int64_t at = page * p.sp_b + off * p.st_b + h * p.sh_b;
-      const int64_t sat = page * p.fp_b + off * p.ft_b + h * p.fh_b;
-      load_unit<KV>(p.k_pool, p.k_sf, at, sat, c, p.k_scale, ko);
-      load_unit<KV>(p.v_pool, p.v_sf, at, sat, c, p.v_scale, vo);
+  const uint32_t n = (uint32_t)(p.T * p.heads) << p.unit_shift, step = gridDim.x * 256;
+  const int c = threadIdx.x & ((1 << p.unit_shift) - 1);
+  for (uint32_t i0 = blockIdx.x * 256 + threadIdx.x; i0 < n; i0 += U * step) {
+    int64_t slot[U];
+    uint32_t h[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t i = i0 + u * step;
+      slot[u] = -1;
+      h[u] = 0;
+      if (i < n) {
+        const uint32_t row = i >> p.unit_shift, tok = p.by_heads.div(row);
+        h[u] = row - tok * p.heads;
+        slot[u] = __ldg(p.slots + tok);
+      }
+    }
+    uint4 ko[U], vo[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      ko[u] = vo[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (slot[u] >= p.total_slots) {
+        record_error(p.err, PKV_DEVERR_SLOT_RANGE);
+      } else if (slot[u] >= 0) {
+        const uint32_t page = p.by_page.div64(slot[u]);
+        const uint32_t off = (uint32_t)(slot[u] - (int64_t)page * p.page_size);
+        const int64_t at = page * p.sp_b + off * p.st_b + h[u] * p.sh_b;
+        const int64_t sat = KV == PKV_NVFP4 ? page * p.fp_b + off * p.ft_b + h[u] * p.fh_b : 0;
+        ko[u] = load_unit<KV>(p.k_pool, p.k_sf, at, sat, c, p.k_scale);
+        vo[u] = load_unit<KV>(p.v_pool, p.v_sf, at, sat, c, p.v_scale);
+      }
     }
 #pragma unroll
-    for (int j = 0; j < OUT; ++j) {
-      p.k[i * OUT + j] = ko[j];
-      p.v[i * OUT + j] = vo[j];
+    for (int u = 0; u < U; ++u) {
+      const uint32_t i = i0 + u * step;
+      if (i < n) {
+        p.k[i] = ko[u];
+        p.v[i] = vo[u];
+      }
     }
   }
+}
+
+static cudaError_t launch_kv_load_rows(const LoadParams& p, int dtype, cudaStream_t s) {
+  const int64_t blocks = std::min<int64_t>((((p.T * p.heads) << p.unit_shift) + 255) / 256, 152 * 8);
+  const dim3 g((unsigned)blocks), b(256);
+  if (dtype == PKV_NVFP4) return launch_pdl(kv_load_kernel<PKV_NVFP4>, g, b, 0, s, p);
+  if (dtype == PKV_FP8_E4M3) return launch_pdl(kv_load_kernel<PKV_FP8_E4M3>, g, b, 0, s, p);
+  return launch_pdl(kv_load_kernel<PKV_BF16>, g, b, 0, s, p);
 }
 
 cudaError_t launch_kv_load(const int64_t* slots, int64_t T, const pkv_cache& c, void* k, void* v, cudaStream_t s) {
@@ -315,16 +353,24 @@ cudaError_t launch_kv_load(const int64_t* slots, int64_t T, const pkv_cache& c, 
   }
   p.page_size = c.page_size;
   p.heads = c.num_kv_heads;
-  p.units = fp4 ? c.head_dim / 16 : c.head_dim / 8;
+  p.unit_shift = c.head_dim == 128 ? 4 : 3;
   p.k_scale = c.k_scale;
   p.v_scale = c.v_scale;
+  p.by_heads = divider(p.heads);
+  p.by_page = divider(p.page_size);
   p.err = device_error_ptr();
   if (!p.err) return cudaErrorInvalidDevice;
-  const int64_t blocks = std::min<int64_t>((T * p.heads * p.units + 255) / 256, 152 * 16);
-  const dim3 g((unsigned)blocks), b(256);
-  if (fp4) return launch_pdl(kv_load_kernel<PKV_NVFP4>, g, b, 0, s, p);
-  if (c.dtype == PKV_FP8_E4M3) return launch_pdl(kv_load_kernel<PKV_FP8_E4M3>, g, b, 0, s, p);
-  return launch_pdl(kv_load_kernel<PKV_BF16>, g, b, 0, s, p);
+  const int64_t most = kMaxRows / p.heads;  // tokens per launch (check_indices: at least one)
+  for (int64_t t0 = 0; t0 < T; t0 += most) {
+    LoadParams q = p;
+    q.slots = slots + t0;
+    q.T = std::min(most, T - t0);
+    q.k += (t0 * p.heads) << p.unit_shift;
+    q.v += (t0 * p.heads) << p.unit_shift;
+    const cudaError_t e = launch_kv_load_rows(q, c.dtype, s);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t launch_kv_store(const void* k, const void* v, const int64_t* slots, int64_t T, const pkv_cache& c,
@@ -357,7 +403,18 @@ cudaError_t launch_kv_store(const void* k, const void* v, const int64_t* slots, 
   if (fp4) {
     const Fp4Pools f{static_cast<uint8_t*>(c.k_sf), static_cast<uint8_t*>(c.v_sf), c.sf_stride_page, c.sf_stride_token,
                      c.sf_stride_head};
-    return launch_pdl(kv_store_fp4_kernel, dim3((unsigned)blocks), dim3(256), 0, s, p, f);
+    const int64_t most = kMaxRows / p.heads;  // tokens per launch (check_indices: at least one)
+    for (int64_t t0 = 0; t0 < T; t0 += most) {
+      StoreParams q = p;
+      q.slots = slots + t0;
+      q.T = std::min(most, T - t0);
+      q.k += t0 * p.heads * 256;
+      q.v += t0 * p.heads * 256;
+      const cudaError_t e = launch_pdl(kv_store_fp4_kernel, dim3((unsigned)blocks), dim3(256), 0, s, q, f, divider(p.heads),
+                                       divider(p.page_size));
+      if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
   }
   return fp8 ? launch_pdl(kv_store_kernel<true>, dim3((unsigned)blocks), dim3(256), 0, s, p)
              : launch_pdl(kv_store_kernel<false>, dim3((unsigned)blocks), dim3(256), 0, s, p);

@@ -140,12 +140,15 @@ __device__ __forceinline__ void e2m1_2x4_to_f16x2x4(uint32_t x, uint32_t (&out)[
       : "=r"(out[1]), "=r"(out[3])
       : "r"(odd));
 }
-// two floats to two E2M1 codes, round to nearest even, saturate to +-6; lo -> low nibble
-__device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
+// eight floats to eight E2M1 codes (nibble i = element i), round to nearest even, saturate to +-6
+__device__ __forceinline__ uint32_t f32x8_to_e2m1x8(const float (&x)[8]) {
   uint32_t r;
-  asm("{\n .reg .b8 t;\n cvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n cvt.u32.u8 %0, t;\n}\n"
+  asm("{\n .reg .b8 b0, b1, b2, b3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n"
+      " mov.b32 %0, {b0, b1, b2, b3};\n}\n"
       : "=r"(r)
-      : "f"(lo), "f"(hi));
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
   return r;
 }
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
@@ -178,6 +181,13 @@ __device__ __forceinline__ float2 f16x2_to_f32x2(uint32_t x) {
                      __half2float(__ushort_as_half((unsigned short)(x >> 16))));
 }
 
+// hardware reciprocal (MUFU), off by about one unit in the last place
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // hardware base-2 exponential (MUFU); ex2(-inf) = +0
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -197,6 +207,11 @@ __device__ __forceinline__ void f2unpack(uint64_t v, float& lo, float& hi) {
 __device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 __device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
