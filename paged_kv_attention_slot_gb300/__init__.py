@@ -53,6 +53,7 @@ def library_path() -> str:
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)  # CUDA is initialised where it is called
 
 
 def _stream_ptr(stream) -> int:
@@ -173,7 +174,7 @@ class KVCache:
 
 def _check_device(cache: "KVCache") -> None:
     """The library launches on the current device."""
-    if cache._device_index < 0 or cache._device_index != torch.cuda.current_device():
+    if cache._device_index < 0 or cache._device_index != _get_device():
         raise ValueError(f"the cache must be on the current CUDA device, not on {cache.k.device}")
 
 

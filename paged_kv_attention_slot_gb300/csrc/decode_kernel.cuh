@@ -486,7 +486,10 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB, HPB>::CTAS) decode_k
           amax = max(amax, max(r & 0x7fffu, (r >> 16) & 0x7fffu));
         }
     amax = __reduce_max_sync(0xffffffffu, amax);  // every warp holds the CTA's whole Q
-    const int e = max(0, (int)(amax >> 7) - 127 - 14);  // bf16 exponent field -> floor(log2 max |q|)
+    // (NVFP4: small rows are scaled up too, so that a small q against a pool of large scale keeps its
+    // bits; where the score scale underflows with it, the scores are 0 to float32 anyway)
+    const int top = (int)(amax >> 7) - 127 - 14;    // bf16 exponent field -> floor(log2 max |q|), less 14
+    const int e = FP4 ? max(-126, top) : max(0, top);
     const float down = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-e (e <= 114: a normal float)
     sc *= __uint_as_float((uint32_t)(127 + e) << 23);              // 2^e
 #pragma unroll

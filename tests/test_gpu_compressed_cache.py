@@ -299,6 +299,22 @@ def test_nvfp4_decode_of_large_queries():
     c.check(*c.plan().run(c.q, c.cache, return_lse=True))
 
 
+@pytest.mark.parametrize("power", [-24, -60, -100])
+def test_nvfp4_decode_of_small_queries(power):
+    # |q| far below f16's normal range against a pool of large scale: the scores stay moderate
+    c = Case([200, 90], 8, 2, 16, "nvfp4", seed=6, q_scale=2.0 ** power, k_scale=0.002)
+    c.cache.struct.k_scale = 0.002 * 2.0 ** -power
+    c.K = c.K * 2.0 ** -power
+    c.check(*c.plan().run(c.q, c.cache, return_lse=True))
+
+
+def test_nvfp4_decode_of_zero_queries_is_the_mean_of_v():
+    c = Case([40, 7], 8, 2, 16, "nvfp4", seed=6, q_scale=0.0)
+    out, lse = c.plan().run(c.q, c.cache, return_lse=True)
+    c.check(out, lse)
+    assert np.allclose(_np(lse), np.log([[40.0], [7.0]]), atol=1e-5)
+
+
 def test_nvfp4_decode_with_requests_without_new_tokens_and_empty_ones():
     c = Case([40, 0, 17, 64], 8, 2, 16, "nvfp4", q_lens=[1, 0, 0, 1], seed=8)
     out, lse = c.plan().run(c.q, c.cache, return_lse=True)
@@ -561,6 +577,87 @@ def test_evict_with_many_units_and_more_moves_than_one_list_holds():
     assert torch.equal(kept[0, 0].cpu(), torch.arange(b, L, dtype=torch.int32))
     assert torch.equal(scores.view(-1)[:b].cpu(), torch.arange(b, L, dtype=torch.float32))
     assert torch.equal(cache.k[:, :, 0, 0].reshape(-1)[:b].cpu().float(), (torch.arange(b, L) // 32).to(torch.bfloat16).float())
+
+
+SLICED = [
+    # lens, kv heads, page, budget, sink, recent: requests beyond the whole form's 12288 keys
+    ([20000, 13000, 100, 12289], 2, 16, 5000, 4, 300),
+    ([20000, 12500], 1, 16, 12400, 0, 12000),  # recent keys that overlap themselves, in tiles of the cluster
+    ([15001], 3, 5, 7000, 0, 0),               # odd pages
+    ([13000], 2, 1, 600, 300, 300),            # nothing of the body
+    ([33000], 1, 128, 30000, 16, 1000),        # more holes than one round of the lists holds
+]
+
+
+@pytest.mark.parametrize("kind", ["heavy", "ties", "zero", "wild"])
+@pytest.mark.parametrize("lens, H, ps, budget, sink, recent", SLICED)
+def test_evict_of_long_requests(lens, H, ps, budget, sink, recent, kind):
+    _check_evict(lens, H, ps, "bf16", budget, sink, recent, kind=kind, D=64, seed=len(lens))
+
+
+@pytest.mark.parametrize("dtype, layout", [("e4m3", "nhd"), ("nvfp4", "padded"), ("nvfp4", "hnd"), ("bf16", "hnd")])
+def test_evict_of_long_requests_moves_every_pool_type(dtype, layout):
+    _check_evict([14000, 12800], 2, 16, dtype, 12000, 4, 2000, layout=layout, seed=9)
+
+
+def test_evict_of_more_long_units_than_clusters_run_at_once():
+    _check_evict([12300] * 40, 4, 16, "bf16", 12200, 0, 40, kind="ties", D=64, seed=10)
+
+
+def test_evict_with_survivors_all_behind_the_budget():
+    # ascending scores: every survivor is a mover, in many rounds of the lists, in both forms
+    pk = _pk()
+    for L, b in ((12000, 5000), (100000, 45000)):
+        ps = 8
+        pool = torch.zeros((L // ps, ps, 1, 64), dtype=torch.bfloat16, device="cuda")
+        pool[..., 0] = (torch.arange(L, device="cuda") // 512).view(-1, ps, 1)
+        cache = pk.KVCache(pool, pool.clone())
+        pages = np.random.RandomState(0).permutation(L // ps).astype(np.int32)
+        at = torch.from_numpy(pages).cuda().long()
+        plan = pk.Plan().plan([0, 1], [0, len(pages)], pages, [ps], num_qo_heads=1, num_kv_heads=1, head_dim=64, page_size=ps)
+        scores = torch.empty((L // ps, 1, ps), device="cuda")
+        scores[at, 0] = torch.arange(L, device="cuda", dtype=torch.float32).view(-1, ps)
+        before = cache.k[at, :, 0, 0].reshape(-1).clone()
+        kept = plan.evict(cache, scores, b)
+        got = kept[0, 0].long()
+        assert torch.equal(got.sort().values, torch.arange(L - b, L, device="cuda"))
+        assert torch.equal(scores[at, 0].reshape(-1)[:b], got.float())
+        for x in (cache.k, cache.v):
+            assert torch.equal(x[at, :, 0, 0].reshape(-1)[:b], before[got])
+
+
+def test_pools_beyond_four_gigabytes():
+    # pages at byte offsets past 2^32 of an NVFP4 pool: write, read back, scored decode, eviction
+    pk = _pk()
+    P, ps, H = 560000, 16, 8
+    cache = pk.KVCache.nvfp4(P, ps, H, 128, 0.002, 0.002)
+    assert cache.k.stride(0) * (P - 30) > 2 ** 32
+    scores = torch.zeros((P, H, ps), device="cuda")
+    pages = np.array([P - 1, 3, P - 30, P - 7, 11, P - 2], np.int32)
+    L = 6 * ps - 5
+    g = torch.Generator().manual_seed(3)
+    k, v = (torch.randn((L, H, 128), generator=g).to(torch.bfloat16) for _ in range(2))
+    slots = torch.from_numpy(pages.astype(np.int64)[np.arange(L) // ps] * ps + np.arange(L) % ps).cuda()
+    pk.kv_store(k.cuda(), v.cuda(), slots, cache, scores=scores)
+    lk, lv = pk.kv_load(slots, cache)
+    K, V = (O4.dequantize(*O4.quantize(x.float().numpy(), 0.002), 0.002) for x in (k, v))
+    for got, ref in ((lk, K), (lv, V)):
+        assert np.all(np.abs(_np(got.float()) - ref) <= 2.0 ** -8 * (1 + 2.0 ** -12) * np.abs(ref))
+    q = torch.randn((1, 32, 128), generator=g).to(torch.bfloat16)
+    plan = pk.Plan().plan([0, 1], [0, 6], pages, [L - 5 * ps], num_qo_heads=32, num_kv_heads=8, head_dim=128, page_size=ps,
+                          kv_dtype="nvfp4", scored=True)
+    out, lse = plan.run(q.cuda(), cache, return_lse=True, scores=scores)
+    qn = q[0].double().numpy()
+    for h in range(32):
+        o, l = OA.attend(qn[h], K[:, h // 4], V[:, h // 4], 0, L - 1, 1 / np.sqrt(128))
+        assert np.abs(_np(out[0, h].float()) - o).max() <= 2e-2 and abs(float(lse[0, h]) - l) <= 2e-3
+    w = OE.key_weights(qn, K, 0, L - 1, 1 / np.sqrt(128), 4)
+    got = _np(scores[torch.from_numpy(pages).cuda().long()]).transpose(0, 2, 1).reshape(-1, H)[:L]
+    assert np.abs(got - w).max() <= 1e-4
+    kept = _np(plan.evict(cache, scores, 40, num_sink=2, num_recent=8))
+    ek, _ = pk.kv_load(slots[:40], cache)
+    for h in range(H):
+        assert torch.equal(ek[:, h], lk[torch.from_numpy(kept[0, h]).cuda().long(), h])
 
 
 def test_evict_of_a_request_longer_than_the_score_cache():
