@@ -115,7 +115,7 @@ __device__ __forceinline__ void add_weights(const RunParams& p, const WorkItem& 
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const int key = base + 4 * (tid + u * threads) + k;
-              x[u][k] = key >= lo && key < hi ? *reinterpret_cast<const float4*>(lg0 + (int64_t)key * G + g)
+              x[u][k] = key >= lo && key < hi ? __ldcg(reinterpret_cast<const float4*>(lg0 + (int64_t)key * G + g))
                                               : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
             }
           const float l0 = lse[g], l1 = lse[g + 1], l2 = lse[g + 2], l3 = lse[g + 3];
@@ -133,7 +133,7 @@ __device__ __forceinline__ void add_weights(const RunParams& p, const WorkItem& 
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const int key = base + 4 * (tid + u * threads) + k;
-              if (key >= lo && key < hi) a[u][k] += ex2(lg0[(int64_t)key * G + g] - l0);
+              if (key >= lo && key < hi) a[u][k] += ex2(__ldcg(lg0 + (int64_t)key * G + g) - l0);
             }
         }
       }
@@ -175,7 +175,7 @@ __device__ __forceinline__ void add_weights(const RunParams& p, const WorkItem& 
 #pragma unroll
       for (int u = 0; u < KU; ++u) {
         const int key = base + tid + u * threads;
-        if (key < hi) a[u] += ex2(lg0[(int64_t)key * G + g] - l0);
+        if (key < hi) a[u] += ex2(__ldcg(lg0 + (int64_t)key * G + g) - l0);
       }
     }
 #pragma unroll
@@ -339,8 +339,10 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB, HPB>::CTAS) decode_k
   // byte strides fit 32 bits; narrow: so do all offsets into the pools
   const bool halves_paged = FP4 && ps_shift >= 4 && (w.kv_begin & 15) == 0 &&
                             ((p.stride_page_b | p.stride_token_b | p.sf_page_b | p.sf_token_b) >> 32) == 0;
-  const bool narrow = halves_paged && (p.num_pages >> 31) == 0 && ((p.num_pages * p.stride_page_b) >> 32) == 0 &&
-                      ((p.num_pages * p.sf_page_b) >> 32) == 0;
+  const bool narrow =
+      halves_paged && ((p.num_pages | p.stride_head_b | p.sf_head_b) >> 31) == 0 &&
+      ((p.num_pages * p.stride_page_b + ps * p.stride_token_b + p.num_kv_heads * p.stride_head_b) >> 32) == 0 &&
+      ((p.num_pages * p.sf_page_b + ps * p.sf_token_b + p.num_kv_heads * p.sf_head_b) >> 32) == 0;
   const unsigned pool_pages = (unsigned)min(p.num_pages, (int64_t)0x7fffffff);  // (a page id is a non-negative int)
   const int64_t lane_off = head_off + (int64_t)lsub * p.stride_token_b + lc * 16;
   const int lane_sw = C::at(lsub, lc);

@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(kScoreThreads) score_add_kernel(const RunParam
   add_weights<kScoreUnroll>(p, w, unit_logits(p, w), s_lse, lo, hi, threadIdx.x, kScoreThreads, [&] {
     pdl_wait();  // the decode run's scaled scores and log-sum-exps
     for (int g = threadIdx.x; g < G; g += kScoreThreads)
-      s_lse[g] = p.lse2[(int64_t)w.q_row * p.num_qo_heads + w.kv_head * G + g];
+      s_lse[g] = __ldcg(p.lse2 + (int64_t)w.q_row * p.num_qo_heads + w.kv_head * G + g);
     __syncthreads();
   });
 }

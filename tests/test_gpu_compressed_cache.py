@@ -56,6 +56,8 @@ def _fp4_pools(P, ps, H, layout, fill=0xA5):
             return torch.full((P, ps, H, w), fill, dtype=torch.uint8, device="cuda")
         if layout == "hnd":
             return torch.full((P, H, ps, w), fill, dtype=torch.uint8, device="cuda").transpose(1, 2)
+        if layout == "head pools":  # one contiguous pool per head
+            return torch.full((H, P, ps, w), fill, dtype=torch.uint8, device="cuda").permute(1, 2, 0, 3)
         # padded rows: more than the row between tokens, heads and pages
         pad = 64 if w >= 64 else 8
         return torch.full((P, ps + 1, H + 1, w + pad), fill, dtype=torch.uint8, device="cuda")[:, :ps, :H, :w]
@@ -78,7 +80,7 @@ def _special_rows(T, H, seed):
     return x.to(torch.bfloat16)
 
 
-@pytest.mark.parametrize("layout", ["nhd", "hnd", "padded"])
+@pytest.mark.parametrize("layout", ["nhd", "hnd", "padded", "head pools"])
 @pytest.mark.parametrize("T, H, ps, scale", [(1, 1, 1, 1.0), (7, 3, 5, 0.125), (64, 8, 16, 0.0017), (301, 2, 128, 0.37)])
 def test_store_writes_the_oracles_codes_and_load_reads_them_back(T, H, ps, scale, layout):
     pk = _pk()
@@ -276,7 +278,7 @@ DECODE = [
 ]
 
 
-@pytest.mark.parametrize("layout", ["nhd", "hnd", "padded"])
+@pytest.mark.parametrize("layout", ["nhd", "hnd", "padded", "head pools"])
 @pytest.mark.parametrize("lens, heads, kv_heads, ps, window, sms", DECODE)
 def test_nvfp4_decode(lens, heads, kv_heads, ps, window, sms, layout):
     c = Case(lens, heads, kv_heads, ps, "nvfp4", layout=layout, window=window, seed=len(lens))
@@ -626,12 +628,19 @@ def test_evict_with_survivors_all_behind_the_budget():
             assert torch.equal(x[at, :, 0, 0].reshape(-1)[:b], before[got])
 
 
-def test_pools_beyond_four_gigabytes():
-    # pages at byte offsets past 2^32 of an NVFP4 pool: write, read back, scored decode, eviction
+@pytest.mark.parametrize("layout", ["pages outermost", "heads outermost"])
+def test_pools_beyond_four_gigabytes(layout):
+    # rows at byte offsets past 2^32 of an NVFP4 pool (by their page, or by their head alone): write, read
+    # back, scored decode, eviction
     pk = _pk()
-    P, ps, H = 560000, 16, 8
-    cache = pk.KVCache.nvfp4(P, ps, H, 128, 0.002, 0.002)
-    assert cache.k.stride(0) * (P - 30) > 2 ** 32
+    P, ps, H = 640000, 16, 8
+    if layout == "pages outermost":
+        cache = pk.KVCache.nvfp4(P, ps, H, 128, 0.002, 0.002)
+        assert cache.k.stride(0) * (P - 30) > 2 ** 32
+    else:
+        pools = [torch.empty((H, P, ps, w), dtype=torch.uint8, device="cuda").permute(1, 2, 0, 3) for w in (64, 64, 8, 8)]
+        cache = pk.KVCache(pools[0], pools[1], 0.002, 0.002, k_sf=pools[2], v_sf=pools[3])
+        assert cache.k.stride(0) * P < 2 ** 32 < cache.k.stride(2) * (H - 1)
     scores = torch.zeros((P, H, ps), device="cuda")
     pages = np.array([P - 1, 3, P - 30, P - 7, 11, P - 2], np.int32)
     L = 6 * ps - 5
