@@ -61,7 +61,7 @@ def _stream_ptr(stream) -> int:
     if stream is not None:
         return int(stream.cuda_stream)
     if _raw_stream is not None:  # the current stream's handle without building a Stream object
-        return int(_raw_stream(torch.cuda.current_device()))
+        return int(_raw_stream(_get_device()))
     return int(torch.cuda.current_stream().cuda_stream)
 
 
@@ -383,8 +383,8 @@ class Plan:
             raise ValueError(f"q must be [{self.total_tokens}, {self.num_qo_heads}, {self.head_dim}]")
         if out is None:
             out = torch.empty_like(q)
-        if (return_lse or lse is not None) and lse is None:
-            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        if lse is None and return_lse:
+            lse = torch.empty((self.total_tokens, self.num_qo_heads), dtype=torch.float32, device=q.device)
         return out, lse
 
     def run_ragged(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor | None = None,
@@ -453,7 +453,7 @@ class Plan:
             s = _stream_ptr(stream)
             if s != self._scratch_stream and not torch.cuda.is_current_stream_capturing():
                 # used off the stream it was allocated on: its memory is not reused before this run is done
-                self.scratch.record_stream(stream or torch.cuda.current_stream())
+                self.scratch.record_stream(torch.cuda.ExternalStream(s) if s else torch.cuda.default_stream())
             check(lib().pkv_attn_decode_run_scored(
                 self._h, q.data_ptr(), C.byref(cache.struct), out.data_ptr(), lse.data_ptr() if lse is not None else None,
                 addr, self.scratch.data_ptr(), self.scratch.numel(), s))
