@@ -403,11 +403,10 @@ __global__ void __launch_bounds__(Form<SLICED>::THREADS, Form<SLICED>::CTAS) evi
   auto row_off = [&](int page, int off) -> int64_t {
     return (int64_t)page * p.stride_page_b + (int64_t)off * p.stride_token_b + head_off;
   };
-  // chunk x of the CTA's columns of the row at byte offset `off`
-  auto chunk_ptr = [&](int64_t off, int x) -> uint4* {
-    const int c = col0 + x;
-    return reinterpret_cast<uint4*>((c < rc ? p.k_pool : p.v_pool) + off) + (c & (rc - 1));
-  };
+  // Each thread moves one column, of the rows row0, row0 + rows_at_once, ... of a list (THREADS is a
+  // multiple of cols).
+  const int col = col0 + (tid & (cols - 1)), row0 = tid >> item_shift, rows_at_once = THREADS >> item_shift;
+  char* const column = (col < rc ? p.k_pool : p.v_pool) + (col & (rc - 1)) * 16;
   auto sf_off = [&](int page, int off) -> int64_t {
     return (int64_t)page * p.sf_page_b + (int64_t)off * p.sf_token_b + sf_head;
   };
@@ -459,18 +458,17 @@ __global__ void __launch_bounds__(Form<SLICED>::THREADS, Form<SLICED>::CTAS) evi
       }
     }
     __syncthreads();
-    const int items = mine << item_shift;
-    for (int x0 = tid; x0 < items; x0 += THREADS * kUnroll) {
+    for (int e0 = row0; e0 < mine; e0 += rows_at_once * kUnroll) {
       uint4 v[kUnroll];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        const int x = x0 + u * THREADS;
-        if (x < items) v[u] = *chunk_ptr(sh.place[x >> item_shift].y, x & (cols - 1));
+        const int e = e0 + u * rows_at_once;
+        if (e < mine) v[u] = *reinterpret_cast<const uint4*>(column + sh.place[e].y);
       }
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        const int x = x0 + u * THREADS;
-        if (x < items) *chunk_ptr(sh.place[x >> item_shift].x, x & (cols - 1)) = v[u];
+        const int e = e0 + u * rows_at_once;
+        if (e < mine) *reinterpret_cast<uint4*>(column + sh.place[e].x) = v[u];
       }
     }
     unit_sync();  // the lists may be rewritten; sources in [front, tail) may be overwritten
@@ -478,7 +476,7 @@ __global__ void __launch_bounds__(Form<SLICED>::THREADS, Form<SLICED>::CTAS) evi
 
   // ---- the last R keys move down by L - b, in order ----
   const bool overlap = L - b < R;  // tiles are then read by all who share them before any is written
-  const int rows = min(THREADS, (THREADS * kUnroll) >> item_shift);  // rows per CTA and tile
+  const int rows = min(THREADS, rows_at_once * kUnroll);  // rows per CTA and tile
   for (int j0 = 0; j0 < R; j0 += C * rows) {
     const int first = j0 + rank * rows;
     const int mine = max(0, min(rows, R - first));
@@ -501,12 +499,11 @@ __global__ void __launch_bounds__(Form<SLICED>::THREADS, Form<SLICED>::CTAS) evi
       }
     }
     __syncthreads();
-    const int items = mine << item_shift;
     uint4 v[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int x = tid + u * THREADS;
-      if (x < items) v[u] = *chunk_ptr(sh.place[x >> item_shift].y, x & (cols - 1));
+      const int e = row0 + u * rows_at_once;
+      if (e < mine) v[u] = *reinterpret_cast<const uint4*>(column + sh.place[e].y);
     }
     if (overlap) unit_sync();
     if (tid < mine) {
@@ -518,8 +515,8 @@ __global__ void __launch_bounds__(Form<SLICED>::THREADS, Form<SLICED>::CTAS) evi
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int x = tid + u * THREADS;
-      if (x < items) *chunk_ptr(sh.place[x >> item_shift].x, x & (cols - 1)) = v[u];
+      const int e = row0 + u * rows_at_once;
+      if (e < mine) *reinterpret_cast<uint4*>(column + sh.place[e].x) = v[u];
     }
     __syncthreads();  // the list is rewritten by the next tile
   }
