@@ -43,7 +43,6 @@ namespace {
 
 constexpr int kBins = 2048;
 constexpr int kUnroll = 4;         // 16-byte chunks in flight per thread
-constexpr int kScoreUnroll = 4;    // groups of four scores in flight per thread
 constexpr int kMaxWhole = 12288;   // longest request of the whole form (48 KB of scores)
 constexpr int kMaxKeys = 32768;    // scores of a slice kept in shared memory (128 KB); longer slices re-read them
 constexpr int kMaxSlice = 262144;  // positions per CTA at most (12 bytes of shared memory per 32 of them)
@@ -57,6 +56,9 @@ struct Form {
   static constexpr int WARPS = THREADS / 32;
   static constexpr int LIST = SLICED ? 2048 : 512;  // moves one CTA holds at a time
   static constexpr int HISTS = SLICED ? 2 : 1;
+  static constexpr int SCORES = SLICED ? 6 : 4;  // groups of four scores in flight per thread
+  static constexpr int KEYS = SLICED ? 1 : 4;    // keys read ahead per thread
+  static constexpr int PLACES = SLICED ? 2 : 1;  // moves whose rows a thread looks up at once
   static_assert(THREADS <= LIST, "the list holds a tile of the last rows");
   static constexpr int GROUPS = SLICED ? kBins / 32 : 1;  // sliced: sums of 32 neighbouring bins
   struct alignas(16) Shared {
@@ -177,10 +179,10 @@ __global__ void __launch_bounds__(Form<SLICED>::THREADS, Form<SLICED>::CTAS) evi
     if ((ps & 3) == 0 && (reinterpret_cast<uintptr_t>(p.scores) & 15) == 0) {
       // four positions of one page at a time; a last group may reach past L, but not past its page
       const int groups = (n + 3) / 4;
-      for (int q0 = tid; q0 < groups; q0 += THREADS * kScoreUnroll) {
-        float4 x[kScoreUnroll];
+      for (int q0 = tid; q0 < groups; q0 += THREADS * F::SCORES) {
+        float4 x[F::SCORES];
 #pragma unroll
-        for (int u = 0; u < kScoreUnroll; ++u) {
+        for (int u = 0; u < F::SCORES; ++u) {
           const int q = q0 + u * THREADS;
           if (q < groups) {
             int page, off;
@@ -189,7 +191,7 @@ __global__ void __launch_bounds__(Form<SLICED>::THREADS, Form<SLICED>::CTAS) evi
           }
         }
 #pragma unroll
-        for (int u = 0; u < kScoreUnroll; ++u) {
+        for (int u = 0; u < F::SCORES; ++u) {
           const int q = q0 + u * THREADS;
           if (q < groups)
             *reinterpret_cast<uint4*>(keys + 4 * q) =
@@ -197,15 +199,15 @@ __global__ void __launch_bounds__(Form<SLICED>::THREADS, Form<SLICED>::CTAS) evi
         }
       }
     } else {
-      for (int k0 = tid; k0 < n; k0 += THREADS * kScoreUnroll) {
-        uint32_t x[kScoreUnroll];
+      for (int k0 = tid; k0 < n; k0 += THREADS * F::SCORES) {
+        uint32_t x[F::SCORES];
 #pragma unroll
-        for (int u = 0; u < kScoreUnroll; ++u) {
+        for (int u = 0; u < F::SCORES; ++u) {
           const int k = k0 + u * THREADS;
           if (k < n) x[u] = key_from_memory(base + k);
         }
 #pragma unroll
-        for (int u = 0; u < kScoreUnroll; ++u) {
+        for (int u = 0; u < F::SCORES; ++u) {
           const int k = k0 + u * THREADS;
           if (k < n) keys[k] = x[u];
         }
@@ -227,9 +229,14 @@ __global__ void __launch_bounds__(Form<SLICED>::THREADS, Form<SLICED>::CTAS) evi
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
       const uint32_t bits = pass == 2 ? 0x3ffu : 0x7ffu;
       uint32_t* hist = sh.hist[SLICED ? pass & 1 : 0];
-      for (int k = body_lo + tid; k < body_hi; k += THREADS) {
-        const uint32_t key = key_at(k);
-        if ((key & fixed) == prefix) atomicAdd(&hist[(key >> shift) & bits], 1u);
+      for (int k0 = body_lo + tid; k0 < body_hi; k0 += THREADS * F::KEYS) {
+        uint32_t x[F::KEYS];
+#pragma unroll
+        for (int u = 0; u < F::KEYS; ++u)
+          if (k0 + u * THREADS < body_hi) x[u] = key_at(k0 + u * THREADS);
+#pragma unroll
+        for (int u = 0; u < F::KEYS; ++u)
+          if (k0 + u * THREADS < body_hi && (x[u] & fixed) == prefix) atomicAdd(&hist[(x[u] >> shift) & bits], 1u);
       }
       if constexpr (SLICED) {
         // the bin of the rest-th key from the top, over the cluster's slices: first its group of 32 bins,
@@ -317,33 +324,41 @@ __global__ void __launch_bounds__(Form<SLICED>::THREADS, Form<SLICED>::CTAS) evi
       prefix |= sh.digit << shift;
       fixed |= bits << shift;
       rest = sh.rest;
-      if (pass == 2) {
-        // the last pass counted every slice's keys equal to T
-        if constexpr (SLICED) {
-          const uint32_t x = lane < rank ? cluster.map_shared_rank(hist, lane)[sh.digit] : 0u;
-          eq_before = __reduce_add_sync(0xffffffffu, x);
-        }
-      } else if (sh.count == rest && prefix > 0) {
+      if (sh.count == rest && prefix > 0) {
         // every key with these digits survives: all keys from `prefix` up, none by position
         prefix -= 1;
         rest = 0;
         break;
       }
+      if constexpr (SLICED)
+        if (pass == 2) {
+          // the last pass counted every slice's keys equal to T
+          const uint32_t x = lane < rank ? cluster.map_shared_rank(hist, lane)[sh.digit] : 0u;
+          eq_before = __reduce_add_sync(0xffffffffu, x);
+        }
     }
     T = prefix;
     need_eq = rest;
   }
 
   // ---- survivors, a bit per position ----
-  for (int w = warp; w < nw; w += WARPS) {
-    const int k = w * 32 + lane;
-    const bool body = k >= body_lo && k < body_hi;
-    const uint32_t key = body ? key_at(k) : 0u;
-    const uint32_t gt = __ballot_sync(0xffffffffu, body && key > T);
-    const uint32_t eq = __ballot_sync(0xffffffffu, body && key == T);
-    if (lane == 0) {
-      lives[w] = gt;
-      eqw[w] = eq;
+  for (int wu = warp; wu < nw; wu += WARPS * F::KEYS) {
+    uint32_t x[F::KEYS];
+#pragma unroll
+    for (int u = 0; u < F::KEYS; ++u) {
+      const int k = (wu + u * WARPS) * 32 + lane;
+      if (k >= body_lo && k < body_hi) x[u] = key_at(k);
+    }
+#pragma unroll
+    for (int u = 0; u < F::KEYS; ++u) {
+      const int w = wu + u * WARPS, k = w * 32 + lane;
+      const bool body = k >= body_lo && k < body_hi;
+      const uint32_t gt = __ballot_sync(0xffffffffu, body && x[u] > T);
+      const uint32_t eq = __ballot_sync(0xffffffffu, body && x[u] == T);
+      if (lane == 0 && w < nw) {
+        lives[w] = gt;
+        eqw[w] = eq;
+      }
     }
   }
   __syncthreads();
@@ -412,50 +427,78 @@ __global__ void __launch_bounds__(Form<SLICED>::THREADS, Form<SLICED>::CTAS) evi
   };
   if constexpr (!SLICED) cluster.barrier_wait();  // all CTAs of the unit have read its scores
   const uint32_t lt = (1u << lane) - 1u;
+  const int front_here = min(max(front - base, 0), n);  // positions of the slice that are in the front
+  const int front_words = (front_here + 31) / 32, mover_word0 = front_here / 32;
   for (uint32_t t0 = 0, per = 0; t0 < holes || t0 == 0; t0 += per * C) {
     per = min((uint32_t)F::LIST, (holes - t0 + C - 1) / C);  // moves per CTA of this round
     const float inv_per = 1.f / (float)max(per, 1u);
-    for (int w = warp; w < nw; w += WARPS) {
+    auto entry = [&](uint32_t t) -> int2* {  // of move t0 + t, in the list of the CTA that does it
+      if constexpr (!SLICED) return sh.move + t;
+      int r = (int)((float)t * inv_per);  // t / per, off by one at most (t < 2^14)
+      r += (uint32_t)(r + 1) * per <= t;
+      r -= (uint32_t)r * per > t;
+      return cluster.map_shared_rank(sh.move, r) + (t - r * per);
+    };
+    // the front, a lane per position: holes take numbers, the others stay
+    for (int w = warp; w < front_words; w += WARPS) {
       const int first = base + w * 32, pos = first + lane;
-      const uint32_t alive = lives[w];
-      const uint32_t hb = ~alive & range_mask(first, S, front), mb = alive & range_mask(first, front, tail);
-      const bool hole = (hb >> lane) & 1, mover = (mb >> lane) & 1;
+      const uint32_t hb = ~lives[w] & range_mask(first, S, front);
+      const bool hole = (hb >> lane) & 1;
       if (with_k && t0 == 0 && pos < front && !hole) kept[pos] = pos;
-      if (hole || mover) {
-        const uint32_t t = (hole ? eqw[w] + __popc(hb & lt) : mov[w] + __popc(mb & lt)) - t0;  // wraps below t0
-        if (t < per * C) {
-          int2* e;
-          if constexpr (SLICED) {
-            int r = (int)((float)t * inv_per);  // t / per, off by one at most (t < 2^14)
-            r += (uint32_t)(r + 1) * per <= t;
-            r -= (uint32_t)r * per > t;
-            e = cluster.map_shared_rank(sh.move, r) + (t - r * per);
-          } else {
-            e = sh.move + t;
-          }
-          if (hole) e->x = pos;
-          else e->y = pos;
-        }
+      const uint32_t t = eqw[w] + __popc(hb & lt) - t0;  // wraps below t0
+      if (hole && t < per * C) entry(t)->x = pos;
+    }
+    // the survivors behind it.  Sliced: a thread per word, since few of many positions survive (131072
+    // keys to 8192: the lists take 4.6 us, with a lane per position 9.6); whole: a lane per position, where a
+    // budget near the length leaves dense words (1088 keys to 1024: 1.1 us, a thread per word 2.1)
+    if constexpr (SLICED) {
+      for (int w = mover_word0 + tid; w < nw; w += THREADS) {
+        const int first = base + w * 32;
+        uint32_t mb = lives[w] & range_mask(first, front, tail);
+        for (uint32_t t = mov[w] - t0; mb != 0; ++t, mb &= mb - 1)
+          if (t < per * C) entry(t)->y = first + __ffs(mb) - 1;
+      }
+    } else {
+      for (int w = mover_word0 + warp; w < nw; w += WARPS) {
+        const int first = base + w * 32;
+        const uint32_t mb = lives[w] & range_mask(first, front, tail);
+        const uint32_t t = mov[w] + __popc(mb & lt) - t0;
+        if (((mb >> lane) & 1) && t < per) entry(t)->y = first + lane;
       }
     }
     if (holes == 0) break;
     unit_sync();  // the lists are complete
     const int mine = (int)min((int64_t)per, max((int64_t)0, (int64_t)holes - t0 - (int64_t)rank * per));
-    for (int e = tid; e < mine; e += THREADS) {
-      const int2 mv = sh.move[e];
-      int dp, dof, sp, sof;
-      place_of(mv.x, dp, dof);
-      place_of(mv.y, sp, sof);
-      sh.place[e] = make_longlong2(row_off(dp, dof), row_off(sp, sof));
-      if (with_k) {
-        kept[mv.x] = mv.y;
-        *score_at(dp, dof) = *score_at(sp, sof);
-      }
-      if (p.k_sf) {
-        const int64_t d = sf_off(dp, dof), s = sf_off(sp, sof);
-        if (with_k) *reinterpret_cast<uint2*>(p.k_sf + d) = *reinterpret_cast<const uint2*>(p.k_sf + s);
-        if (with_v) *reinterpret_cast<uint2*>(p.v_sf + d) = *reinterpret_cast<const uint2*>(p.v_sf + s);
-      }
+    for (int e = tid; e < mine; e += THREADS * F::PLACES) {
+      int2 mv[F::PLACES];
+      int dp[F::PLACES], dof[F::PLACES], sp[F::PLACES], sof[F::PLACES];
+      float sc[F::PLACES];
+#pragma unroll
+      for (int u = 0; u < F::PLACES; ++u)
+        if (e + u * THREADS < mine) {
+          mv[u] = sh.move[e + u * THREADS];
+          place_of(mv[u].x, dp[u], dof[u]);
+          place_of(mv[u].y, sp[u], sof[u]);
+        }
+#pragma unroll
+      for (int u = 0; u < F::PLACES; ++u)
+        if (e + u * THREADS < mine) {
+          if (with_k) sc[u] = *score_at(sp[u], sof[u]);
+          sh.place[e + u * THREADS] = make_longlong2(row_off(dp[u], dof[u]), row_off(sp[u], sof[u]));
+        }
+#pragma unroll
+      for (int u = 0; u < F::PLACES; ++u)
+        if (e + u * THREADS < mine) {
+          if (p.k_sf) {
+            const int64_t d = sf_off(dp[u], dof[u]), s = sf_off(sp[u], sof[u]);
+            if (with_k) *reinterpret_cast<uint2*>(p.k_sf + d) = *reinterpret_cast<const uint2*>(p.k_sf + s);
+            if (with_v) *reinterpret_cast<uint2*>(p.v_sf + d) = *reinterpret_cast<const uint2*>(p.v_sf + s);
+          }
+          if (with_k) {
+            kept[mv[u].x] = mv[u].y;
+            *score_at(dp[u], dof[u]) = sc[u];
+          }
+        }
     }
     __syncthreads();
     for (int e0 = row0; e0 < mine; e0 += rows_at_once * kUnroll) {
