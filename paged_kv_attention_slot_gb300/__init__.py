@@ -387,6 +387,19 @@ class Plan:
             lse = torch.empty((self.total_tokens, self.num_qo_heads), dtype=torch.float32, device=q.device)
         return out, lse
 
+    def _check_tensors(self, q, out, lse, cache):
+        """The tensors of a run over an NVFP4 cache or with scores: on the cache's device, outputs of the run's shapes."""
+        d = cache._device_index
+        if q.get_device() != d:
+            raise ValueError("q must be on the cache's device")
+        if out is not None and (out.dtype != torch.bfloat16 or not out.is_contiguous() or out.shape != q.shape
+                                or out.get_device() != d):
+            raise ValueError(f"out must be a contiguous bf16 tensor {list(q.shape)} on the cache's device")
+        if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or lse.shape != q.shape[:2]
+                                or lse.get_device() != d):
+            raise ValueError(f"lse must be a contiguous float32 tensor {list(q.shape[:2])} on the cache's device")
+        _check_device(cache)
+
     def run_ragged(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor | None = None,
                    lse: torch.Tensor | None = None, return_lse: bool = False, stream=None):
         """Attention of a "ragged" plan: k, v are contiguous bf16 [kv_indptr[-1], num_kv_heads, head_dim]."""
@@ -439,8 +452,8 @@ class Plan:
             if not self.scored or merge_into:
                 raise ValueError("scores need a plan made with scored=True (decode or mixed) and no merge_into")
             addr = _check_scores(scores, cache)
-            if self.scratch is None or q.get_device() != cache._device_index:
-                raise ValueError("a scored run needs a plan with a workspace and q on the cache's device")
+            if self.scratch is None:
+                raise ValueError("a scored run needs a plan with a workspace")
         if merge_into:
             if self.mode not in ("prefill", "extend") or out is None or lse is None:
                 raise ValueError("merge_into needs a prefill plan and the held state in out and lse")
@@ -448,6 +461,8 @@ class Plan:
             check(lib().pkv_attn_prefill_run_merge(self._h, q.data_ptr(), C.byref(cache.struct), out.data_ptr(),
                                                    lse.data_ptr(), _stream_ptr(stream)))
             return out, lse
+        if scores is not None or cache.dtype == _lib.PKV_NVFP4:
+            self._check_tensors(q, out, lse, cache)
         out, lse = self._outputs(q, out, lse, return_lse)
         if scores is not None:
             s = _stream_ptr(stream)

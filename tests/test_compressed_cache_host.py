@@ -289,3 +289,17 @@ def test_binding_refuses_bad_scored_runs_and_evictions(pk):
         _plan(pk).evict(c, s[:2], 4)
     with pytest.raises(ValueError):
         _plan(pk).evict(c, s, 4)  # scores on the host
+
+
+def test_binding_refuses_nvfp4_runs_off_the_device_and_outputs_of_another_shape(pk):
+    c, p = _fp4(pk), _plan(pk, kv_dtype="nvfp4")
+    q = torch.zeros((2, 8, 128), dtype=torch.bfloat16)
+    lse = torch.zeros((2, 8))
+    for out in (q[:1], q.float(), q.transpose(0, 1), q.view(2, 1024)):
+        with pytest.raises(ValueError, match="out must be"):
+            p.run(q, c, out=out)
+    for bad in (lse[:1], lse.double(), lse[:, :4], torch.zeros((8, 2)).t()):
+        with pytest.raises(ValueError, match="lse must be"):
+            p.run(q, c, out=q.clone(), lse=bad)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        p.run(q, c)  # a cache and a q on the host
