@@ -661,12 +661,14 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB, HPB>::CTAS) decode_k
         mx[k] = fmaxf(x[0][0][k], x[0][1][k]);
         if constexpr (C::SUBS == 2) mx[k] = fmax3(mx[k], x[1][0][k], x[1][1][k]);
       }
-#pragma unroll
-      for (int sh = 4; sh < 32; sh <<= 1)
-#pragma unroll
-        for (int k = 0; k < NCOL; ++k) mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], sh));
-      // every tile holds at least one visible key, so the tile maxima are finite
+      // (A column's lanes hold the same m, so the vote over each lane's own keys decides for the column; its
+      // maximum over the lanes is formed only where m moves.)
       if (__any_sync(0xffffffffu, mx[0] > m[nb][0] + 8.f || mx[NCOL - 1] > m[nb][NCOL - 1] + 8.f)) {
+        // every tile holds at least one visible key, so the tile maxima are finite
+#pragma unroll
+        for (int sh = 4; sh < 32; sh <<= 1)
+#pragma unroll
+          for (int k = 0; k < NCOL; ++k) mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], sh));
         float cf[NCOL];
 #pragma unroll
         for (int k = 0; k < NCOL; ++k) {
