@@ -56,9 +56,13 @@ struct Form {
   static constexpr int WARPS = THREADS / 32;
   static constexpr int LIST = SLICED ? 2048 : 512;  // moves one CTA holds at a time
   static constexpr int HISTS = SLICED ? 2 : 1;
-  static constexpr int SCORES = SLICED ? 6 : 4;  // groups of four scores in flight per thread
-  static constexpr int KEYS = SLICED ? 1 : 4;    // keys read ahead per thread
-  static constexpr int PLACES = SLICED ? 2 : 1;  // moves whose rows a thread looks up at once
+  // groups of four scores in flight per thread (sliced: 4 is 0.1 us slower on 2 x 131072 keys)
+  static constexpr int SCORES = SLICED ? 6 : 4;
+  // keys read ahead per thread: whole, 8 x 1060 keys, 8.9 us with 4, 9.9 with 1 (a warp has little else to
+  // do); sliced, where eight warps per scheduler hide the reads, 35.9 us with 1, 37 with 2
+  static constexpr int KEYS = SLICED ? 1 : 4;
+  // moves whose rows a thread looks up at once: whole, 64 x 512..4160 keys, 64 us with 1, 69 with 2 (spills)
+  static constexpr int PLACES = SLICED ? 2 : 1;
   static_assert(THREADS <= LIST, "the list holds a tile of the last rows");
   static constexpr int GROUPS = SLICED ? kBins / 32 : 1;  // sliced: sums of 32 neighbouring bins
   struct alignas(16) Shared {
