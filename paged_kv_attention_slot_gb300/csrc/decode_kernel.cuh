@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB, HPB>::CTAS) decode_k
             const O base = (O)hp * (unsigned)p.stride_page_b + (O)ho * (unsigned)p.stride_token_b + (O)lane_off;
 #pragma unroll
             for (int j = 0; j < 16 / RPI; ++j) {
-              const O at = base + (O)(j * (unsigned)row_step);
+              const O at = base + (O)j * (O)row_step;  // (the step may pass 2^32 where a token's stride does not)
               cp_async16_pol(dk + lane_sw + (16 * hf + j * RPI) * C::ROWB, p.k_pool + at, 16u, kv_policy);
               cp_async16_pol(dv + lane_sw + (16 * hf + j * RPI) * C::ROWB, p.v_pool + at, 16u, kv_policy);
             }

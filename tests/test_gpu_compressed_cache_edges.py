@@ -1,0 +1,67 @@
+"""The compressed cache at the edges of what its entry points accept.
+
+Tolerances are those of tests/test_gpu_compressed_cache.py (derived in its docstring)."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import attention as OA
+from oracle import nvfp4 as O4
+from tests.test_gpu_compressed_cache import _np, _pk
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    import paged_kv_attention_slot_gb300 as pk
+
+    pk._lib.lib()
+    assert pk.device_error() == 0
+    yield
+    assert pk.device_error() == 0
+
+
+# ------------------------------------------------------------------------------------------------
+# strides
+# ------------------------------------------------------------------------------------------------
+def test_nvfp4_pool_whose_rows_lie_a_gigabyte_apart():
+    # [page_size, pages, heads, ...] pools: 2^29 bytes from a token's codes to the next one's, so eight tokens
+    # are 2^32 bytes apart
+    pk = _pk()
+    P, ps, H, Hq = 1 << 20, 16, 8, 32
+    pools = [torch.empty((ps, P, H, w), dtype=torch.uint8, device="cuda").permute(1, 0, 2, 3) for w in (64, 64, 8, 8)]
+    cache = pk.KVCache(pools[0], pools[1], 0.002, 0.002, k_sf=pools[2], v_sf=pools[3])
+    assert cache.k.stride(1) == 2 ** 29
+    pages = np.array([P - 1, 3, P - 30, P - 7, 11, P - 2], np.int32)
+    L = 6 * ps - 5
+    g = torch.Generator().manual_seed(3)
+    k, v = (torch.randn((L, H, 128), generator=g).to(torch.bfloat16) for _ in range(2))
+    slots = torch.from_numpy(pages.astype(np.int64)[np.arange(L) // ps] * ps + np.arange(L) % ps).cuda()
+    pk.kv_store(k.cuda(), v.cuda(), slots, cache)
+    lk, lv = pk.kv_load(slots, cache)
+    K, V = (O4.dequantize(*O4.quantize(x.float().numpy(), 0.002), 0.002) for x in (k, v))
+    for got, ref in ((lk, K), (lv, V)):
+        assert np.all(np.abs(_np(got.float()) - ref) <= 2.0 ** -8 * (1 + 2.0 ** -12) * np.abs(ref))
+    q = torch.randn((1, Hq, 128), generator=g).to(torch.bfloat16)
+    plan = pk.Plan().plan([0, 1], [0, 6], pages, [L - 5 * ps], num_qo_heads=Hq, num_kv_heads=H, head_dim=128, page_size=ps,
+                          kv_dtype="nvfp4")
+    out, lse = plan.run(q.cuda(), cache, return_lse=True)
+    qn = q[0].double().numpy()
+    scale = 1 / np.sqrt(128)
+    for h in range(Hq):
+        Kh, Vh = K[:, h // 4], V[:, h // 4]
+        o, l = OA.attend(qn[h], Kh, Vh, 0, L - 1, scale)
+        absv, _ = OA.attend(qn[h], Kh, np.abs(Vh), 0, L - 1, scale)
+        dx = 2.0 ** -16 * scale * float(np.max(np.abs(Kh) @ np.abs(qn[h])))
+        tol = 2.0 ** -8 * np.abs(o) + (2.0 ** -11 + 2 * dx + 2.0 ** -18) * absv * (1 + 2.0 ** -8) + L * 2.0 ** -25 * np.abs(Vh).max()
+        assert np.all(np.abs(_np(out[0, h].float()) - o) <= tol), h
+        assert abs(float(lse[0, h]) - l) <= dx + 2.0 ** -22 * (1 + abs(l)) + 2.0 ** -20, h
+    scores = torch.zeros((P, H, ps), device="cuda")
+    scores[torch.from_numpy(pages).cuda().long()] = torch.rand((6, H, ps), generator=g).cuda()
+    kept = _np(plan.evict(cache, scores, 40, num_sink=2, num_recent=8))
+    ek, ev = pk.kv_load(slots[:40], cache)
+    for h in range(H):
+        old = torch.from_numpy(kept[0, h]).cuda().long()
+        assert torch.equal(ek[:, h], lk[old, h]) and torch.equal(ev[:, h], lv[old, h])
