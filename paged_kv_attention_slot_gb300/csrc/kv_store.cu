@@ -120,19 +120,20 @@ struct Fp4Pools {
   int64_t sp_b, st_b, sh_b;  // strides of the scale pools in bytes
 };
 
-// Quotients rounded to nearest without a division: q = t r with r = 1 / s rounded, then one Newton step on
-// the quotient (Markstein's correction), two quotients at a time.  The caller keeps t / s away from over-
-// and underflow.
-__device__ __forceinline__ uint64_t div2_rn(uint64_t t2, uint64_t minus_s2, uint64_t r2) {
-  const uint64_t q2 = fmul2(t2, r2);
-  return ffma2(ffma2(q2, minus_s2, t2), r2, q2);
+// Quotients t / s rounded to nearest without a division: q = t r with r = 1 / s rounded, then one Newton step on
+// the quotient (Markstein's correction), two quotients at a time.  It takes u = -t and -r: the step is then
+// q - r (q s - t), whose sums keep the sign of t = -0 where t - q s would be +0.  The caller keeps t / s away
+// from over- and underflow.
+__device__ __forceinline__ uint64_t div2_rn(uint64_t u2, uint64_t s2, uint64_t minus_r2) {
+  const uint64_t q2 = fmul2(u2, minus_r2);
+  return ffma2(ffma2(q2, s2, u2), minus_r2, q2);
 }
 
 // The 16 codes of a block of bf16 pairs w under the block scale s (r = 1 / s rounded).  CLAMP: values may be
 // beyond 2688 = 6 * 448, where the scale is 448 and the code 6, infinities included.
 template <bool CLAMP>
 __device__ __forceinline__ uint2 quant_codes(const uint32_t (&w)[8], float inv, float s, float r) {
-  const uint64_t inv2 = f2pack(inv, inv), r2 = f2pack(r, r), ms2 = f2pack(-s, -s);
+  const uint64_t minus_inv2 = f2pack(-inv, -inv), minus_r2 = f2pack(-r, -r), s2 = f2pack(s, s);
   uint32_t c[2];
 #pragma unroll
   for (int v = 0; v < 2; ++v) {
@@ -140,13 +141,13 @@ __device__ __forceinline__ uint2 quant_codes(const uint32_t (&w)[8], float inv, 
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t x = w[4 * v + j];
-      uint64_t t2 = fmul2(f2pack(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)), inv2);
+      uint64_t u2 = fmul2(f2pack(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)), minus_inv2);
       if constexpr (CLAMP) {
         float lo, hi;
-        f2unpack(t2, lo, hi);
-        t2 = f2pack(fminf(fmaxf(lo, -2688.f), 2688.f), fminf(fmaxf(hi, -2688.f), 2688.f));
+        f2unpack(u2, lo, hi);
+        u2 = f2pack(fminf(fmaxf(lo, -2688.f), 2688.f), fminf(fmaxf(hi, -2688.f), 2688.f));
       }
-      f2unpack(div2_rn(t2, ms2, r2), q[2 * j], q[2 * j + 1]);
+      f2unpack(div2_rn(u2, s2, minus_r2), q[2 * j], q[2 * j + 1]);
     }
     c[v] = f32x8_to_e2m1x8(q);
   }

@@ -65,3 +65,29 @@ def test_nvfp4_pool_whose_rows_lie_a_gigabyte_apart():
     for h in range(H):
         old = torch.from_numpy(kept[0, h]).cuda().long()
         assert torch.equal(ek[:, h], lk[old, h]) and torch.equal(ev[:, h], lv[old, h])
+
+
+# ------------------------------------------------------------------------------------------------
+# signed zeros
+# ------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("scale", [1.0, 0.0017, 2.0 ** 20])
+def test_store_keeps_the_sign_of_zeros_beside_other_values(scale):
+    # zeros of both signs, and values whose quotient or scaled value is too small for any code but a zero
+    pk = _pk()
+    T, H = 48, 2
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn((T, H, 128), generator=g) * scale
+    r = torch.rand((T, H, 128), generator=g)
+    for lo, val in ((0.0, 0.0), (0.2, -0.0), (0.4, -1e-4 * scale), (0.5, 1e-4 * scale), (0.6, -1e-40), (0.7, 1e-40)):
+        x[(r >= lo) & (r < lo + 0.1)] = val
+    k = x.to(torch.bfloat16)
+    cache = pk.KVCache.nvfp4(T // 16, 16, H, 128, scale, scale)
+    pk.kv_store(k.cuda(), (-k).cuda(), torch.arange(T, device="cuda"), cache)
+    for pool, sf, y in ((cache.k, cache.k_sf, k), (cache.v, cache.v_sf, -k)):
+        codes, f = O4.quantize(y.float().numpy(), scale)
+        assert np.array_equal(_np(sf).reshape(T, H, 8), f)
+        assert np.array_equal(_np(pool).reshape(T, H, 64), codes)
+        assert (O4.unpack(codes) == 8).any() and (O4.unpack(codes) == 0).any()
+    back, _ = pk.kv_load(torch.arange(T, device="cuda"), cache)
+    minus = (k == 0) & torch.signbit(k)
+    assert minus.any() and torch.signbit(back.cpu()[minus]).all() and not back.cpu()[minus].any()
