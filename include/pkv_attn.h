@@ -275,6 +275,10 @@ int pkv_attn_plan(pkv_plan* plan, const pkv_plan_args* args, void* workspace, si
  *   q    device, bf16, [total_tokens, num_qo_heads, head_dim], contiguous (total_tokens =
  *        qo_indptr[batch_size] of the plan).
  *   o    device, bf16, same shape as q: o[row, h, :] = sum_j softmax_j(scale * q.k_j) v_j.
+ *        FP8 and NVFP4 pools (decode): q is rounded to f16 after a power-of-two scaling that the query heads
+ *        of one KV head (16 at a time) share.  FP8, largest finite |q| of them below 2^15: no scaling.  Else
+ *        bf16 values down to 2^-28 of that largest are exact, smaller ones off by at most 2^-39 of it.
+ *        An infinity or a NaN stays within its own head.
  *   lse  device float32 [total_tokens, num_qo_heads] or NULL: natural-log log-sum-exp of the scaled
  *        scores of each row (the statistic "SGLang 源码完全拆解(八)：Attention Backend", section
  *        «extend 的两种形态», merges states with).

@@ -8,7 +8,7 @@ import torch
 
 from oracle import attention as OA
 from oracle import nvfp4 as O4
-from tests.test_gpu_compressed_cache import _np, _pk
+from tests.test_gpu_compressed_cache import Case, _np, _pk
 
 pytestmark = pytest.mark.gpu
 
@@ -91,3 +91,28 @@ def test_store_keeps_the_sign_of_zeros_beside_other_values(scale):
     back, _ = pk.kv_load(torch.arange(T, device="cuda"), cache)
     minus = (k == 0) & torch.signbit(k)
     assert minus.any() and torch.signbit(back.cpu()[minus]).all() and not back.cpu()[minus].any()
+
+
+# ------------------------------------------------------------------------------------------------
+# query heads of one group
+# ------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), 2.0 ** 16])
+@pytest.mark.parametrize("heads, kv_heads", [(8, 2), (16, 2), (32, 2), (40, 2)])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3", "nvfp4"])
+def test_a_head_does_not_depend_on_its_neighbours(dtype, heads, kv_heads, what):
+    # every other head holds a NaN, an infinity or large values; the heads between them are what they are without
+    c = Case([200, 90, 700], heads, kv_heads, 16, dtype, seed=6)
+    bad = np.arange(heads) % 2 == 1
+    out, lse = c.plan(num_sms=8).run(c.q, c.cache, return_lse=True)
+    q = c.q.clone()
+    if what == 2.0 ** 16:
+        q[:, bad] = (q[:, bad].float() * what).to(torch.bfloat16)
+    else:
+        q[:, bad, 5] = what
+    o2, l2 = c.plan(num_sms=8).run(q, c.cache, return_lse=True)
+    out[:, ~bad], lse[:, ~bad] = o2[:, ~bad], l2[:, ~bad]
+    c.check(out, lse)
+    if what == 2.0 ** 16:
+        assert torch.isfinite(o2.float()).all() and torch.isfinite(l2).all()
+    else:
+        assert not torch.isfinite(l2[:, bad]).any()
