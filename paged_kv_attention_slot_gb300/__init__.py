@@ -178,12 +178,21 @@ def _check_device(cache: "KVCache") -> None:
         raise ValueError(f"the cache must be on the current CUDA device, not on {cache.k.device}")
 
 
+def _as_stream(handle: int) -> torch.cuda.Stream:
+    return torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+
+
 def _new(shape, dtype, device, stream) -> torch.Tensor:
-    """An output tensor whose memory belongs to the stream that will write it."""
-    if stream is not None and isinstance(stream, torch.cuda.Stream):
-        with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype, device=device)
-    return torch.empty(shape, dtype=dtype, device=device)
+    """A tensor whose memory belongs to the stream that will write it: a block that the current stream has freed
+    may still be in use there.  Its reader is taken to be the current stream, whose work on it then delays
+    the memory's next use."""
+    if stream is None or int(stream.cuda_stream) == _stream_ptr(None):
+        return torch.empty(shape, dtype=dtype, device=device)
+    reader = torch.cuda.current_stream()
+    with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else _as_stream(int(stream.cuda_stream))):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(reader)
+    return t
 
 
 def _check_scores(scores: torch.Tensor, cache: KVCache) -> int:
@@ -280,7 +289,9 @@ class Plan:
         check(lib().pkv_plan_create(C.byref(h)))
         self._h = h
         self.workspace = None
+        self._own_workspace = True  # allocated here, not given by the caller
         self.scratch = None  # of scored runs
+        self._streams = set()  # handles of the streams the plan's own buffers are recorded on
         self.scored = False
         self.mode = None
         self._keep = None
@@ -292,6 +303,21 @@ class Plan:
                 self._h = None
         except Exception:
             pass
+
+    def _buffer(self, num_bytes: int, stream, device="cuda") -> torch.Tensor:
+        """A new workspace or scratch for work on `stream`."""
+        self._streams.clear()  # it is recorded on none
+        return _new((num_bytes,), torch.uint8, device, stream)
+
+    def _use(self, handle: int) -> int:
+        """The plan's own buffers are about to be used on this stream: their memory is not given away before
+        that work is done.  (Not for a captured run: a graph's replays are the caller's to keep buffers for.)"""
+        if handle not in self._streams and not torch.cuda.is_current_stream_capturing():
+            self._streams.add(handle)
+            for t in (self.workspace if self._own_workspace else None, self.scratch):
+                if t is not None:
+                    t.record_stream(_as_stream(handle))
+        return handle
 
     @staticmethod
     def _args(qo_indptr, kv_indptr, kv_indices, last_page_len, num_qo_heads, num_kv_heads, head_dim, page_size,
@@ -332,18 +358,19 @@ class Plan:
             check(lib().pkv_attn_plan(self._h, C.byref(a), None, 0, None))
         else:
             if workspace is not None:
-                self.workspace = workspace
+                self.workspace, self._own_workspace = workspace, False
             if self.workspace is None:
-                self.workspace = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+                self.workspace = self._buffer(1 << 20, stream)
             st = lib().pkv_attn_plan(self._h, C.byref(a), self.workspace.data_ptr(), self.workspace.numel(),
-                                     _stream_ptr(stream))
+                                     self._use(_stream_ptr(stream)))
             if st == _lib.PKV_EWORKSPACE and workspace is None:
                 # grow the binding-owned workspace and plan again
                 n = C.c_size_t(0)
                 check(lib().pkv_plan_workspace_size(C.byref(a), C.byref(n)))
-                self.workspace = torch.empty(int(n.value) + (int(n.value) >> 2), dtype=torch.uint8, device="cuda")
+                self.workspace = self._buffer(int(n.value) + (int(n.value) >> 2), stream)
+                self._own_workspace = True
                 st = lib().pkv_attn_plan(self._h, C.byref(a), self.workspace.data_ptr(), self.workspace.numel(),
-                                         _stream_ptr(stream))
+                                         self._use(_stream_ptr(stream)))
             check(st)
         self.scored = False
         self.mode = mode
@@ -359,9 +386,7 @@ class Plan:
             check(lib().pkv_attn_scored_scratch_size(self._h, C.byref(n)))
             if not host_only and (self.scratch is None or self.scratch.numel() < n.value
                                   or self.scratch.device != self.workspace.device):
-                self._scratch_stream = _stream_ptr(None)
-                self.scratch = torch.empty(int(n.value) + (int(n.value) >> 2), dtype=torch.uint8,
-                                           device=self.workspace.device)
+                self.scratch = self._buffer(int(n.value) + (int(n.value) >> 2), stream, self.workspace.device)
             self.scored = True
         return self
 
@@ -376,15 +401,15 @@ class Plan:
         check(lib().pkv_plan_work_items(self._h, _ptr(out), out.size))
         return out[: n * 8].reshape(n, 8)
 
-    def _outputs(self, q, out, lse, return_lse):
+    def _outputs(self, q, out, lse, return_lse, stream=None):
         if q.dtype != torch.bfloat16 or not q.is_contiguous():
             raise ValueError("q must be a contiguous bf16 tensor")
         if q.shape != (self.total_tokens, self.num_qo_heads, self.head_dim):
             raise ValueError(f"q must be [{self.total_tokens}, {self.num_qo_heads}, {self.head_dim}]")
         if out is None:
-            out = torch.empty_like(q)
+            out = torch.empty_like(q) if stream is None else _new(q.shape, q.dtype, q.device, stream)
         if lse is None and return_lse:
-            lse = torch.empty((self.total_tokens, self.num_qo_heads), dtype=torch.float32, device=q.device)
+            lse = _new((self.total_tokens, self.num_qo_heads), torch.float32, q.device, stream)
         return out, lse
 
     def _check_tensors(self, q, out, lse, cache):
@@ -410,9 +435,9 @@ class Plan:
                 raise ValueError(f"{name} must be a contiguous bf16 tensor")
             if tuple(t.shape) != (self.kv_rows, self.num_kv_heads, self.head_dim):
                 raise ValueError(f"{name} must be [{self.kv_rows}, {self.num_kv_heads}, {self.head_dim}]")
-        out, lse = self._outputs(q, out, lse, return_lse)
+        out, lse = self._outputs(q, out, lse, return_lse, stream)
         check(lib().pkv_attn_ragged_run(self._h, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                                        lse.data_ptr() if lse is not None else None, _stream_ptr(stream)))
+                                        lse.data_ptr() if lse is not None else None, self._use(_stream_ptr(stream))))
         return (out, lse) if (return_lse or lse is not None) else out
 
     def run_paged_ragged(self, q: torch.Tensor, cache: KVCache, k_new: torch.Tensor, v_new: torch.Tensor,
@@ -428,10 +453,10 @@ class Plan:
                 raise ValueError(f"{name} must be a contiguous bf16 tensor")
             if tuple(t.shape) != (self.total_tokens, self.num_kv_heads, self.head_dim):
                 raise ValueError(f"{name} must be [{self.total_tokens}, {self.num_kv_heads}, {self.head_dim}]")
-        out, lse = self._outputs(q, out, lse, return_lse)
+        out, lse = self._outputs(q, out, lse, return_lse, stream)
         check(lib().pkv_attn_paged_ragged_run(self._h, q.data_ptr(), C.byref(cache.struct), k_new.data_ptr(),
                                               v_new.data_ptr(), out.data_ptr(),
-                                              lse.data_ptr() if lse is not None else None, _stream_ptr(stream)))
+                                              lse.data_ptr() if lse is not None else None, self._use(_stream_ptr(stream))))
         return (out, lse) if (return_lse or lse is not None) else out
 
     def run(self, q: torch.Tensor, cache: KVCache, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
@@ -459,16 +484,13 @@ class Plan:
                 raise ValueError("merge_into needs a prefill plan and the held state in out and lse")
             self._outputs(q, out, lse, True)
             check(lib().pkv_attn_prefill_run_merge(self._h, q.data_ptr(), C.byref(cache.struct), out.data_ptr(),
-                                                   lse.data_ptr(), _stream_ptr(stream)))
+                                                   lse.data_ptr(), self._use(_stream_ptr(stream))))
             return out, lse
         if scores is not None or cache.dtype == _lib.PKV_NVFP4:
             self._check_tensors(q, out, lse, cache)
-        out, lse = self._outputs(q, out, lse, return_lse)
+        out, lse = self._outputs(q, out, lse, return_lse, stream)
+        s = self._use(_stream_ptr(stream))
         if scores is not None:
-            s = _stream_ptr(stream)
-            if s != self._scratch_stream and not torch.cuda.is_current_stream_capturing():
-                # used off the stream it was allocated on: its memory is not reused before this run is done
-                self.scratch.record_stream(torch.cuda.ExternalStream(s) if s else torch.cuda.default_stream())
             check(lib().pkv_attn_decode_run_scored(
                 self._h, q.data_ptr(), C.byref(cache.struct), out.data_ptr(), lse.data_ptr() if lse is not None else None,
                 addr, self.scratch.data_ptr(), self.scratch.numel(), s))
@@ -481,9 +503,8 @@ class Plan:
             fns = [lib().pkv_attn_prefill_run]
         for fn in fns:
             check(fn(self._h, q.data_ptr(), C.byref(cache.struct), out.data_ptr(),
-                     lse.data_ptr() if lse is not None else None, _stream_ptr(stream)))
+                     lse.data_ptr() if lse is not None else None, s))
         return (out, lse) if (return_lse or lse is not None) else out
-
 
     def evict(self, cache: KVCache, scores: torch.Tensor, budget: int, num_sink: int = 0, num_recent: int = 0,
               kept: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -509,7 +530,7 @@ class Plan:
               or kept.get_device() != cache._device_index):
             raise ValueError(f"kept must be a contiguous int32 tensor {list(shape)} on the cache's device")
         check(lib().pkv_kv_evict(self._h, C.byref(cache.struct), addr, budget, num_sink, num_recent, kept.data_ptr(),
-                                 _stream_ptr(stream)))
+                                 self._use(_stream_ptr(stream))))
         return kept
 
 
@@ -553,10 +574,12 @@ class CascadePlan:
             return_lse: bool = False, stream=None):
         """pkv_cascade_run: the suffix plan into (out, lse), then the shared pass merged into them."""
         if lse is None:
-            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-        out, lse = self.suffix._outputs(q, out, lse, True)
+            lse = _new(q.shape[:2], torch.float32, q.device, stream)
+        out, lse = self.suffix._outputs(q, out, lse, True, stream)
+        s = _stream_ptr(stream)
+        self.shared._use(s)
         check(lib().pkv_cascade_run(self.shared._h, self.suffix._h, q.data_ptr(), C.byref(cache.struct),
-                                    out.data_ptr(), lse.data_ptr(), _stream_ptr(stream)))
+                                    out.data_ptr(), lse.data_ptr(), self.suffix._use(s)))
         return (out, lse) if return_lse else out
 
 
@@ -575,9 +598,9 @@ def merge_state(o_a: torch.Tensor, lse_a: torch.Tensor, o_b: torch.Tensor, lse_b
         if t.dtype != torch.float32 or not t.is_contiguous():
             raise ValueError("lse_a and lse_b must be contiguous float32 tensors")
     if out is None:
-        out = torch.empty_like(o_a)
+        out = _new(o_a.shape, o_a.dtype, o_a.device, stream)
     if lse_out is None:
-        lse_out = torch.empty_like(lse_a)
+        lse_out = _new(lse_a.shape, lse_a.dtype, lse_a.device, stream)
     check(lib().pkv_merge_state(o_a.data_ptr(), lse_a.data_ptr(), o_b.data_ptr(), lse_b.data_ptr(), out.data_ptr(),
                                 lse_out.data_ptr(), lse_a.numel(), o_a.shape[-1], _stream_ptr(stream)))
     return out, lse_out

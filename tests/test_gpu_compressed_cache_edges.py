@@ -116,3 +116,33 @@ def test_a_head_does_not_depend_on_its_neighbours(dtype, heads, kv_heads, what):
         assert torch.isfinite(o2.float()).all() and torch.isfinite(l2).all()
     else:
         assert not torch.isfinite(l2[:, bad]).any()
+
+
+# ------------------------------------------------------------------------------------------------
+# streams
+# ------------------------------------------------------------------------------------------------
+def test_memory_for_work_on_another_stream_is_not_taken_from_the_current_one():
+    # a block that the current stream has just freed may still be in use there: the plan's workspace and
+    # scratch and a run's outputs, all written on `side`, must not be given it
+    pk = _pk()
+    c = Case([700, 45], 32, 8, 16, "nvfp4", seed=32)
+    side = torch.cuda.Stream()
+    c.plan(scored=True).run(c.q, c.cache, return_lse=True, scores=torch.zeros((c.cache.num_pages, 8, 16), device="cuda"))
+    scores = torch.zeros((c.cache.num_pages, 8, 16), device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    sizes = [1 << 20, 800 * 32 * 4 * 5 // 4, c.q.numel() * 2, c.q.shape[0] * 32 * 4]
+    held = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(3)]
+    spans = [(t.data_ptr(), t.data_ptr() + t.numel()) for t in held]
+    del held  # the current stream's free blocks
+    side.wait_stream(torch.cuda.current_stream())
+    b = c.b
+    p = pk.Plan().plan(b.qo_indptr, b.kv_indptr, b.kv_indices, b.last_page_len, num_qo_heads=32, num_kv_heads=8, head_dim=128,
+                       page_size=16, kv_dtype="nvfp4", scored=True, stream=side)
+    out, lse = p.run(c.q, c.cache, return_lse=True, scores=scores, stream=side)
+    kept = p.evict(c.cache, scores, 100, stream=side)
+    k, v = pk.kv_load(torch.arange(8, device="cuda"), c.cache, stream=side)
+    for name, t in dict(workspace=p.workspace, scratch=p.scratch, out=out, lse=lse, kept=kept, k=k, v=v).items():
+        assert not any(lo <= t.data_ptr() < hi for lo, hi in spans), name
+    torch.cuda.current_stream().wait_stream(side)
+    c.check(out, lse)
