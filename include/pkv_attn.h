@@ -309,7 +309,7 @@ int pkv_attn_prefill_run(const pkv_plan* plan, const void* q, const pkv_cache* c
  *   scratch  device, 256-byte aligned, >= pkv_attn_scored_scratch_size() bytes: the scaled scores of the
  *            visible keys, written and read within the call; under the same rules as the plan workspace.
  * No page may be listed twice in the plan's kv_indices (a shared page would be updated by two requests
- * at once): PKV_EINVAL.
+ * at once): PKV_EINVAL.  At most 12288 query heads per KV head.
  */
 int pkv_attn_decode_run_scored(const pkv_plan* plan, const void* q, const pkv_cache* cache, void* o, float* lse,
                                float* scores, void* scratch, size_t scratch_bytes, void* stream);

@@ -942,6 +942,8 @@ int pkv_attn_scored_scratch_size(const pkv_plan* plan, size_t* bytes) {
   if (!plan || !plan->valid) return fail(PKV_EINVAL, "plan is NULL or has not been planned");
   if (plan->mode != PKV_MODE_DECODE && plan->mode != PKV_MODE_MIXED)
     return fail(PKV_EINVAL, "accumulated scores need a PKV_MODE_DECODE or PKV_MODE_MIXED plan");
+  if (plan->Hq / plan->Hkv > pkv::kScoredMaxGroup)
+    return fail(PKV_EUNSUPPORTED, "accumulated scores cover up to " + std::to_string(pkv::kScoredMaxGroup) + " query heads per KV head");
   int st = check_pages_unique(plan);
   if (st != PKV_OK) return st;
   *bytes = pkv::scored_lse_offset(plan) + (size_t)plan->total_tokens * plan->Hq * sizeof(float);

@@ -17,6 +17,7 @@ namespace pkv {
 namespace {
 
 constexpr int kScoreThreads = 256;
+static_assert(kScoredMaxGroup * sizeof(float) <= 48 << 10, "s_lse fits the shared memory of a plain launch");
 constexpr int kScoreUnroll = 2;  // groups of four keys in flight per thread
 
 __global__ void __launch_bounds__(kScoreThreads) score_add_kernel(const RunParams p) {

@@ -141,6 +141,7 @@ constexpr int32_t kEvictMaxLen = 1 << 21;  // longest request the eviction kerne
 cudaError_t launch_decode(const RunParams& p, int kv_dtype, cudaStream_t s);
 // decode and the score update; any_split: some unit is shared by several CTAs
 cudaError_t launch_decode_scored(const RunParams& p, int kv_dtype, bool any_split, cudaStream_t s);
+constexpr int kScoredMaxGroup = 12288;  // query heads per KV head whose log-sum-exps fit 48 KB of shared memory
 int decode_ctas_per_sm(int kv_dtype, int head_dim, int group);  // resident decode CTAs per SM
 cudaError_t launch_prefill(const RunParams& p, const void* tmap_q, const void* tmap_o, int64_t total_tokens,
                            cudaStream_t s);
