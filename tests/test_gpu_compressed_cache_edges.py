@@ -7,8 +7,9 @@ import pytest
 import torch
 
 from oracle import attention as OA
+from oracle import eviction as OE
 from oracle import nvfp4 as O4
-from tests.test_gpu_compressed_cache import Case, _np, _pk
+from tests.test_gpu_compressed_cache import Case, _check_evict, _check_scores, _np, _pk
 
 pytestmark = pytest.mark.gpu
 
@@ -146,3 +147,153 @@ def test_memory_for_work_on_another_stream_is_not_taken_from_the_current_one():
         assert not any(lo <= t.data_ptr() < hi for lo, hi in spans), name
     torch.cuda.current_stream().wait_stream(side)
     c.check(out, lse)
+
+
+# ------------------------------------------------------------------------------------------------
+# eviction with more units than run at once
+# ------------------------------------------------------------------------------------------------
+def _many(units_per_sm):
+    """Requests (of 8 KV heads) so that there are more than this many units for each SM."""
+    n = torch.cuda.get_device_properties(0).multi_processor_count
+    return int(units_per_sm * n) // 8 + 1
+
+
+@pytest.mark.parametrize("dtype, D, layout", [("bf16", 64, "nhd"), ("bf16", 128, "hnd"), ("e4m3", 128, "nhd"), ("nvfp4", 128, "hnd"),
+                                              ("nvfp4", 128, "padded")])
+@pytest.mark.parametrize("kind, budget, sink, recent", [("heavy", 96, 4, 16), ("ties", 100, 0, 90), ("wild", 33, 1, 0)])
+def test_evict_by_one_cta_per_unit(dtype, D, layout, kind, budget, sink, recent):
+    # more than 2.5 units per SM: a unit has one CTA, which moves K, V, both block scales and the scores
+    n = _many(2.5)
+    lens = [101 + 13 * (i % 9) for i in range(n)]
+    assert min(lens) > budget and 2 * n * 8 > 5 * torch.cuda.get_device_properties(0).multi_processor_count
+    _check_evict(lens, 8, 16, dtype, budget, sink, recent, kind=kind, D=D, layout=layout, seed=n)
+
+
+def test_evict_by_one_cta_per_unit_in_several_rounds_of_the_list():
+    # more moves per unit than one list (512) holds
+    n = _many(2.5)
+    _check_evict([1400 + i for i in range(n)], 8, 16, "bf16", 700, 0, 64, kind="wild", D=64, seed=3)
+
+
+# ------------------------------------------------------------------------------------------------
+# very many query heads
+# ------------------------------------------------------------------------------------------------
+def test_scored_decode_of_the_largest_group():
+    c = Case([20, 33], 12288, 1, 16, "bf16", D=64, seed=60)
+    start = torch.rand((c.cache.num_pages, 1, 16), generator=torch.Generator().manual_seed(1)).cuda()
+    scores = start.clone()
+    c.check(*c.plan(scored=True).run(c.q, c.cache, return_lse=True, scores=scores))
+    b = c.b
+    w = np.zeros((c.cache.num_pages, 1, 16))
+    OE.add_weights(w, b.q.double().numpy(), c.K, b.kv_indptr, b.kv_indices, b.last_page_len, b.qo_indptr, 16)
+    # 12288 weights of relative error 2 dx + 2^-19 are added in sequence: their sum is off by at most 12288 * 2^-24
+    # of itself on top
+    ref = _np(start).astype(np.float64) + w
+    tol = w * (2 * c.dx() + 2.0 ** -19 + 12288 * 2.0 ** -24) + 2.0 ** -23 * ref
+    assert np.all(np.abs(_np(scores) - ref) <= tol)
+    assert np.array_equal(_np(scores)[w == 0], _np(start)[w == 0])
+
+
+# ------------------------------------------------------------------------------------------------
+# scores at any 4-byte address
+# ------------------------------------------------------------------------------------------------
+def _unaligned(t):
+    """A contiguous copy that starts 4 bytes past a 16-byte boundary."""
+    u = torch.empty(t.numel() + 4, dtype=t.dtype, device=t.device)[1:t.numel() + 1].view(t.shape)
+    assert u.data_ptr() % 16 == 4 and u.is_contiguous()
+    return u.copy_(t)
+
+
+@pytest.mark.parametrize("sms", [0, 4])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3", "nvfp4"])
+def test_scores_need_not_be_aligned_to_vectors(dtype, sms):
+    # the single-key forms of the score update and of eviction's reads, on pages that vectors would fit
+    pk = _pk()
+    c = Case([700, 45, 130], 16, 2, 16, dtype, seed=61)
+    start = torch.rand((c.cache.num_pages, 2, 16), generator=torch.Generator().manual_seed(1)).cuda()
+    scores = _unaligned(start)
+    p = c.plan(num_sms=sms, scored=True)
+    c.check(*p.run(c.q, c.cache, return_lse=True, scores=scores))
+    _check_scores(c, scores, start)
+    pools = [x.clone() for x in c.pools]
+    aligned = scores.clone()
+    want = p.evict(c.cache, aligned, 100, num_sink=2, num_recent=10)
+    moved = [x.clone() for x in c.pools]
+    for x, y in zip(c.pools, pools):
+        x.copy_(y)
+    assert torch.equal(p.evict(c.cache, scores, 100, num_sink=2, num_recent=10), want)
+    assert torch.equal(scores, aligned) and all(torch.equal(x, y) for x, y in zip(c.pools, moved))
+    x = torch.ones((1, 2, 128), dtype=torch.bfloat16, device="cuda")
+    pk.kv_store(x, x, torch.tensor([int(c.b.kv_indices[0]) * 16 + 3], device="cuda"), c.cache, scores=scores)
+    aligned[int(c.b.kv_indices[0]), :, 3] = 0
+    assert torch.equal(scores, aligned)
+
+
+def test_evict_of_a_long_request_with_unaligned_scores():
+    pk = _pk()
+    L, ps, b = 14000, 16, 3000
+    n = -(-L // ps)
+    fresh = torch.rand((n, 1, ps), generator=torch.Generator().manual_seed(2)).cuda()
+    k = torch.randn((n, ps, 1, 64), generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).cuda()
+    plan = pk.Plan().plan([0, 1], [0, n], np.arange(n), [L - (n - 1) * ps], num_qo_heads=1, num_kv_heads=1, head_dim=64, page_size=ps)
+    got = []
+    for s in (fresh.clone(), _unaligned(fresh)):
+        cache = pk.KVCache(k.clone(), -k)
+        kept = plan.evict(cache, s, b, num_sink=4, num_recent=100)
+        got.append((kept, s.clone(), cache.k, cache.v))
+    assert all(torch.equal(x, y) for x, y in zip(*got))
+
+
+# ------------------------------------------------------------------------------------------------
+# two calls at once
+# ------------------------------------------------------------------------------------------------
+def test_layers_evicted_at_once_on_one_plan():
+    # eviction only reads the plan: the layers of a step may be evicted side by side
+    pk = _pk()
+    c = Case([3000, 900, 2000], 8, 8, 16, "bf16", seed=62)
+    p = c.plan()
+    layers = []
+    for i in range(4):
+        g = torch.Generator().manual_seed(i)
+        scores = torch.rand((c.cache.num_pages, 8, 16), generator=g).cuda()
+        pools = [x.clone().mul_(i + 1) for x in c.pools]
+        layers.append((pk.KVCache(*pools), scores, [x.clone() for x in pools], scores.clone()))
+    want = []
+    for cache, scores, pools, fresh in layers:
+        kept = p.evict(cache, scores, 800, num_sink=4, num_recent=64)
+        want.append((kept, scores.clone(), cache.k.clone(), cache.v.clone()))
+        cache.k.copy_(pools[0])
+        cache.v.copy_(pools[1])
+        scores.copy_(fresh)
+    streams = [torch.cuda.Stream() for _ in layers]
+    torch.cuda.synchronize()
+    kept = [p.evict(cache, scores, 800, num_sink=4, num_recent=64, stream=s) for (cache, scores, _, _), s in zip(layers, streams)]
+    torch.cuda.synchronize()
+    for (cache, scores, _, _), k, w in zip(layers, kept, want):
+        assert all(torch.equal(x, y) for x, y in zip((k, scores, cache.k, cache.v), w))
+
+
+# ------------------------------------------------------------------------------------------------
+# more rows than one launch indexes
+# ------------------------------------------------------------------------------------------------
+def test_store_and_load_of_more_rows_than_one_launch_covers():
+    # 2^26 (token, head) rows per launch; the token behind them goes with a second one
+    pk = _pk()
+    H, T = 65536, 1026
+    x = torch.empty((T, H, 128), dtype=torch.bfloat16, device="cuda")
+    row = torch.randn((H, 128), generator=torch.Generator().manual_seed(4)).to(torch.bfloat16).cuda()
+    for t in range(T):
+        x[t] = row.roll(t, 0)
+    cache = pk.KVCache.nvfp4(T, 1, H, 128, 0.002, 0.002)
+    slots = torch.arange(T, device="cuda").flip(0).contiguous()
+    pk.kv_store(x, x, slots, cache)
+    k, v = pk.kv_load(slots, cache)
+    one = pk.KVCache.nvfp4(1, 1, H, 128, 0.002, 0.002)
+    zero = torch.zeros(1, dtype=torch.int64, device="cuda")
+    for t in (0, 1, 500, 1022, 1023, 1024, 1025):
+        pk.kv_store(x[t:t + 1], x[t:t + 1], zero, one)
+        a = pk.kv_load(zero, one)[0][0]
+        assert torch.equal(cache.k[T - 1 - t, 0], one.k[0, 0]) and torch.equal(cache.v_sf[T - 1 - t, 0], one.v_sf[0, 0])
+        assert torch.equal(k[t], a) and torch.equal(v[t], a)
+    del x, k, v, cache
+    torch.cuda.empty_cache()
