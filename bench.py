@@ -55,7 +55,7 @@ def _src_hash(*names):
     return h.hexdigest()[:16]
 
 
-DECODE_SOURCES = ["decode.cu", "ptx.cuh", "pkv_internal.h"]
+DECODE_SOURCES = ["decode.cu", "decode_kernel.cuh", "ptx.cuh", "pkv_internal.h"]
 # the workload both arms name in `config` (the oracle arm times the step's attention on a bounded sample
 # of its requests, stated in its `cpu_baseline.sample`)
 DECODE_WORKLOAD = ("llama8b_decode: batch 64, 32 q / 8 kv heads, head_dim 128, bf16 KV, KV length U[512,4096], "
