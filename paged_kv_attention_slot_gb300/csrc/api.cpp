@@ -1018,7 +1018,6 @@ int pkv_kv_evict(const pkv_plan* plan, const pkv_cache* cache, float* scores, in
   p.sf_page_b = rp.sf_page_b;
   p.sf_token_b = rp.sf_token_b;
   p.sf_head_b = rp.sf_head_b;
-  p.num_pages = cache->num_pages;
   p.scores = scores;
   p.kept = kept;
   p.page_size = plan->ps;

@@ -10,10 +10,10 @@
 // GB300 design.  Decode is HBM-bound (about G flops per byte of KV), so the kernel is built around
 // streaming the pages at full bandwidth while keeping the per-key work short:
 //  * one CTA = 4 warps = one work item (request, KV head, group of <= 16 query heads) with a key
-//    range; a range short enough for one CTA is read by it alone (each warp takes every 4th 16-key
-//    tile), a long one is shared by several CTAs whose warps claim 32-key groups of it from a
-//    per-range counter at run time, so the CTAs of a range finish together;
-//  * every warp runs its own cp.async ring (16 keys per stage, K and V rows gathered page by page
+//    range; a range short enough for one CTA is read by it alone (each warp takes every 4th tile of
+//    16 keys, NVFP4: 32), a long one is shared by several CTAs whose warps claim groups of two tiles
+//    from a per-range counter at run time, so the CTAs of a range finish together;
+//  * every warp runs its own cp.async ring (a tile per stage, K and V rows gathered page by page
 //    through kv_indices, 16-byte vectors, XOR-swizzled so ldmatrix reads are conflict-free), so no
 //    CTA-wide barrier sits in the main loop;
 //  * the products run on m16n8k16 tensor-core MMAs with the KEYS in M and the (<= 8 per n-block)
@@ -21,8 +21,14 @@
 //    per KV head, a 16-key tile costs 8 MMAs per product (not 16 with heads in M), and the output
 //    accumulator is 32 registers per 8 heads.  P^T goes from the accumulator layout of the first MMA
 //    to the operand layout of the second with one movmatrix.trans per 8x8 block;
-//  * the online softmax runs per head column: a max over the 16 keys of the tile (3 shuffles), base-2
-//    exponentials with the scale folded in, running sums kept per lane and reduced at the end;
+//  * the online softmax runs per head column: base-2 exponentials with the scale folded in, against a
+//    reference that moves only when a key exceeds it by more than 2^8 (one vote per tile; only then is the
+//    tile's maximum formed across lanes, 3 shuffles), running sums kept per lane and reduced at the end;
+//  * scores, references, sums and outputs are float32; the probabilities enter the second product in the
+//    type its MMA takes beside V: bf16 for bf16 pools, f16 for the others.  That is what the outputs are
+//    off by beyond their own rounding: relative to a 64-bit result the bf16 outputs by 0.0023 and the NVFP4
+//    and E4M3 ones by 0.0017, where 32 bits throughout, rounded once, are off by 0.0017 (batches of 64).
+//    Keeping more would take a second product per tile for the rest of the bits;
 //  * FP8 (E4M3) pages are widened to f16 in registers (exact); the K scale is folded into the score
 //    scale and the V scale into the output; the head-dim order inside each 16-element block is
 //    permuted identically for Q and K (a dot product does not depend on order) so one ldmatrix feeds
@@ -278,7 +284,7 @@ __device__ __forceinline__ void merge_accumulate(float4 (&acc)[NA], const int (&
 }
 
 // SCORED: every visible key's scaled score (log2 units) goes to p.logits, each row's log2-sum-exp to
-// p.lse2 (for the accumulated attention weights, score_add.cu).
+// p.lse2 (for the accumulated attention weights, decode_scored.cu).
 template <int D, int KV, int NB, int HPB, bool SCORED>
 __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB, HPB>::CTAS) decode_kernel(const RunParams p, int32_t* err) {
   using C = DecodeCfg<D, KV, NB, HPB>;
@@ -1143,8 +1149,9 @@ static cudaError_t launch_decode_any(const RunParams& p, int kv_dtype, cudaStrea
   if (kv_dtype == PKV_FP8_E4M3 || kv_dtype == PKV_NVFP4) {
     if (p.head_dim != 128) return cudaErrorInvalidValue;
     // NVFP4: up to 4 query heads the pair form fills the 8 columns (4 heads: 64 requests of 512-4096 keys
-    // 41.8 us against 48.8 in the 8-head form, 2 x 131072 keys 59.6 against 68.9); for 5 to 8 heads it
-    // needs a second n-block and loses (8 heads, 256 ragged requests: 119 against 106 us)
+    // 39.4 us against 46.7 in the 8-head form, 2 x 131072 keys 54.9 against 64.9); for 5 to 8 heads it
+    // needs a second n-block and loses (8 heads: 64 requests 53.0 against 48.9, 2 x 131072 keys 75.8
+    // against 69.3, 256 ragged requests 112.5 against 100.0)
     if (kv_dtype == PKV_NVFP4)
       return p.group <= 4 ? launch_decode_t<128, PKV_NVFP4, 1, 4, SCORED>(p, s)
              : !nb2       ? launch_decode_t<128, PKV_NVFP4, 1, 8, SCORED>(p, s)

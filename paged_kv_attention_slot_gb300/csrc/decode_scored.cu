@@ -8,7 +8,8 @@
 // beside the 512 of a bf16 key row pair at 4 query heads per KV head) in a scratch that mostly stays in
 // L2.  A CTA that read a whole unit turns its scores into weights itself when it knows lse; for units
 // shared by several CTAs the kernel below does it, on the decode's own work list: a CTA takes the keys
-// its decode CTA would take on an even split.  Either way every score has one owner and needs no atomic.
+// its decode CTA would take on an even split.  Either way one thread makes one addition to a score per launch,
+// so no order of additions matters; it is made at L2 (red.add), so that no thread waits for the old value.
 
 #include "decode_kernel.cuh"
 
@@ -22,8 +23,9 @@ constexpr int kScoreUnroll = 2;  // groups of four keys in flight per thread
 
 __global__ void __launch_bounds__(kScoreThreads) score_add_kernel(const RunParams p) {
   extern __shared__ float s_lse[];  // [group] log2-sum-exp of the KV head's query heads
-  // The work list and the page table were written by kernels before the decode run, which waited for them
-  // before this grid could start: they may be read at once, beside the decode's tail.
+  // The work list and the page table were written by kernels that the decode run had waited for before
+  // this grid could start (which is when the decode's last CTA has left: it has no earlier trigger), so
+  // they may be read before the wait for the decode's own writes.
   const WorkItem w = p.work[blockIdx.x];
   const int G = p.group;
   // the first head group's CTAs add all of the KV head's query heads; a unit that one decode CTA read

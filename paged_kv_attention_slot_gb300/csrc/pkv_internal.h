@@ -127,7 +127,6 @@ struct EvictParams {
   char* v_sf;
   int64_t stride_page_b, stride_token_b, stride_head_b;
   int64_t sf_page_b, sf_token_b, sf_head_b;
-  int64_t num_pages;
   float* scores;
   int32_t* kept;
   int32_t page_size;
