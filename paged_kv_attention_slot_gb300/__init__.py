@@ -178,10 +178,6 @@ def _check_device(cache: "KVCache") -> None:
         raise ValueError(f"the cache must be on the current CUDA device, not on {cache.k.device}")
 
 
-def _as_stream(handle: int) -> torch.cuda.Stream:
-    return torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
-
-
 def _new(shape, dtype, device, stream) -> torch.Tensor:
     """A tensor whose memory belongs to the stream that will write it: a block that the current stream has freed
     may still be in use there.  Its reader is taken to be the current stream, whose work on it then delays
@@ -189,7 +185,9 @@ def _new(shape, dtype, device, stream) -> torch.Tensor:
     if stream is None or int(stream.cuda_stream) == _stream_ptr(None):
         return torch.empty(shape, dtype=dtype, device=device)
     reader = torch.cuda.current_stream()
-    with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else _as_stream(int(stream.cuda_stream))):
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream.cuda_stream))
+    with torch.cuda.stream(stream):
         t = torch.empty(shape, dtype=dtype, device=device)
     t.record_stream(reader)
     return t
@@ -309,14 +307,19 @@ class Plan:
         self._streams.clear()  # it is recorded on none
         return _new((num_bytes,), torch.uint8, device, stream)
 
-    def _use(self, handle: int) -> int:
-        """The plan's own buffers are about to be used on this stream: their memory is not given away before
-        that work is done.  (Not for a captured run: a graph's replays are the caller's to keep buffers for.)"""
+    def _use(self, stream) -> int:
+        """Handle of the stream, on which the plan's own buffers are about to be used: their memory is not given
+        away before that work is done.  (Not for a captured run: a graph's replays are the caller's to keep the
+        plan for.  Nor on a stream that is not torch's, which may be gone when the memory is given back.)"""
+        handle = _stream_ptr(stream)
         if handle not in self._streams and not torch.cuda.is_current_stream_capturing():
             self._streams.add(handle)
-            for t in (self.workspace if self._own_workspace else None, self.scratch):
-                if t is not None:
-                    t.record_stream(_as_stream(handle))
+            s = torch.cuda.current_stream() if stream is None else stream
+            # (the id of a stream from elsewhere is its handle)
+            if isinstance(s, torch.cuda.Stream) and (s.stream_id != handle or handle == 0):
+                for t in (self.workspace if self._own_workspace else None, self.scratch):
+                    if t is not None:
+                        t.record_stream(s)
         return handle
 
     @staticmethod
@@ -362,7 +365,7 @@ class Plan:
             if self.workspace is None:
                 self.workspace = self._buffer(1 << 20, stream)
             st = lib().pkv_attn_plan(self._h, C.byref(a), self.workspace.data_ptr(), self.workspace.numel(),
-                                     self._use(_stream_ptr(stream)))
+                                     self._use(stream))
             if st == _lib.PKV_EWORKSPACE and workspace is None:
                 # grow the binding-owned workspace and plan again
                 n = C.c_size_t(0)
@@ -370,7 +373,7 @@ class Plan:
                 self.workspace = self._buffer(int(n.value) + (int(n.value) >> 2), stream)
                 self._own_workspace = True
                 st = lib().pkv_attn_plan(self._h, C.byref(a), self.workspace.data_ptr(), self.workspace.numel(),
-                                         self._use(_stream_ptr(stream)))
+                                         self._use(stream))
             check(st)
         self.scored = False
         self.mode = mode
@@ -437,7 +440,7 @@ class Plan:
                 raise ValueError(f"{name} must be [{self.kv_rows}, {self.num_kv_heads}, {self.head_dim}]")
         out, lse = self._outputs(q, out, lse, return_lse, stream)
         check(lib().pkv_attn_ragged_run(self._h, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                                        lse.data_ptr() if lse is not None else None, self._use(_stream_ptr(stream))))
+                                        lse.data_ptr() if lse is not None else None, self._use(stream)))
         return (out, lse) if (return_lse or lse is not None) else out
 
     def run_paged_ragged(self, q: torch.Tensor, cache: KVCache, k_new: torch.Tensor, v_new: torch.Tensor,
@@ -456,7 +459,7 @@ class Plan:
         out, lse = self._outputs(q, out, lse, return_lse, stream)
         check(lib().pkv_attn_paged_ragged_run(self._h, q.data_ptr(), C.byref(cache.struct), k_new.data_ptr(),
                                               v_new.data_ptr(), out.data_ptr(),
-                                              lse.data_ptr() if lse is not None else None, self._use(_stream_ptr(stream))))
+                                              lse.data_ptr() if lse is not None else None, self._use(stream)))
         return (out, lse) if (return_lse or lse is not None) else out
 
     def run(self, q: torch.Tensor, cache: KVCache, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
@@ -484,12 +487,12 @@ class Plan:
                 raise ValueError("merge_into needs a prefill plan and the held state in out and lse")
             self._outputs(q, out, lse, True)
             check(lib().pkv_attn_prefill_run_merge(self._h, q.data_ptr(), C.byref(cache.struct), out.data_ptr(),
-                                                   lse.data_ptr(), self._use(_stream_ptr(stream))))
+                                                   lse.data_ptr(), self._use(stream)))
             return out, lse
         if scores is not None or cache.dtype == _lib.PKV_NVFP4:
             self._check_tensors(q, out, lse, cache)
         out, lse = self._outputs(q, out, lse, return_lse, stream)
-        s = self._use(_stream_ptr(stream))
+        s = self._use(stream)
         if scores is not None:
             check(lib().pkv_attn_decode_run_scored(
                 self._h, q.data_ptr(), C.byref(cache.struct), out.data_ptr(), lse.data_ptr() if lse is not None else None,
@@ -530,7 +533,7 @@ class Plan:
               or kept.get_device() != cache._device_index):
             raise ValueError(f"kept must be a contiguous int32 tensor {list(shape)} on the cache's device")
         check(lib().pkv_kv_evict(self._h, C.byref(cache.struct), addr, budget, num_sink, num_recent, kept.data_ptr(),
-                                 self._use(_stream_ptr(stream))))
+                                 self._use(stream)))
         return kept
 
 
@@ -576,10 +579,9 @@ class CascadePlan:
         if lse is None:
             lse = _new(q.shape[:2], torch.float32, q.device, stream)
         out, lse = self.suffix._outputs(q, out, lse, True, stream)
-        s = _stream_ptr(stream)
-        self.shared._use(s)
+        self.shared._use(stream)
         check(lib().pkv_cascade_run(self.shared._h, self.suffix._h, q.data_ptr(), C.byref(cache.struct),
-                                    out.data_ptr(), lse.data_ptr(), self.suffix._use(s)))
+                                    out.data_ptr(), lse.data_ptr(), self.suffix._use(stream)))
         return (out, lse) if return_lse else out
 
 

@@ -2,6 +2,8 @@
 
 Tolerances are those of tests/test_gpu_compressed_cache.py (derived in its docstring)."""
 
+import ctypes as C
+
 import numpy as np
 import pytest
 import torch
@@ -147,6 +149,49 @@ def test_memory_for_work_on_another_stream_is_not_taken_from_the_current_one():
         assert not any(lo <= t.data_ptr() < hi for lo, hi in spans), name
     torch.cuda.current_stream().wait_stream(side)
     c.check(out, lse)
+
+
+def test_a_stream_from_elsewhere_may_be_gone_before_the_plan():
+    c = Case([700, 45], 32, 8, 16, "nvfp4", seed=32)
+    scores = torch.zeros((c.cache.num_pages, 8, 16), device="cuda")
+    rt = torch.cuda.cudart()
+    handle = C.c_uint64(0)
+    assert int(rt.cudaStreamCreate(C.addressof(handle))) == 0
+    ext = torch.cuda.ExternalStream(handle.value)
+    ext.wait_stream(torch.cuda.current_stream())
+    p = c.plan(scored=True, stream=ext)
+    out, lse = p.run(c.q, c.cache, return_lse=True, scores=scores, stream=ext)
+    with torch.cuda.stream(ext):
+        out2 = p.run(c.q, c.cache)
+    ext.synchronize()
+    c.check(out, lse)
+    c.check(out2, lse)
+    assert int(rt.cudaStreamDestroy(handle.value)) == 0
+    del p, out, lse, out2  # their memory goes back without a look at the stream
+    again = torch.empty(8 << 20, dtype=torch.uint8, device="cuda").zero_()
+    torch.cuda.synchronize()
+    assert not again.any()
+
+
+def test_runs_on_a_side_stream_inside_a_capture():
+    c = Case([700, 45, 2000], 32, 8, 16, "nvfp4", seed=33)
+    p = c.plan(num_sms=40, scored=True)
+    scores = torch.zeros((c.cache.num_pages, 8, 16), device="cuda")
+    p.run(c.q, c.cache, scores=scores)
+    scores.zero_()
+    torch.cuda.synchronize()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        out, lse = p.run(c.q, c.cache, return_lse=True, scores=scores, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        total = out.float().sum()
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    c.check(out, lse)
+    _check_scores(c, scores, torch.zeros_like(scores), times=2)
+    assert torch.isfinite(total)
 
 
 # ------------------------------------------------------------------------------------------------
