@@ -343,6 +343,121 @@ int pkv_attn_scored_scratch_size(const pkv_plan* plan, size_t* bytes);
 int pkv_kv_evict(const pkv_plan* plan, const pkv_cache* cache, float* scores, int32_t budget, int32_t num_sink,
                  int32_t num_recent, int32_t* kept, void* stream);
 
+/* ---------------------------------------------------------------------------------------------- */
+/* a decode step that reads only the pages that matter                                              */
+/* ---------------------------------------------------------------------------------------------- */
+/*
+ * (The pages have no counterpart for these calls: additions of this library.)  With long contexts a decode step's
+ * time is the reading of its keys.  The calls below leave every key in the cache and read, per token and KV head,
+ * only the pages whose keys can matter to it, found by a cheap score over 8-bit bounds of each page's keys:
+ *   once per batch      pkv_attn_plan_blocks, pkv_token_map
+ *   once per layer      pkv_rope_kv_store, pkv_key_bounds_update, pkv_block_select, pkv_attn_decode_run_blocks
+ * "Block" b of a request is the b-th page of its page list.  Pages of at least 8 tokens; requests of up to 49152
+ * pages; at most 128 query heads per KV head.
+ */
+
+/*
+ * pkv_token_map: positions and slots of the planned new tokens, from the plan's own metadata on the device.  Token t of
+ * request i sits at key P = L_i - n_i + t:  slot_mapping = page(P / page_size) * page_size + P % page_size,
+ * positions = P + offsets[i].
+ *   plan      PKV_MODE_DECODE, PKV_MODE_PREFILL or PKV_MODE_MIXED, causal.
+ *   offsets   device int64 [batch_size] or NULL (0): what a request's positions are ahead of its keys, e.g. the keys
+ *             that pkv_kv_evict dropped.
+ *   positions, slot_mapping  device int64 [total_tokens] (out).
+ */
+int pkv_token_map(const pkv_plan* plan, const int64_t* offsets, int64_t* positions, int64_t* slot_mapping, void* stream);
+
+/*
+ * pkv_rope_kv_store: rotary positions of this step's q and k, and the KV write (pkv_kv_store), in one launch.  For a
+ * token at position P, with angle a_i = P f_i for pair i of a head's first rotary_dim elements,
+ *   (x1, x2) -> amplitude * (x1 cos a_i - x2 sin a_i, x2 cos a_i + x1 sin a_i),
+ * pair i being elements (i, i + rotary_dim / 2), or (2 i, 2 i + 1) where `interleaved`; elements from rotary_dim on
+ * pass through, v is not turned.  Float32, rounded to bf16 once; the pool gets what pkv_kv_store makes of that key.
+ *   q        device bf16 [num_tokens, num_qo_heads, head_dim], k and v device bf16 [num_tokens, num_kv_heads, head_dim], any token and
+ *            head strides that are multiples of 8 elements (views of one projection's output), 16-byte aligned.
+ *   q_out    device bf16, contiguous (out); may be q where q is contiguous.  k_out: the turned keys, contiguous, or NULL;
+ *            may be k where k is contiguous.  No other overlap.
+ *   positions     device int64 [num_tokens], any value.
+ *   slot_mapping  as pkv_kv_store: negative = not written to the pool (q_out and k_out are), out of range = not written
+ *                 and recorded as PKV_DEVERR_SLOT_RANGE; no slot twice.
+ *   phase_step    device uint64 [rotary_dim / 2]: f_i / (2 pi) as a fraction of 2^64, so that phase = position *
+ *                 step modulo 2^64 is exact; its top 32 bits are used (2^-32 of a turn).
+ *   amplitude     factor of the turned elements (1 without a scaling that asks for another).
+ *   scores        as pkv_kv_store_scored, or NULL.
+ * rotary_dim: a multiple of 16 up to head_dim.  num_tokens == 0 is a no-op.
+ */
+typedef struct pkv_rope_args {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  void* k_out;
+  const int64_t* positions;
+  const int64_t* slot_mapping;
+  const uint64_t* phase_step;
+  float* scores;
+  int64_t num_tokens;
+  int64_t q_stride_token, q_stride_head; /* elements */
+  int64_t k_stride_token, k_stride_head;
+  int64_t v_stride_token, v_stride_head;
+  int32_t num_qo_heads;
+  int32_t rotary_dim;
+  int32_t interleaved;
+  float amplitude;
+} pkv_rope_args;
+
+int pkv_rope_kv_store(const pkv_rope_args* args, const pkv_cache* cache, void* stream);
+
+/*
+ * pkv_key_bounds_update: bounds of the keys of the planned requests' pages, per KV head h and channel d, over the page's
+ * valid keys j:  lo = floor(min_j k_jd / scale[h, d]),  hi = ceil(max_j k_jd / scale[h, d]), both clamped to [-127, 127]
+ * (quotients in float32; a NaN key element gives -127 and 127).  Keys are the values that attention reads (codes times scales).
+ *   plan       PKV_MODE_DECODE, PKV_MODE_PREFILL or PKV_MODE_MIXED; page_size >= 8.
+ *   codes      device int8 [num_pages, num_kv_heads, 2, head_dim] (lower, upper), contiguous, 16-byte aligned (out).
+ *   scale      device float32 [num_kv_heads, head_dim], > 0, 16-byte aligned: about max |k| / 127 of the channel.  What
+ *              lies beyond 127 steps is bounded by 127 only.
+ *   all_pages  0: the pages that hold a new token of the plan (after the KV write, every step); else every page (after
+ *              pkv_kv_evict, which moves keys, or for a cache that has no bounds yet).  No other page's bounds change.
+ * Each page is read afresh, so the result depends on the pool only.  A page listed twice must be as full for both.
+ */
+int pkv_key_bounds_update(const pkv_plan* plan, const pkv_cache* cache, int8_t* codes, const float* scale, int32_t all_pages,
+                          void* stream);
+
+/*
+ * pkv_attn_plan_blocks: pkv_attn_plan for decode over min(num_blocks, pages) selected pages of each request, its last page among
+ * them.  PKV_MODE_DECODE without a sliding window.  The plan serves pkv_block_select and pkv_attn_decode_run_blocks, beside
+ * pkv_token_map, pkv_key_bounds_update and pkv_kv_evict; the runs over every page refuse it.
+ */
+int pkv_attn_plan_blocks(pkv_plan* plan, const pkv_plan_args* args, int32_t num_blocks, void* workspace,
+                         size_t workspace_bytes, void* stream);
+int pkv_plan_blocks_workspace_size(const pkv_plan_args* args, int32_t num_blocks, size_t* bytes);
+
+/*
+ * pkv_block_select: the pages to read for every new token and KV head h.  A request with at most num_blocks pages gets
+ * all of them; of a longer one the first num_sink and last num_recent, and of the others those with the largest
+ *   score_b = sum_d w+_d hi_bd + w-_d lo_bd    (equal scores: the lower page),
+ *   w+_d, w-_d = sums over the G query heads g of h of max(c_gd, 0), min(c_gd, 0),
+ *   c_gd = rint(a_gd / max |a| * floor(32767 / G)),  a_gd = q_gd * scale[h, d]  (float32; a non-finite a_gd counts as 0),
+ * which, up to the rounding of c, bounds sum_g q_g.k over the page's keys from above.  c and everything behind it are whole
+ * numbers: the result does not depend on an order of additions.
+ *   q        device bf16 [total_tokens, num_qo_heads, head_dim], contiguous.
+ *   codes, scale  as pkv_key_bounds_update; num_pages: pages that codes has.
+ *   num_sink >= 0, num_recent >= 1, num_sink + num_recent <= num_blocks.
+ *   blocks   device int32 [total_tokens, num_kv_heads, num_blocks] (out): ascending blocks of the request, -1 behind them.
+ */
+int pkv_block_select(const pkv_plan* plan, const void* q, const int8_t* codes, const float* scale, int64_t num_pages,
+                     int32_t num_sink, int32_t num_recent, int32_t* blocks, void* stream);
+
+/*
+ * pkv_attn_decode_run_blocks: pkv_attn_decode_run whose query heads of KV head h see the keys of the pages
+ * blocks[row, h, :] only.  blocks as pkv_block_select writes them, or a caller's own choice: min(num_blocks, pages) different
+ * blocks of the request, its last one in the last place.  A block outside the request is recorded as
+ * PKV_DEVERR_PAGE_RANGE (nothing out of bounds is read; that row's values are then undefined).
+ * o, lse as pkv_attn_decode_run; lse is that of the selected keys.
+ */
+int pkv_attn_decode_run_blocks(const pkv_plan* plan, const void* q, const pkv_cache* cache, const int32_t* blocks, void* o,
+                               float* lse, void* stream);
+
 /*
  * pkv_attn_prefill_run_merge: pkv_attn_prefill_run whose result is merged into a state the caller
  * already holds in (o, lse) -- the merge of "SGLang 源码完全拆解(八)：Attention Backend", section

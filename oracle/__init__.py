@@ -15,6 +15,8 @@ The oracle restates what the pages define, in plain numpy, in float64:
 * ``oracle.nvfp4`` -- the NVFP4 codec: E2M1 codes under one E4M3 scale per 16
   elements and one float32 scale per tensor.
 * ``oracle.eviction`` -- accumulated attention weights and the eviction by them.
+* ``oracle.blocks`` -- a decode step over selected pages: token map, rotary positions,
+  key bounds, page selection, attention over the selection.
 * ``oracle.attention`` -- the KV write (a scatter through slot_mapping), the
   paged attention definition (per request: gather the pages in logical order,
   bottom-right-aligned causal mask, optional sliding window, GQA by contiguous
@@ -22,7 +24,8 @@ The oracle restates what the pages define, in plain numpy, in float64:
   two attention states.
 
 Every function is pinned by ``tests/test_oracle_pins.py`` (the codec and the
-eviction by ``tests/test_compressed_cache_host.py``) against something
+eviction by ``tests/test_compressed_cache_host.py``, the selected pages by
+``tests/test_blocks_host.py``) against something
 other than itself: the worked examples the pages print (``tests/golden/``),
 closed forms, invariants the pages state, brute force on tiny inputs and the
 library routine the pages' own CPU reference uses.  No function here is
@@ -33,4 +36,4 @@ is the seeded input generator ``workloads.py``, which holds none of the
 method's arithmetic.
 """
 
-from . import attention, eviction, fp8, metadata, nvfp4  # noqa: F401
+from . import attention, blocks, eviction, fp8, metadata, nvfp4  # noqa: F401

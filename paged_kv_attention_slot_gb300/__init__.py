@@ -30,11 +30,23 @@ Long contexts in less memory: a 4-bit pool, and eviction by accumulated attentio
     plan = Plan().plan(..., mode="decode", kv_dtype="nvfp4", scored=True)
     out = plan.run(q, cache, scores=scores)                                        # adds each key's weight
     kept = plan.evict(cache, scores, budget=4096, num_sink=4, num_recent=64)       # then re-plan: min(L, 4096) keys
+
+Or in less time, every key kept: a decode step that reads, per token and KV head, the pages that a score over 8-bit
+bounds of their keys selects:
+
+    rotary = Rotary(128, base=500000.0)
+    bounds = KeyBounds.of(cache, scale)                     # [kv_heads, head_dim]: about max |k| / 127 of each channel
+    plan = Plan().plan(..., mode="decode", num_blocks=256)
+    positions, slots = plan.token_map()                     # once per batch
+    q = rope_store(q, k, v, positions, slots, cache, rotary)  # per layer: turn q and k, write K and V
+    plan.bound_keys(cache, bounds)                          # bounds of the pages just written to
+    out = plan.run(q, cache, blocks=plan.select(q, bounds))
 """
 
 from __future__ import annotations
 
 import ctypes as C
+import math
 
 import numpy as np
 import torch
@@ -43,7 +55,7 @@ from . import _lib
 from ._lib import PkvError, check, lib
 
 __all__ = [
-    "KVCache", "Plan", "CascadePlan", "PkvError", "kv_store", "kv_load", "merge_state", "device_error", "block_table_to_csr",
+    "KVCache", "KeyBounds", "Rotary", "Plan", "CascadePlan", "PkvError", "kv_store", "kv_load", "rope_store", "merge_state", "device_error", "block_table_to_csr",
     "token_table_to_page_table", "library_path",
 ]
 
@@ -258,6 +270,140 @@ def kv_load(slot_mapping: torch.Tensor, cache: KVCache, k: torch.Tensor | None =
     return k, v
 
 
+class Rotary:
+    """Rotary positions: the angles per position of the pairs of a head's first rotary_dim elements.
+
+    Pair i is elements (i, i + rotary_dim / 2), or (2 i, 2 i + 1) with interleaved=True, and turns by
+    f_i = base ** (-2 i / rotary_dim) radians per position.  scaling stretches the wavelengths 2 pi / f_i for contexts
+    `factor` times as long as the original_positions a model was trained on:
+      None          not at all;
+      "linear"      all of them by the factor;
+      "base"        none of the shortest, all of the longest: base grows by factor ** (rotary_dim / (rotary_dim - 2));
+      "wavelength"  those that turn at most low_turns times within original_positions by the factor, those that turn at
+                    least high_turns times not at all, those between in proportion to their turns;
+      "ramp"        the same, in proportion to the pair's index (the borders rounded outwards to whole
+                    indices), and turned elements times amplitude, 0.1 ln(factor) + 1 unless given.
+    inv_freq: the f_i themselves, rotary_dim / 2 of them, instead of base and scaling.  rotary_dim is a multiple of 16."""
+
+    def __init__(self, head_dim: int, rotary_dim: int | None = None, base: float = 10000.0, interleaved: bool = False,
+                 scaling: str | None = None, factor: float = 1.0, original_positions: int = 8192, low_turns: float = 1.0,
+                 high_turns: float = 4.0, inv_freq=None, amplitude: float | None = None, device="cuda"):
+        R = head_dim if rotary_dim is None else int(rotary_dim)
+        if R < 16 or R > head_dim or R % 16:
+            raise ValueError("rotary_dim must be a multiple of 16 in [16, head_dim]")
+        if inv_freq is not None:
+            if scaling is not None:
+                raise ValueError("inv_freq holds the scaled frequencies: it excludes scaling")
+            f = np.array(inv_freq, dtype=np.float64)
+            if f.shape != (R // 2,) or not np.all(np.isfinite(f)):
+                raise ValueError(f"inv_freq must be {R // 2} finite numbers")
+        else:
+            f, ramp_amplitude = self._frequencies(R, float(base), scaling, float(factor), original_positions, low_turns, high_turns)
+            amplitude = ramp_amplitude if amplitude is None else amplitude
+        self.head_dim, self.rotary_dim, self.interleaved = int(head_dim), R, bool(interleaved)
+        self.amplitude = 1.0 if amplitude is None else float(amplitude)
+        if not math.isfinite(self.amplitude):
+            raise ValueError("amplitude must be finite")
+        self.inv_freq = f
+        # whole turns are dropped: positions are integers
+        steps = [round(math.fmod(x / (2 * math.pi), 1.0) * 2.0 ** 64) % 2 ** 64 for x in f.tolist()]
+        self.phase_step = torch.from_numpy(np.array(steps, dtype=np.uint64).view(np.int64)).to(device)
+
+    @staticmethod
+    def _frequencies(R, base, scaling, factor, original_positions, low_turns, high_turns):
+        if not (base > 0 and math.isfinite(base) and factor > 0 and math.isfinite(factor)):
+            raise ValueError("base and factor must be positive and finite")
+        if scaling == "base":
+            base *= factor ** (R / (R - 2))
+        f = base ** (-np.arange(0, R, 2, dtype=np.float64) / R)
+        if scaling in (None, "base"):
+            return f, None
+        if scaling == "linear":
+            return f / factor, None
+        if scaling not in ("wavelength", "ramp"):
+            raise ValueError(f"unknown scaling {scaling!r}")
+        if not (0 < low_turns < high_turns and original_positions > 0):
+            raise ValueError("scaling needs 0 < low_turns < high_turns and original_positions > 0")
+        if scaling == "wavelength":
+            keep = np.clip((original_positions * f / (2 * math.pi) - low_turns) / (high_turns - low_turns), 0.0, 1.0)
+            return (1.0 - keep) * f / factor + keep * f, None
+        if not base > 1:
+            raise ValueError("the ramp scaling needs base > 1")
+        # the (real) index of the pair that turns so many times within original_positions
+        first, last = (R * math.log(original_positions / (t * 2 * math.pi)) / (2 * math.log(base)) for t in (high_turns, low_turns))
+        first, last = max(math.floor(first), 0), min(math.ceil(last), R - 1)
+        stretch = np.clip((np.arange(R // 2) - first) / max(last - first, 1e-3), 0.0, 1.0)
+        return f / factor * stretch + f * (1.0 - stretch), 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+
+
+def rope_store(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, slot_mapping: torch.Tensor,
+               cache: KVCache, rotary: Rotary, q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+               return_k: bool = False, scores: torch.Tensor | None = None, stream=None):
+    """Turn q and k by their positions and write K and V at slot_mapping, in one launch (kv_store of the turned keys).
+
+    q [T, num_qo_heads, head_dim], k and v [T, num_kv_heads, head_dim]: bf16, the last dimension contiguous, other
+    strides multiples of 8 (views of one projection's output).  positions, slot_mapping: [T] int64, device.
+    Returns the turned q, contiguous (q_out, which may be q), or (q, k) with return_k=True or a k_out to
+    write the turned keys to (for the ragged runs).  scores: as kv_store."""
+    d = cache._device_index
+    T = q.shape[0]
+    D = cache._geometry[3]
+    if q.dim() != 3 or k.shape != (T, cache._geometry[2], D) or v.shape != k.shape or q.shape[2] != D:
+        raise ValueError("q must be [T, num_qo_heads, head_dim], k and v [T, num_kv_heads, head_dim] of the cache's geometry")
+    if rotary.head_dim != D:
+        raise ValueError(f"the rotary is for head_dim {rotary.head_dim}, the cache has {D}")
+    for t in (q, k, v):
+        if t.dtype != torch.bfloat16 or t.stride(2) != 1 or t.get_device() != d:
+            raise ValueError("q, k and v must be bf16 tensors on the cache's device with a contiguous last dimension")
+    for t in (positions, slot_mapping):
+        if t.dtype != torch.int64 or t.shape != (T,) or not t.is_contiguous() or t.get_device() != d:
+            raise ValueError("positions and slot_mapping must be contiguous int64 tensors [T] on the cache's device")
+    if rotary.phase_step.get_device() != d:
+        raise ValueError("the rotary must be on the cache's device")
+    for t, like in ((q_out, q), (k_out, k)):
+        if t is not None and (t.dtype != torch.bfloat16 or t.shape != like.shape or not t.is_contiguous() or t.get_device() != d):
+            raise ValueError("q_out and k_out must be contiguous bf16 tensors like q and k")
+    _check_device(cache)
+    return_k = return_k or k_out is not None
+    if q_out is None:
+        q_out = _new(q.shape, torch.bfloat16, q.device, stream)
+    if k_out is None and return_k:
+        k_out = _new(k.shape, torch.bfloat16, k.device, stream)
+    a = _lib.pkv_rope_args(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), k_out.data_ptr() if return_k else None, positions.data_ptr(),
+        slot_mapping.data_ptr(), rotary.phase_step.data_ptr(), _check_scores(scores, cache) if scores is not None else None, T,
+        q.stride(0), q.stride(1), k.stride(0), k.stride(1), v.stride(0), v.stride(1), q.shape[1], rotary.rotary_dim,
+        rotary.interleaved, rotary.amplitude)
+    check(lib().pkv_rope_kv_store(C.byref(a), C.byref(cache.struct), _stream_ptr(stream)))
+    return (q_out, k_out) if return_k else q_out
+
+
+class KeyBounds:
+    """8-bit bounds of the keys of one layer's pages, per KV head and channel, in steps of scale.
+
+    codes: int8 [num_pages, num_kv_heads, 2, head_dim] (lower, upper), contiguous; scale: float32 [num_kv_heads, head_dim],
+    positive, about max |k| / 127 of each channel (keys beyond 127 steps are bounded by 127 only).  Plan.bound_keys
+    writes the codes, Plan.select reads them."""
+
+    def __init__(self, codes: torch.Tensor, scale: torch.Tensor):
+        if codes.dtype != torch.int8 or codes.dim() != 4 or codes.shape[2] != 2 or not codes.is_contiguous():
+            raise ValueError("codes must be a contiguous int8 tensor [num_pages, num_kv_heads, 2, head_dim]")
+        if scale.dtype != torch.float32 or scale.shape != (codes.shape[1], codes.shape[3]) or not scale.is_contiguous():
+            raise ValueError("scale must be a contiguous float32 tensor [num_kv_heads, head_dim]")
+        if scale.device != codes.device:
+            raise ValueError("codes and scale must be on one device")
+        self.codes, self.scale = codes, scale
+        self._pages, self._heads = codes.shape[0], (codes.shape[1], codes.shape[3])
+        self._device_index = codes.get_device()
+
+    @classmethod
+    def of(cls, cache: KVCache, scale) -> "KeyBounds":
+        """Zeroed bounds of a cache's pages; scale: a number or a tensor [num_kv_heads, head_dim]."""
+        P, _, H, D = cache._geometry
+        scale = torch.as_tensor(scale, dtype=torch.float32, device=cache._device).expand(H, D).contiguous()
+        return cls(torch.zeros((P, H, 2, D), dtype=torch.int8, device=cache._device), scale)
+
+
 def device_error(reset: bool = True, stream=None) -> int:
     """Synchronise and read (and by default clear) the device error word; 0 means no error."""
     code = C.c_int32(0)
@@ -291,6 +437,7 @@ class Plan:
         self.scratch = None  # of scored runs
         self._streams = set()  # handles of the streams the plan's own buffers are recorded on
         self.scored = False
+        self.num_blocks = 0
         self.mode = None
         self._keep = None
 
@@ -337,45 +484,61 @@ class Plan:
     @staticmethod
     def workspace_size(qo_indptr, kv_indptr, kv_indices, last_page_len, *, num_qo_heads, num_kv_heads, head_dim,
                        page_size=1, mode="decode", window_left=-1, sm_scale=0.0, kv_dtype="bf16", max_splits=0,
-                       num_sms=0, causal=True) -> int:
+                       num_sms=0, causal=True, num_blocks=0) -> int:
         a, keep = Plan._args(qo_indptr, kv_indptr, kv_indices, last_page_len, num_qo_heads, num_kv_heads,
                              head_dim, page_size, mode, window_left, sm_scale, kv_dtype, max_splits, num_sms, causal)
+        return Plan._workspace_size(a, num_blocks)
+
+    @staticmethod
+    def _workspace_size(a, num_blocks) -> int:
         n = C.c_size_t(0)
-        check(lib().pkv_plan_workspace_size(C.byref(a), C.byref(n)))
+        if num_blocks:
+            check(lib().pkv_plan_blocks_workspace_size(C.byref(a), num_blocks, C.byref(n)))
+        else:
+            check(lib().pkv_plan_workspace_size(C.byref(a), C.byref(n)))
         return int(n.value)
+
+    def _make(self, a, num_blocks, workspace, num_bytes, stream) -> int:
+        if num_blocks:
+            return lib().pkv_attn_plan_blocks(self._h, C.byref(a), num_blocks, workspace, num_bytes, stream)
+        return lib().pkv_attn_plan(self._h, C.byref(a), workspace, num_bytes, stream)
 
     def plan(self, qo_indptr, kv_indptr, kv_indices, last_page_len, *, num_qo_heads, num_kv_heads, head_dim,
              page_size=1, mode="decode", window_left=-1, sm_scale=0.0, kv_dtype="bf16", max_splits=0, num_sms=0,
              causal=True, workspace: torch.Tensor | None = None, host_only: bool = False, stream=None,
-             scored: bool = False) -> "Plan":
+             scored: bool = False, num_blocks: int = 0) -> "Plan":
         """Plan a batch.  Host int arrays in; the binding keeps a device workspace (grown on demand).
 
         mode "ragged": kv_indptr holds row offsets into contiguous k / v tensors (run with
         run_ragged); kv_indices, last_page_len and page_size are ignored.  causal=False: every query
         sees all keys of its request (prefill / ragged plans).  scored=True (decode and mixed plans):
         reserve the scratch of run(..., scores=...) and check that no page is listed twice.  A workspace
-        or scratch that a captured graph uses must not grow: plan the largest batch first."""
+        or scratch that a captured graph uses must not grow: plan the largest batch first.
+
+        num_blocks > 0 (decode plans without a sliding window): the runs read that many selected pages of each
+        request (select, then run(..., blocks=...)); requests with fewer pages all of theirs."""
+        num_blocks = int(num_blocks)
+        if scored and num_blocks:
+            raise ValueError("accumulated scores need a plan over every page: scored and num_blocks exclude each other")
         a, keep = self._args(qo_indptr, kv_indptr, kv_indices, last_page_len, num_qo_heads, num_kv_heads, head_dim,
                              page_size, mode, window_left, sm_scale, kv_dtype, max_splits, num_sms, causal)
         if host_only:
-            check(lib().pkv_attn_plan(self._h, C.byref(a), None, 0, None))
+            check(self._make(a, num_blocks, None, 0, None))
         else:
             if workspace is not None:
                 self.workspace, self._own_workspace = workspace, False
             if self.workspace is None:
                 self.workspace = self._buffer(1 << 20, stream)
-            st = lib().pkv_attn_plan(self._h, C.byref(a), self.workspace.data_ptr(), self.workspace.numel(),
-                                     self._use(stream))
+            st = self._make(a, num_blocks, self.workspace.data_ptr(), self.workspace.numel(), self._use(stream))
             if st == _lib.PKV_EWORKSPACE and workspace is None:
                 # grow the binding-owned workspace and plan again
-                n = C.c_size_t(0)
-                check(lib().pkv_plan_workspace_size(C.byref(a), C.byref(n)))
-                self.workspace = self._buffer(int(n.value) + (int(n.value) >> 2), stream)
+                n = self._workspace_size(a, num_blocks)
+                self.workspace = self._buffer(n + (n >> 2), stream)
                 self._own_workspace = True
-                st = lib().pkv_attn_plan(self._h, C.byref(a), self.workspace.data_ptr(), self.workspace.numel(),
-                                         self._use(stream))
+                st = self._make(a, num_blocks, self.workspace.data_ptr(), self.workspace.numel(), self._use(stream))
             check(st)
         self.scored = False
+        self.num_blocks = num_blocks
         self.mode = mode
         self.num_qo_heads = num_qo_heads
         self.head_dim = head_dim
@@ -463,7 +626,8 @@ class Plan:
         return (out, lse) if (return_lse or lse is not None) else out
 
     def run(self, q: torch.Tensor, cache: KVCache, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
-            return_lse: bool = False, merge_into: bool = False, stream=None, scores: torch.Tensor | None = None):
+            return_lse: bool = False, merge_into: bool = False, stream=None, scores: torch.Tensor | None = None,
+            blocks: torch.Tensor | None = None):
         """Attention for every planned token row; q is [total_tokens, num_qo_heads, head_dim] bf16.
 
         merge_into=True (prefill plans): out / lse hold a state on entry (e.g. from run_ragged over the
@@ -471,7 +635,10 @@ class Plan:
 
         scores (plans made with scored=True): float32 [num_pages, num_kv_heads, page_size]; every visible
         key of a request with one new token gains its attention weight, summed over the query heads of
-        its KV head (pkv_attn_decode_run_scored).  Rows of longer requests add nothing."""
+        its KV head (pkv_attn_decode_run_scored).  Rows of longer requests add nothing.
+
+        blocks (plans made with num_blocks): int32 [total_tokens, num_kv_heads, num_blocks], the pages that each token's query
+        heads see, as select gives them (pkv_attn_decode_run_blocks)."""
         if self.mode == "ragged":
             raise ValueError("a ragged plan runs with run_ragged(q, k, v)")
         if self.mode == "paged_ragged":
@@ -482,6 +649,15 @@ class Plan:
             addr = _check_scores(scores, cache)
             if self.scratch is None:
                 raise ValueError("a scored run needs a plan with a workspace")
+        if blocks is not None:
+            if not self.num_blocks or scores is not None or merge_into:
+                raise ValueError("blocks need a plan made with num_blocks, and no scores or merge_into")
+            self._check_blocks(blocks, cache._device_index)
+            self._check_tensors(q, out, lse, cache)
+            out, lse = self._outputs(q, out, lse, return_lse, stream)
+            check(lib().pkv_attn_decode_run_blocks(self._h, q.data_ptr(), C.byref(cache.struct), blocks.data_ptr(), out.data_ptr(),
+                                                   lse.data_ptr() if lse is not None else None, self._use(stream)))
+            return (out, lse) if (return_lse or lse is not None) else out
         if merge_into:
             if self.mode not in ("prefill", "extend") or out is None or lse is None:
                 raise ValueError("merge_into needs a prefill plan and the held state in out and lse")
@@ -508,6 +684,66 @@ class Plan:
             check(fn(self._h, q.data_ptr(), C.byref(cache.struct), out.data_ptr(),
                      lse.data_ptr() if lse is not None else None, s))
         return (out, lse) if (return_lse or lse is not None) else out
+
+    def _check_blocks(self, blocks, device_index) -> None:
+        if (blocks.dtype != torch.int32 or blocks.shape != (self.total_tokens, self.num_kv_heads, self.num_blocks)
+                or not blocks.is_contiguous() or blocks.get_device() != device_index):
+            raise ValueError(f"blocks must be a contiguous int32 tensor {[self.total_tokens, self.num_kv_heads, self.num_blocks]} "
+                             "on the cache's device")
+
+    def token_map(self, offsets: torch.Tensor | None = None, stream=None):
+        """Positions and slots of the planned new tokens: (positions, slot_mapping), int64 [total_tokens].
+
+        Computed on the device from the plan's lengths and page table (decode, prefill and mixed plans).  offsets: int64
+        [batch_size], added to the positions of each request's tokens, e.g. the keys that evict dropped."""
+        if self.workspace is None:
+            raise ValueError("token_map needs a plan with a workspace")
+        device = self.workspace.device
+        if offsets is not None and (offsets.dtype != torch.int64 or offsets.shape != (self.batch_size,) or not offsets.is_contiguous()
+                                    or offsets.device != device):
+            raise ValueError(f"offsets must be a contiguous int64 tensor [{self.batch_size}] on the plan's device")
+        out = _new((2, self.total_tokens), torch.int64, device, stream)
+        positions, slots = out.unbind(0)
+        check(lib().pkv_token_map(self._h, offsets.data_ptr() if offsets is not None else None, positions.data_ptr(),
+                                  slots.data_ptr(), self._use(stream)))
+        return positions, slots
+
+    def bound_keys(self, cache: KVCache, bounds: KeyBounds, all_pages: bool = False, stream=None) -> None:
+        """Write the bounds of the keys of the planned requests' pages: of those that hold a new token (every step,
+        after the KV write), or of all of them (a cache without bounds, or after evict)."""
+        if bounds._pages != cache._geometry[0] or bounds._heads != cache._geometry[2:]:
+            raise ValueError("the bounds do not match the cache's geometry")
+        if bounds._device_index != cache._device_index:
+            raise ValueError("the bounds must be on the cache's device")
+        _check_device(cache)
+        check(lib().pkv_key_bounds_update(self._h, C.byref(cache.struct), bounds.codes.data_ptr(), bounds.scale.data_ptr(),
+                                          1 if all_pages else 0, self._use(stream)))
+
+    def select(self, q: torch.Tensor, bounds: KeyBounds, num_sink: int = 1, num_recent: int = 1,
+               blocks: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """The pages that each token's query heads see (plans made with num_blocks): int32 [total_tokens, num_kv_heads,
+        num_blocks], ascending page numbers within the request, -1 behind them.
+
+        Of a request with more than num_blocks pages the first num_sink and the last num_recent (at least 1), and the others with the
+        largest upper bound of q.k, summed over the query heads of the KV head (pkv_block_select)."""
+        if not self.num_blocks:
+            raise ValueError("select needs a plan made with num_blocks")
+        d = bounds._device_index
+        if q.dtype != torch.bfloat16 or q.shape != (self.total_tokens, self.num_qo_heads, self.head_dim) or not q.is_contiguous() \
+                or q.get_device() != d:
+            raise ValueError(f"q must be a contiguous bf16 tensor {[self.total_tokens, self.num_qo_heads, self.head_dim]} on the "
+                             "bounds' device")
+        if bounds._heads != (self.num_kv_heads, self.head_dim):
+            raise ValueError("the bounds do not match the plan's KV heads and head_dim")
+        if d < 0 or d != _get_device():
+            raise ValueError("the bounds must be on the current CUDA device")
+        if blocks is None:
+            blocks = _new((self.total_tokens, self.num_kv_heads, self.num_blocks), torch.int32, q.device, stream)
+        else:
+            self._check_blocks(blocks, d)
+        check(lib().pkv_block_select(self._h, q.data_ptr(), bounds.codes.data_ptr(), bounds.scale.data_ptr(), bounds._pages,
+                                     num_sink, num_recent, blocks.data_ptr(), self._use(stream)))
+        return blocks
 
     def evict(self, cache: KVCache, scores: torch.Tensor, budget: int, num_sink: int = 0, num_recent: int = 0,
               kept: torch.Tensor | None = None, stream=None) -> torch.Tensor:

@@ -62,6 +62,31 @@ class pkv_cache(C.Structure):
     ]
 
 
+class pkv_rope_args(C.Structure):
+    _fields_ = [
+        ("q", C.c_void_p),
+        ("k", C.c_void_p),
+        ("v", C.c_void_p),
+        ("q_out", C.c_void_p),
+        ("k_out", C.c_void_p),
+        ("positions", C.c_void_p),
+        ("slot_mapping", C.c_void_p),
+        ("phase_step", C.c_void_p),
+        ("scores", C.c_void_p),
+        ("num_tokens", C.c_int64),
+        ("q_stride_token", C.c_int64),
+        ("q_stride_head", C.c_int64),
+        ("k_stride_token", C.c_int64),
+        ("k_stride_head", C.c_int64),
+        ("v_stride_token", C.c_int64),
+        ("v_stride_head", C.c_int64),
+        ("num_qo_heads", C.c_int32),
+        ("rotary_dim", C.c_int32),
+        ("interleaved", C.c_int32),
+        ("amplitude", C.c_float),
+    ]
+
+
 _i32p = C.POINTER(C.c_int32)
 
 
@@ -116,6 +141,15 @@ _SIGS = {
     "pkv_kv_load": (C.c_int, [C.c_void_p, C.c_int64, C.POINTER(pkv_cache), C.c_void_p, C.c_void_p, C.c_void_p]),
     "pkv_kv_evict": (C.c_int, [C.c_void_p, C.POINTER(pkv_cache), C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_void_p,
                                C.c_void_p]),
+    "pkv_token_map": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "pkv_rope_kv_store": (C.c_int, [C.POINTER(pkv_rope_args), C.POINTER(pkv_cache), C.c_void_p]),
+    "pkv_key_bounds_update": (C.c_int, [C.c_void_p, C.POINTER(pkv_cache), C.c_void_p, C.c_void_p, C.c_int32, C.c_void_p]),
+    "pkv_attn_plan_blocks": (C.c_int, [C.c_void_p, C.POINTER(pkv_plan_args), C.c_int32, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "pkv_plan_blocks_workspace_size": (C.c_int, [C.POINTER(pkv_plan_args), C.c_int32, C.POINTER(C.c_size_t)]),
+    "pkv_block_select": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64, C.c_int32, C.c_int32,
+                                   C.c_void_p, C.c_void_p]),
+    "pkv_attn_decode_run_blocks": (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(pkv_cache), C.c_void_p, C.c_void_p, C.c_void_p,
+                                             C.c_void_p]),
     "pkv_plan_create": (C.c_int, [C.POINTER(C.c_void_p)]),
     "pkv_plan_destroy": (None, [C.c_void_p]),
     "pkv_plan_workspace_size": (C.c_int, [C.POINTER(pkv_plan_args), C.POINTER(C.c_size_t)]),

@@ -25,6 +25,7 @@
 #include <string>
 #include <vector>
 
+#include "decode_blocks.h"
 #include "pkv_internal.h"
 
 using pkv::MergeItem;
@@ -202,7 +203,8 @@ void order_by_group(std::vector<WorkItem>& all, size_t begin, size_t end, int32_
 }
 
 // Validate the arguments and build the work list into P (no device work).
-int build_plan(const pkv_plan_args* a, pkv_plan* P) {
+// num_blocks > 0: a decode plan over that many selected pages of each request.
+int build_plan(const pkv_plan_args* a, pkv_plan* P, int32_t num_blocks = 0) {
   if (!a) return fail(PKV_EINVAL, "args is NULL");
   const int32_t B = a->batch_size;
   if (B < 0) return fail(PKV_EINVAL, "batch_size < 0");
@@ -233,6 +235,16 @@ int build_plan(const pkv_plan_args* a, pkv_plan* P) {
     return fail(PKV_EUNSUPPORTED, a->kv_dtype == PKV_NVFP4 ? "NVFP4 KV needs head_dim 128" : "FP8 KV needs head_dim 128");
   if (a->max_splits < 0) return fail(PKV_EINVAL, "max_splits < 0");
   const int32_t G = a->num_qo_heads / a->num_kv_heads;
+  if (num_blocks > 0) {
+    if (a->mode != PKV_MODE_DECODE) return fail(PKV_EINVAL, "selected pages need a PKV_MODE_DECODE plan");
+    if (a->window_left >= 0) return fail(PKV_EINVAL, "selected pages and a sliding window exclude each other");
+    if (a->page_size < pkv::kBlocksMinPage)
+      return fail(PKV_EUNSUPPORTED, "selected pages need a page_size of at least " + std::to_string(pkv::kBlocksMinPage));
+    if (G > pkv::kSelectMaxGroup)
+      return fail(PKV_EUNSUPPORTED, "selected pages cover up to " + std::to_string(pkv::kSelectMaxGroup) + " query heads per KV head");
+    if (num_blocks > pkv::kSelectMaxBlocks)
+      return fail(PKV_EUNSUPPORTED, "num_blocks must be at most " + std::to_string(pkv::kSelectMaxBlocks));
+  }
   // requests with more than one new token go to the prefill kernel (all of them in prefill mode)
   bool any_extend = a->mode == PKV_MODE_PREFILL || ragged || two_src;
   if (a->mode == PKV_MODE_MIXED)
@@ -253,6 +265,7 @@ int build_plan(const pkv_plan_args* a, pkv_plan* P) {
   int64_t nnz = B > 0 ? a->kv_indptr[B] : 0;
   if (!ragged && nnz > 0 && !a->kv_indices) return fail(PKV_EINVAL, "kv_indices is NULL");
 
+  P->num_blocks = num_blocks;
   P->req.assign(B, ReqInfo{});
   P->max_page_id = -1;
   P->pages_unique.store(-1, std::memory_order_relaxed);
@@ -353,7 +366,13 @@ int build_plan(const pkv_plan_args* a, pkv_plan* P) {
       if (P->req[i].q_len != 1) continue;
       ++P->num_decodes;
       ++P->num_decode_tokens;
-      const int32_t L = P->req[i].kv_len;
+      int32_t L = P->req[i].kv_len;
+      if (num_blocks > 0) {  // the keys of its selected pages, the last page among them
+        const int64_t pages = (int64_t)a->kv_indptr[i + 1] - a->kv_indptr[i];
+        if (pages > pkv::kSelectMaxBlocks)
+          return fail(PKV_EUNSUPPORTED, "selected pages cover requests of up to " + std::to_string(pkv::kSelectMaxBlocks) + " pages");
+        if (pages > num_blocks) L = (int32_t)(L - (pages - num_blocks) * a->page_size);
+      }
       const int32_t pos = L - 1;
       const int32_t lo = a->window_left >= 0 ? std::max(0, pos - a->window_left) : 0;
       units.push_back({i, lo, L});
@@ -677,7 +696,8 @@ pkv::RunParams make_params(const pkv_plan* P, const void* q, const pkv_cache* c,
   return p;
 }
 
-int check_run(const pkv_plan* P, int mode, const void* q, const pkv_cache* c, void* o) {
+// blocks: the run is given a selection of pages
+int check_run(const pkv_plan* P, int mode, const void* q, const pkv_cache* c, void* o, bool blocks = false) {
   if (!P || !P->valid) return fail(PKV_EINVAL, "plan is NULL or has not been planned");
   if (!P->ws) return fail(PKV_EINVAL, "the plan is host-only (planned without a workspace)");
   if (mode == PKV_MODE_RAGGED || mode == PKV_MODE_PAGED_RAGGED ? P->mode != mode
@@ -686,6 +706,9 @@ int check_run(const pkv_plan* P, int mode, const void* q, const pkv_cache* c, vo
                             : mode == PKV_MODE_RAGGED ? "ragged_run needs a PKV_MODE_RAGGED plan"
                             : mode == PKV_MODE_PAGED_RAGGED ? "paged_ragged_run needs a PKV_MODE_PAGED_RAGGED plan"
                                                       : "prefill_run needs a PKV_MODE_PREFILL or PKV_MODE_MIXED plan");
+  if (blocks != (P->num_blocks > 0))
+    return fail(PKV_EINVAL, blocks ? "decode_run_blocks needs a plan made with pkv_attn_plan_blocks"
+                                   : "a plan made with pkv_attn_plan_blocks runs with pkv_attn_decode_run_blocks");
   int st = pkv::check_cache(P, c);
   if (st != PKV_OK) return st;
   if (P->total_tokens > 0 && (!q || !o)) return fail(PKV_EINVAL, "q and o must be non-NULL");
@@ -716,40 +739,19 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode_tiled() {
 
 }  // namespace
 
-// ================================================================================================
-// C ABI
-// ================================================================================================
-extern "C" {
+namespace {
 
-const char* pkv_last_error(void) { return g_err.c_str(); }
-
-int pkv_plan_create(pkv_plan** out) {
-  if (!out) return fail(PKV_EINVAL, "out is NULL");
-  *out = new pkv_plan();
-  return PKV_OK;
-}
-
-void pkv_plan_destroy(pkv_plan* plan) {
-  if (!plan) return;
-  if (plan->copy_done) {
-    cudaEventSynchronize(plan->copy_done);
-    cudaEventDestroy(plan->copy_done);
-  }
-  if (plan->pinned) cudaFreeHost(plan->pinned);
-  cudaGetLastError();
-  delete plan;
-}
-
-int pkv_plan_workspace_size(const pkv_plan_args* args, size_t* bytes) {
+int plan_workspace_size(const pkv_plan_args* args, int32_t num_blocks, size_t* bytes) {
   if (!bytes) return fail(PKV_EINVAL, "bytes is NULL");
   pkv_plan tmp;
-  int st = build_plan(args, &tmp);
+  int st = build_plan(args, &tmp, num_blocks);
   if (st != PKV_OK) return st;
   *bytes = tmp.need_bytes;
   return PKV_OK;
 }
 
-int pkv_attn_plan(pkv_plan* plan, const pkv_plan_args* args, void* workspace, size_t workspace_bytes, void* stream) {
+int make_plan(pkv_plan* plan, const pkv_plan_args* args, int32_t num_blocks, void* workspace, size_t workspace_bytes,
+              void* stream) {
   if (!plan) return fail(PKV_EINVAL, "plan is NULL");
   plan->valid = false;
   // the pinned staging buffer may still be the source of the previous plan's copy
@@ -757,7 +759,12 @@ int pkv_attn_plan(pkv_plan* plan, const pkv_plan_args* args, void* workspace, si
     PKV_CUDA(cudaEventSynchronize(plan->copy_done), "waiting for the previous plan copy");
     plan->copy_pending = false;
   }
-  int st = build_plan(args, plan);
+  int st = PKV_OK;
+  try {
+    st = build_plan(args, plan, num_blocks);
+  } catch (const std::bad_alloc&) {
+    st = fail(PKV_EUNSUPPORTED, "out of host memory while planning");
+  }
   if (st != PKV_OK) {
     plan->valid = false;
     return st;
@@ -825,6 +832,54 @@ int pkv_attn_plan(pkv_plan* plan, const pkv_plan_args* args, void* workspace, si
   plan->ws_bytes = workspace_bytes;
   plan->valid = true;
   return PKV_OK;
+}
+
+}  // namespace
+
+// ================================================================================================
+// C ABI
+// ================================================================================================
+extern "C" {
+
+const char* pkv_last_error(void) { return g_err.c_str(); }
+
+int pkv_plan_create(pkv_plan** out) {
+  if (!out) return fail(PKV_EINVAL, "out is NULL");
+  *out = new pkv_plan();
+  return PKV_OK;
+}
+
+void pkv_plan_destroy(pkv_plan* plan) {
+  if (!plan) return;
+  if (plan->copy_done) {
+    cudaEventSynchronize(plan->copy_done);
+    cudaEventDestroy(plan->copy_done);
+  }
+  if (plan->pinned) cudaFreeHost(plan->pinned);
+  cudaGetLastError();
+  delete plan;
+}
+
+int pkv_plan_workspace_size(const pkv_plan_args* args, size_t* bytes) {
+  return plan_workspace_size(args, 0, bytes);
+}
+
+int pkv_plan_blocks_workspace_size(const pkv_plan_args* args, int32_t num_blocks, size_t* bytes) {
+  if (num_blocks < 1) return fail(PKV_EINVAL, "num_blocks must be at least 1");
+  return plan_workspace_size(args, num_blocks, bytes);
+}
+
+int pkv_attn_plan(pkv_plan* plan, const pkv_plan_args* args, void* workspace, size_t workspace_bytes, void* stream) {
+  return make_plan(plan, args, 0, workspace, workspace_bytes, stream);
+}
+
+int pkv_attn_plan_blocks(pkv_plan* plan, const pkv_plan_args* args, int32_t num_blocks, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  if (num_blocks < 1) {
+    if (plan) plan->valid = false;
+    return fail(PKV_EINVAL, "num_blocks must be at least 1");
+  }
+  return make_plan(plan, args, num_blocks, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"
@@ -942,6 +997,7 @@ int pkv_attn_scored_scratch_size(const pkv_plan* plan, size_t* bytes) {
   if (!plan || !plan->valid) return fail(PKV_EINVAL, "plan is NULL or has not been planned");
   if (plan->mode != PKV_MODE_DECODE && plan->mode != PKV_MODE_MIXED)
     return fail(PKV_EINVAL, "accumulated scores need a PKV_MODE_DECODE or PKV_MODE_MIXED plan");
+  if (plan->num_blocks > 0) return fail(PKV_EINVAL, "accumulated scores need a plan over every page");
   if (plan->Hq / plan->Hkv > pkv::kScoredMaxGroup)
     return fail(PKV_EUNSUPPORTED, "accumulated scores cover up to " + std::to_string(pkv::kScoredMaxGroup) + " query heads per KV head");
   int st = check_pages_unique(plan);
@@ -1092,7 +1148,167 @@ int run_prefill(const pkv_plan* plan, int mode, const void* q, const pkv_cache* 
 }
 }  // namespace
 
+namespace {
+
+// A call beside the runs that reads the plan's metadata: the plan, its mode and the device.
+int check_paged_plan(const pkv_plan* P, const char* what) {
+  if (!P || !P->valid) return fail(PKV_EINVAL, "plan is NULL or has not been planned");
+  if (!P->ws) return fail(PKV_EINVAL, "the plan is host-only (planned without a workspace)");
+  if (P->mode != PKV_MODE_DECODE && P->mode != PKV_MODE_PREFILL && P->mode != PKV_MODE_MIXED)
+    return fail(PKV_EINVAL, std::string(what) + " needs a PKV_MODE_DECODE, PKV_MODE_PREFILL or PKV_MODE_MIXED plan");
+  int dev = -1;
+  PKV_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
+  if (dev != P->device) return fail(PKV_EINVAL, "the current device is not the device the plan was made on");
+  return PKV_OK;
+}
+
+int check_bounds(const int8_t* codes, const float* scale) {
+  if (!codes || !scale) return fail(PKV_EINVAL, "codes and scale must be non-NULL");
+  if (((uintptr_t)codes | (uintptr_t)scale) & 15) return fail(PKV_EINVAL, "codes and scale must be 16-byte aligned");
+  return PKV_OK;
+}
+
+}  // namespace
+
 extern "C" {
+
+int pkv_token_map(const pkv_plan* plan, const int64_t* offsets, int64_t* positions, int64_t* slot_mapping, void* stream) {
+  int st = check_paged_plan(plan, "token_map");
+  if (st != PKV_OK) return st;
+  if (!plan->causal) return fail(PKV_EINVAL, "the new tokens of a non-causal plan have no positions");
+  if (plan->total_tokens == 0) return PKV_OK;
+  if (!positions || !slot_mapping) return fail(PKV_EINVAL, "positions and slot_mapping must be non-NULL");
+  if (((uintptr_t)positions | (uintptr_t)slot_mapping | (uintptr_t)offsets) & 7)
+    return fail(PKV_EINVAL, "offsets, positions and slot_mapping must be 8-byte aligned");
+  const char* ws = (const char*)plan->ws;
+  PKV_CUDA(pkv::launch_token_map((const ReqInfo*)(ws + plan->off_req), (const int32_t*)(ws + plan->off_idx), plan->batch,
+                                 plan->total_tokens, plan->ps, offsets, positions, slot_mapping, (cudaStream_t)stream),
+           "token_map launch");
+  return PKV_OK;
+}
+
+int pkv_rope_kv_store(const pkv_rope_args* a, const pkv_cache* cache, void* stream) {
+  if (!a) return fail(PKV_EINVAL, "args is NULL");
+  if (!cache) return fail(PKV_EINVAL, "cache is NULL");
+  if (a->num_tokens < 0) return fail(PKV_EINVAL, "num_tokens < 0");
+  if (a->num_tokens > INT32_MAX) return fail(PKV_EUNSUPPORTED, "num_tokens must be below 2^31");
+  if (a->num_qo_heads < 1 || a->num_qo_heads > 65536) return fail(PKV_EINVAL, "num_qo_heads must be in [1, 65536]");
+  int st = check_pool(cache);
+  if (st == PKV_OK) st = check_indices(cache);
+  if (st != PKV_OK) return st;
+  if (a->rotary_dim < 16 || a->rotary_dim > cache->head_dim || a->rotary_dim % 16)
+    return fail(PKV_EUNSUPPORTED, "rotary_dim must be a multiple of 16 in [16, head_dim]");
+  if (a->interleaved != 0 && a->interleaved != 1) return fail(PKV_EINVAL, "interleaved must be 0 or 1");
+  if (!std::isfinite(a->amplitude)) return fail(PKV_EINVAL, "amplitude is not finite");
+  const int64_t strides[6] = {a->q_stride_token, a->q_stride_head, a->k_stride_token, a->k_stride_head, a->v_stride_token, a->v_stride_head};
+  for (int64_t x : strides)
+    if (x < 0 || x % 8) return fail(PKV_EINVAL, "strides of q, k and v must be non-negative multiples of 8 elements");
+  if (a->num_tokens == 0) return PKV_OK;
+  if (!a->q || !a->k || !a->v || !a->q_out || !a->positions || !a->slot_mapping || !a->phase_step || !cache->k || !cache->v)
+    return fail(PKV_EINVAL, "NULL pointer argument");
+  if (((uintptr_t)a->q | (uintptr_t)a->k | (uintptr_t)a->v | (uintptr_t)a->q_out | (uintptr_t)a->k_out) & 15)
+    return fail(PKV_EINVAL, "q, k, v, q_out and k_out must be 16-byte aligned");
+  if (((uintptr_t)a->positions | (uintptr_t)a->slot_mapping | (uintptr_t)a->phase_step) & 7)
+    return fail(PKV_EINVAL, "positions, slot_mapping and phase_step must be 8-byte aligned");
+  if ((uintptr_t)a->scores & 3) return fail(PKV_EINVAL, "scores must be 4-byte aligned");
+  float inv_k = 1.f, inv_v = 1.f;
+  if (cache->dtype != PKV_BF16) {
+    inv_k = 1.0f / cache->k_scale;
+    inv_v = 1.0f / cache->v_scale;
+  }
+  PKV_CUDA(pkv::launch_rope_store(*a, *cache, inv_k, inv_v, (cudaStream_t)stream), "rope_kv_store launch");
+  return PKV_OK;
+}
+
+int pkv_key_bounds_update(const pkv_plan* plan, const pkv_cache* cache, int8_t* codes, const float* scale, int32_t all_pages,
+                          void* stream) {
+  int st = check_paged_plan(plan, "key_bounds_update");
+  if (st == PKV_OK) st = pkv::check_cache(plan, cache);
+  if (st != PKV_OK) return st;
+  if (plan->ps < pkv::kBlocksMinPage)
+    return fail(PKV_EUNSUPPORTED, "key bounds need a page_size of at least " + std::to_string(pkv::kBlocksMinPage));
+  st = check_bounds(codes, scale);
+  if (st != PKV_OK) return st;
+  pkv::RunParams rp{};
+  pkv::set_cache_params(rp, plan, cache);
+  pkv::BoundsParams p{};
+  p.last_only = plan->mode == PKV_MODE_DECODE && !all_pages;
+  p.new_only = !all_pages;
+  p.units = (p.last_only ? (int64_t)plan->batch : (int64_t)plan->indices.size()) * plan->Hkv;
+  if (p.units == 0) return PKV_OK;
+  p.req = (const ReqInfo*)((char*)plan->ws + plan->off_req);
+  p.kv_indices = (const int32_t*)((char*)plan->ws + plan->off_idx);
+  p.k_pool = rp.k_pool;
+  p.k_sf = rp.k_sf;
+  p.stride_page_b = rp.stride_page_b;
+  p.stride_token_b = rp.stride_token_b;
+  p.stride_head_b = rp.stride_head_b;
+  p.sf_page_b = rp.sf_page_b;
+  p.sf_token_b = rp.sf_token_b;
+  p.sf_head_b = rp.sf_head_b;
+  p.codes = codes;
+  p.scale = scale;
+  p.k_scale = cache->dtype == PKV_BF16 ? 1.f : cache->k_scale;
+  p.batch = plan->batch;
+  p.num_kv_heads = plan->Hkv;
+  p.page_size = plan->ps;
+  int32_t sms = 0;
+  st = query_num_sms(0, &sms);
+  if (st != PKV_OK) return st;
+  PKV_CUDA(pkv::launch_key_bounds(p, cache->dtype, plan->D, sms, (cudaStream_t)stream), "key_bounds launch");
+  return PKV_OK;
+}
+
+int pkv_block_select(const pkv_plan* plan, const void* q, const int8_t* codes, const float* scale, int64_t num_pages,
+                     int32_t num_sink, int32_t num_recent, int32_t* blocks, void* stream) {
+  int st = check_paged_plan(plan, "block_select");
+  if (st != PKV_OK) return st;
+  if (plan->num_blocks == 0) return fail(PKV_EINVAL, "block_select needs a plan made with pkv_attn_plan_blocks");
+  if (num_sink < 0 || num_recent < 1 || (int64_t)num_sink + num_recent > plan->num_blocks)
+    return fail(PKV_EINVAL, "block_select needs num_sink >= 0, num_recent >= 1 and num_sink + num_recent <= num_blocks");
+  if (num_pages <= plan->max_page_id)
+    return fail(PKV_EINVAL, "the plan references page " + std::to_string(plan->max_page_id) + " but the bounds have " +
+                                std::to_string(num_pages) + " pages");
+  st = check_bounds(codes, scale);
+  if (st != PKV_OK) return st;
+  if (plan->total_tokens == 0) return PKV_OK;
+  if (!q || (uintptr_t)q & 1) return fail(PKV_EINVAL, "q must be non-NULL and 2-byte aligned");
+  if (!blocks || (uintptr_t)blocks & 3) return fail(PKV_EINVAL, "blocks must be non-NULL and 4-byte aligned");
+  pkv::SelectParams p{};
+  p.req = (const ReqInfo*)((char*)plan->ws + plan->off_req);
+  p.kv_indices = (const int32_t*)((char*)plan->ws + plan->off_idx);
+  p.q = q;
+  p.codes = codes;
+  p.scale = scale;
+  p.blocks = blocks;
+  p.num_kv_heads = plan->Hkv;
+  p.group = plan->Hq / plan->Hkv;
+  p.head_dim = plan->D;
+  p.page_size = plan->ps;
+  p.num_blocks = plan->num_blocks;
+  p.num_sink = num_sink;
+  p.num_recent = num_recent;
+  int32_t max_blocks = 0, sms = 0;
+  for (const ReqInfo& r : plan->req)
+    if (r.q_len) max_blocks = std::max(max_blocks, (int32_t)(((int64_t)r.kv_len + plan->ps - 1) / plan->ps));
+  st = query_num_sms(0, &sms);
+  if (st != PKV_OK) return st;
+  PKV_CUDA(pkv::launch_block_select(p, plan->batch, max_blocks, sms, (cudaStream_t)stream), "block_select launch");
+  return PKV_OK;
+}
+
+int pkv_attn_decode_run_blocks(const pkv_plan* plan, const void* q, const pkv_cache* cache, const int32_t* blocks, void* o,
+                               float* lse, void* stream) {
+  int st = check_run(plan, PKV_MODE_DECODE, q, cache, o, true);
+  if (st != PKV_OK) return st;
+  if (plan->num_decode_work == 0) return PKV_OK;
+  if (!blocks || (uintptr_t)blocks & 3) return fail(PKV_EINVAL, "blocks must be non-NULL and 4-byte aligned");
+  pkv::RunParams p = make_params(plan, q, cache, o, lse, 0, plan->num_decode_work);
+  p.blocks = blocks;
+  p.num_blocks = plan->num_blocks;
+  PKV_CUDA(pkv::launch_decode_blocks(p, cache->dtype, (cudaStream_t)stream), "decode launch");
+  return PKV_OK;
+}
 
 int pkv_attn_prefill_run(const pkv_plan* plan, const void* q, const pkv_cache* cache, void* o, float* lse,
                          void* stream) {

@@ -285,7 +285,9 @@ __device__ __forceinline__ void merge_accumulate(float4 (&acc)[NA], const int (&
 
 // SCORED: every visible key's scaled score (log2 units) goes to p.logits, each row's log2-sum-exp to
 // p.lse2 (for the accumulated attention weights, decode_scored.cu).
-template <int D, int KV, int NB, int HPB, bool SCORED>
+// BLOCKS: the unit's keys are those of the pages that p.blocks lists for its token row and KV head, in the list's
+// order; key positions (kv_begin, kv_end) count within them.
+template <int D, int KV, int NB, int HPB, bool SCORED, bool BLOCKS>
 __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB, HPB>::CTAS) decode_kernel(const RunParams p, int32_t* err) {
   using C = DecodeCfg<D, KV, NB, HPB>;
   constexpr bool FP4 = KV == PKV_NVFP4;
@@ -381,8 +383,20 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB, HPB>::CTAS) decode_k
 
   // The page id of the row this lane resolves is fetched one tile ahead, so the index load never
   // stalls the issue of the copies.
+  const int32_t* blocks = nullptr;
+  unsigned num_pages = 0;  // of the request
+  if constexpr (BLOCKS) {
+    blocks = p.blocks + ((int64_t)w.q_row * p.num_kv_heads + w.kv_head) * p.num_blocks;
+    num_pages = (unsigned)page_of(__ldg(&p.req[w.req].kv_len) - 1) + 1u;
+  }
   auto fetch_page = [&](int key) -> int {
-    return key < w.kv_end ? __ldg(p.kv_indices + w.page_base + page_of(key)) : 0;
+    if (key >= w.kv_end) return 0;
+    int at = page_of(key);
+    if constexpr (BLOCKS) {
+      at = __ldg(blocks + at);
+      if ((unsigned)at >= num_pages) return -1;  // (recorded where its rows are read)
+    }
+    return __ldg(p.kv_indices + w.page_base + at);
   };
   int next_page = fetch_page(lkey + lr);
   // Load the tile starting at lkey into `stage` and advance the sequence.
@@ -1125,25 +1139,25 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB, HPB>::CTAS) decode_k
   }
 }
 
-template <int D, int KV, int NB, int HPB, bool SCORED>
+template <int D, int KV, int NB, int HPB, bool SCORED, bool BLOCKS>
 static cudaError_t launch_decode_t(const RunParams& p, cudaStream_t s) {
   using C = DecodeCfg<D, KV, NB, HPB>;
   static bool attr_set[64] = {false};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 0 && dev < 64 && !attr_set[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, KV, NB, HPB, SCORED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, KV, NB, HPB, SCORED, BLOCKS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          C::SMEM);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
   int32_t* err = device_error_ptr();
   if (!err) return cudaErrorInvalidDevice;
-  return launch_pdl(decode_kernel<D, KV, NB, HPB, SCORED>, dim3((unsigned)p.num_work), dim3(128), (size_t)C::SMEM, s, p, err);
+  return launch_pdl(decode_kernel<D, KV, NB, HPB, SCORED, BLOCKS>, dim3((unsigned)p.num_work), dim3(128), (size_t)C::SMEM, s, p, err);
 }
 
 // The instance for the pool's type, head_dim and query heads per KV head.
-template <bool SCORED>
+template <bool SCORED, bool BLOCKS = false>
 static cudaError_t launch_decode_any(const RunParams& p, int kv_dtype, cudaStream_t s) {
   const bool nb2 = p.group > 8;
   if (kv_dtype == PKV_FP8_E4M3 || kv_dtype == PKV_NVFP4) {
@@ -1153,16 +1167,16 @@ static cudaError_t launch_decode_any(const RunParams& p, int kv_dtype, cudaStrea
     // needs a second n-block and loses (8 heads: 64 requests 53.0 against 48.9, 2 x 131072 keys 75.8
     // against 69.3, 256 ragged requests 112.5 against 100.0)
     if (kv_dtype == PKV_NVFP4)
-      return p.group <= 4 ? launch_decode_t<128, PKV_NVFP4, 1, 4, SCORED>(p, s)
-             : !nb2       ? launch_decode_t<128, PKV_NVFP4, 1, 8, SCORED>(p, s)
-                          : launch_decode_t<128, PKV_NVFP4, 2, 8, SCORED>(p, s);
-    return nb2 ? launch_decode_t<128, PKV_FP8_E4M3, 2, 8, SCORED>(p, s)
-               : launch_decode_t<128, PKV_FP8_E4M3, 1, 8, SCORED>(p, s);
+      return p.group <= 4 ? launch_decode_t<128, PKV_NVFP4, 1, 4, SCORED, BLOCKS>(p, s)
+             : !nb2       ? launch_decode_t<128, PKV_NVFP4, 1, 8, SCORED, BLOCKS>(p, s)
+                          : launch_decode_t<128, PKV_NVFP4, 2, 8, SCORED, BLOCKS>(p, s);
+    return nb2 ? launch_decode_t<128, PKV_FP8_E4M3, 2, 8, SCORED, BLOCKS>(p, s)
+               : launch_decode_t<128, PKV_FP8_E4M3, 1, 8, SCORED, BLOCKS>(p, s);
   }
   if (p.head_dim == 128)
-    return nb2 ? launch_decode_t<128, PKV_BF16, 2, 8, SCORED>(p, s) : launch_decode_t<128, PKV_BF16, 1, 8, SCORED>(p, s);
+    return nb2 ? launch_decode_t<128, PKV_BF16, 2, 8, SCORED, BLOCKS>(p, s) : launch_decode_t<128, PKV_BF16, 1, 8, SCORED, BLOCKS>(p, s);
   if (p.head_dim == 64)
-    return nb2 ? launch_decode_t<64, PKV_BF16, 2, 8, SCORED>(p, s) : launch_decode_t<64, PKV_BF16, 1, 8, SCORED>(p, s);
+    return nb2 ? launch_decode_t<64, PKV_BF16, 2, 8, SCORED, BLOCKS>(p, s) : launch_decode_t<64, PKV_BF16, 1, 8, SCORED, BLOCKS>(p, s);
   return cudaErrorInvalidValue;
 }
 

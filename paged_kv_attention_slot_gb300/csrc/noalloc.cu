@@ -68,6 +68,7 @@ extern "C" int pkv_attn_decode_run_noalloc(const pkv_plan* plan, const void* q, 
   using namespace pkv;
   if (!plan || !plan->valid) return noalloc_fail(PKV_EINVAL, "plan is NULL or has not been planned");
   if (plan->mode != PKV_MODE_DECODE) return noalloc_fail(PKV_EINVAL, "needs a PKV_MODE_DECODE plan");
+  if (plan->num_blocks > 0) return noalloc_fail(PKV_EINVAL, "a plan made with pkv_attn_plan_blocks runs with pkv_attn_decode_run_blocks");
   if (plan->need_bytes > kNoAllocScratchBytes)
     return noalloc_fail(PKV_EWORKSPACE, "the plan needs " + std::to_string(plan->need_bytes) +
                                             " bytes of scratch; the no-allocation path has " +

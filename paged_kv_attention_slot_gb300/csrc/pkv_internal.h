@@ -105,6 +105,8 @@ struct RunParams {
   int32_t wait_limit_k;  // prefill: bound on each in-kernel wait, in units of 1024 SM clock cycles
   int32_t hold_wait;     // prefill: 1 = the MMA thread first waits on a barrier nothing arrives at (the
                          // wait runs out and the CTA takes its timeout path; a test of that path)
+  const int32_t* blocks;  // decode over selected pages: [total_tokens, num_kv_heads, num_blocks] logical pages
+  int32_t num_blocks;
   float scale_log2;    // sm_scale * log2(e) (* k_scale for FP8 KV)
   float out_scale;     // 1, or v_scale for FP8 KV
   int64_t num_work;
@@ -174,6 +176,8 @@ struct pkv_plan {
   bool causal = true;   // false: every query sees all keys of its request (prefill / ragged plans)
   bool ragged = false;  // PKV_MODE_RAGGED: request i reads rows kv_indptr[i].. of contiguous K/V; max_page_id = last row
   bool paged_ragged = false;  // PKV_MODE_PAGED_RAGGED: pages hold the prefix, the new rows come from k_new / v_new
+  int32_t num_blocks = 0;  // > 0: a decode plan over that many selected pages of each request (work items' key
+                           // positions count within the selection)
   float sm_scale = 0.f;
   int64_t total_tokens = 0, max_page_id = -1, kv_tokens = 0, kv_chunk = 0, num_partials = 0;
   int64_t num_decode_work = 0;  // the decode kernel's items come first in `work`, the prefill kernel's after
