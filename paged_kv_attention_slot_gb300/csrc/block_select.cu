@@ -17,6 +17,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "decode_blocks.h"
 #include "ptx.cuh"
@@ -27,60 +28,72 @@ namespace pkv {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kBinBits = 11;
-constexpr int kBins = 1 << kBinBits;
 constexpr int kSelectMaxCluster = 8;
+constexpr int kFewPages = 256;     // competing pages of the narrow form: a thread each
+constexpr int kCandidates = 256;   // keys of one digit that are compared with each other
 
-struct SelectShared {
-  uint32_t hist[kBins];
-  int32_t w[2][2][128];  // [half of the threads][lower, upper][channel]: whole-number weights
-  float warp_max[kWarps];
-  uint32_t warp_lo[kWarps], warp_hi[kWarps];
-  uint64_t warp_sum[kWarps];
-  uint32_t digit, rest, count;  // of the radix pass: the digit found, the keys to take inside it, its keys
+// WIDE: for more than kFewPages competing pages.  UNROLL: warp-wide loads in flight (of two vectors each).
+template <bool WIDE>
+struct Form {
+  static constexpr int THREADS = WIDE ? 512 : 256;
+  static constexpr int WARPS = THREADS / 32;
+  static constexpr int CTAS = WIDE ? 1 : 3;
+  static constexpr int UNROLL = WIDE ? 8 : 4;
+  static constexpr int BIN_BITS = WIDE ? 11 : 8;
+  static constexpr int BINS = 1 << BIN_BITS;
+  struct alignas(16) Shared {  // (packed and hist are read 16 bytes at a time)
+    int32_t w[2][2][128];   // [half of the threads][lower, upper][channel]: whole-number weights
+    alignas(16) uint32_t packed[2][2][8][4];  // [lower, upper][half of 16 channels][16 channels][pair]: two 16-bit weights to a word
+    float warp_max[WARPS];
+    uint32_t warp_sum[WARPS];
+    uint32_t digit, rest, count;  // of the radix pass: the digit found, the keys to take inside it, its keys
+    uint32_t candidates;
+    uint32_t least, most;         // of the keys
+    alignas(16) uint32_t hist[BINS];          // keys of each digit, the largest digit first
+    alignas(16) uint2 candidate[kCandidates];  // (key, place)
+  };
 };
 
-// exclusive prefix over the block's threads of v, and the block's total
-template <typename V>
-__device__ __forceinline__ V block_prefix(V v, uint64_t* warp_sum, V& total) {
+// exclusive prefix over the block's threads of v
+template <int WARPS>
+__device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t* warp_sum) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  V inc = v;
+  uint32_t inc = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const V u = __shfl_up_sync(0xffffffffu, inc, o);
+    const uint32_t u = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += u;
   }
   __syncthreads();  // the previous use of warp_sum is over
   if (lane == 31) warp_sum[warp] = inc;
   __syncthreads();
-  V before = 0;
-  total = 0;
+  uint32_t before = 0;
 #pragma unroll
-  for (int k = 0; k < kWarps; ++k) {
-    const V s = (V)warp_sum[k];
-    before += k < warp ? s : (V)0;
-    total += s;
+  for (int k = 0; k < WARPS; ++k) {
+    const uint32_t s = warp_sum[k];
+    before += k < warp ? s : 0u;
   }
   return before + inc - v;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) block_select_kernel(const SelectParams p) {
-  constexpr int LANES = D / 16;      // per page: 16 bytes of the lower and of the upper bounds each
-  constexpr int PAGES = 32 / LANES;  // per warp-wide load
-  constexpr int UNROLL = 4;          // such loads in flight
-  constexpr int PARTS = kThreads / D;
-  constexpr int HELD = 8;  // query values a thread keeps between the two looks at them
+template <int D, bool WIDE>
+__global__ void __launch_bounds__(Form<WIDE>::THREADS, Form<WIDE>::CTAS) block_select_kernel(const SelectParams p) {
+  using F = Form<WIDE>;
+  constexpr int THREADS = F::THREADS, WARPS = F::WARPS, UNROLL = F::UNROLL;
+  constexpr int LANES = D / 16;          // per page: 16 bytes of the lower and of the upper bounds each
+  constexpr int PAGES = 32 / LANES;      // per warp-wide load
+  constexpr int STEP = WARPS * PAGES;    // pages between the loads of one thread
+  constexpr int PARTS = THREADS / D;     // threads per channel
+  constexpr int BINS = F::BINS, BIN_BITS = F::BIN_BITS;
+  constexpr int READ = WIDE ? 8 : 1;     // keys that a thread reads at once
+  constexpr int HELD = 4;                // query values a thread keeps between the two looks at them
   extern __shared__ __align__(16) uint8_t smem[];
-  SelectShared& sh = *reinterpret_cast<SelectShared*>(smem);
-  uint32_t* keys = reinterpret_cast<uint32_t*>(smem + sizeof(SelectShared));  // [body pages, rounded up to 32]
-  uint32_t* gtw = keys + p.key_cap;                                           // a bit per key: above the threshold
-  uint32_t* eqw = gtw + p.key_cap / 32;                                       // at the threshold
+  typename F::Shared& sh = *reinterpret_cast<typename F::Shared*>(smem);
+  uint32_t* keys = reinterpret_cast<uint32_t*>(smem + sizeof(typename F::Shared));  // [competing pages, rounded up to 32]
+  uint32_t* lives = keys + p.key_cap;  // a bit per key: it stays
 
   cg::cluster_group cluster = cg::this_cluster();
-  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int C = WIDE ? (int)cluster.num_blocks() : 1, rank = WIDE ? (int)cluster.block_rank() : 0;
   const int unit = blockIdx.x / C;
   const int i = unit / p.num_kv_heads, h = unit - i * p.num_kv_heads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -95,35 +108,70 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const SelectPara
   const int m = K - S - R;  // pages to find
   if (N <= K || m == 0) {   // (the whole cluster) nothing competes
     if (rank == 0)
-      for (int j = tid; j < K; j += kThreads) out[j] = N <= K ? (j < N ? j : -1) : (j < S ? j : N - K + j);
+      for (int j = tid; j < K; j += THREADS) out[j] = N <= K ? (j < N ? j : -1) : (j < S ? j : N - K + j);
     return;
   }
   const int nb = N - S - R;  // competing pages S .. N - R - 1
-  if (C > 1) cluster.barrier_arrive();  // (every CTA of the cluster runs before its memory is written to)
+  if (rank == 0) {
+    for (int k = tid; k < BINS; k += THREADS) sh.hist[k] = 0u;
+    if (tid == 0) {
+      sh.candidates = 0u;
+      sh.least = 0xffffffffu;
+      sh.most = 0u;
+    }
+  }
+  if (C > 1) cluster.barrier_arrive();  // (every CTA of the cluster runs, and rank 0 is ready, before its memory is written to)
+
+  // ---- the first bounds of this CTA's slice are on their way while the weights are formed ----
+  const int slice = C > 1 ? ((nb + C - 1) / C + 31) / 32 * 32 : nb;
+  const int lo = rank * slice, hi = min(nb, lo + slice);
+  const int lc = lane % LANES, lp = lane / LANES;
+  const int32_t* pages = p.kv_indices + rq.x + S;
+  const int8_t* codes = p.codes + (int64_t)h * (2 * D) + lc * 16;
+  const int64_t page_bytes = (int64_t)p.num_kv_heads * (2 * D);
+  int b0 = lo + warp * PAGES + lp;  // this lane's first page
+  int page[UNROLL];
+  uint4 x[UNROLL][2];
+  auto fetch_pages = [&](int b) {
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) page[u] = b + u * STEP < hi ? __ldg(pages + b + u * STEP) : 0;
+  };
+  auto fetch_bounds = [&](int b) {
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+      x[u][0] = x[u][1] = make_uint4(0u, 0u, 0u, 0u);
+      if (b + u * STEP < hi) {
+        const uint4* at = reinterpret_cast<const uint4*>(codes + page[u] * page_bytes);
+        x[u][0] = __ldg(at);
+        x[u][1] = __ldg(at + LANES);
+      }
+    }
+  };
+  fetch_pages(b0);
 
   // ---- whole-number weights ----
   const int G = p.group;
   const int d = tid % D, part = tid / D;
   const float scale = __ldg(p.scale + h * D + d);
   const uint16_t* q = static_cast<const uint16_t*>(p.q) + ((int64_t)rq.z * p.num_kv_heads + h) * G * D + d;
-  auto value = [&](int g) -> float {
-    const float a = __uint_as_float((uint32_t)__ldg(q + g * D) << 16) * scale;
+  auto value = [&](uint16_t bits) -> float {
+    const float a = __uint_as_float((uint32_t)bits << 16) * scale;
     return fabsf(a) <= 3.402823466e38f ? a : 0.f;  // an infinity or a NaN counts as 0
   };
-  float held[HELD], top = 0.f;
+  uint16_t held[HELD];
 #pragma unroll
-  for (int r = 0; r < HELD; ++r) {
-    const int g = part + r * PARTS;
-    held[r] = g < G ? value(g) : 0.f;
-    top = fmaxf(top, fabsf(held[r]));
-  }
-  for (int g = part + HELD * PARTS; g < G; g += PARTS) top = fmaxf(top, fabsf(value(g)));
+  for (int r = 0; r < HELD; ++r) held[r] = part + r * PARTS < G ? __ldg(q + (part + r * PARTS) * D) : (uint16_t)0;
+  fetch_bounds(b0);
+  float top = 0.f;
+#pragma unroll
+  for (int r = 0; r < HELD; ++r) top = fmaxf(top, fabsf(value(held[r])));
+  for (int g = part + HELD * PARTS; g < G; g += PARTS) top = fmaxf(top, fabsf(value(__ldg(q + g * D))));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   if (lane == 0) sh.warp_max[warp] = top;
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < kWarps; ++k) top = fmaxf(top, sh.warp_max[k]);
+  for (int k = 0; k < WARPS; ++k) top = fmaxf(top, sh.warp_max[k]);
   const float T = (float)(32767 / G);
   int32_t neg = 0, pos = 0;
   auto add = [&](float a) {
@@ -134,51 +182,42 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const SelectPara
   if (top > 0.f) {
 #pragma unroll
     for (int r = 0; r < HELD; ++r)
-      if (part + r * PARTS < G) add(held[r]);
-    for (int g = part + HELD * PARTS; g < G; g += PARTS) add(value(g));
+      if (part + r * PARTS < G) add(value(held[r]));
+    for (int g = part + HELD * PARTS; g < G; g += PARTS) add(value(__ldg(q + g * D)));
   }
-  // (head_dim 64 has four parts: two of them to a half, one after the other)
-  if (part < 2) {
-    sh.w[part][0][d] = neg;
-    sh.w[part][1][d] = pos;
-  }
-  __syncthreads();
-  if constexpr (PARTS > 2) {
-    if (part >= 2) {
-      sh.w[part - 2][0][d] += neg;
-      sh.w[part - 2][1][d] += pos;
+  // two parts at a time (sums of whole numbers: in any order)
+#pragma unroll
+  for (int k = 0; k < PARTS; k += 2) {
+    if ((part & ~1) == k) {
+      int32_t(&w)[2][128] = sh.w[part & 1];
+      w[0][d] = k ? w[0][d] + neg : neg;
+      w[1][d] = k ? w[1][d] + pos : pos;
     }
     __syncthreads();
   }
-  // this lane's weights, two to a word: channels 16 lc .. 16 lc + 15 of the lower and of the upper bounds
-  const int lc = lane % LANES, lp = lane / LANES;
+  if (tid < D) {
+    const int s = tid / (D / 2), c = tid % (D / 2) * 2;  // channels c, c + 1 of the lower or of the upper bounds
+    const int a = sh.w[0][s][c] + sh.w[1][s][c], b = sh.w[0][s][c + 1] + sh.w[1][s][c + 1];
+    sh.packed[s][c >> 3 & 1][c >> 4][c >> 1 & 3] = ((uint32_t)a & 0xffffu) | ((uint32_t)b << 16);
+  }
+  __syncthreads();
+  // this lane's weights: channels 16 lc .. 16 lc + 15
   uint32_t w[2][8];
 #pragma unroll
   for (int s = 0; s < 2; ++s)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int at = 16 * lc + 2 * j;
-      const int a = sh.w[0][s][at] + sh.w[1][s][at], b = sh.w[0][s][at + 1] + sh.w[1][s][at + 1];
-      w[s][j] = ((uint32_t)a & 0xffffu) | ((uint32_t)b << 16);
+    for (int j = 0; j < 2; ++j) {
+      const uint4 x4 = *reinterpret_cast<const uint4*>(sh.packed[s][j][lc]);
+      w[s][4 * j] = x4.x, w[s][4 * j + 1] = x4.y, w[s][4 * j + 2] = x4.z, w[s][4 * j + 3] = x4.w;
     }
 
-  // ---- scores of this CTA's slice ----
+  // ---- scores of the slice, to the first CTA ----
   if (C > 1) cluster.barrier_wait();
   uint32_t* to = C > 1 ? cluster.map_shared_rank(keys, 0) : keys;
-  const int slice = ((nb + C - 1) / C + 31) / 32 * 32;
-  const int lo = rank * slice, hi = min(nb, lo + slice);
-  const int32_t* pages = p.kv_indices + rq.x + S;
-  for (int b0 = lo + warp * PAGES; b0 < hi; b0 += kWarps * PAGES * UNROLL) {
-    int page[UNROLL];
-#pragma unroll
-    for (int u = 0; u < UNROLL; ++u) page[u] = __ldg(pages + min(b0 + u * kWarps * PAGES + lp, hi - 1));
-    uint4 x[UNROLL][2];
-#pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
-      const uint4* at = reinterpret_cast<const uint4*>(p.codes + ((int64_t)page[u] * p.num_kv_heads + h) * (2 * D)) + lc;
-      x[u][0] = __ldg(at);
-      x[u][1] = __ldg(at + LANES);
-    }
+  uint32_t least = 0xffffffffu, most = 0u;
+  for (; b0 - lp < hi; b0 += UNROLL * STEP) {  // warp-uniform
+    fetch_pages(b0 + UNROLL * STEP);
+    uint32_t key[UNROLL];
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
       int acc = 0;
@@ -191,11 +230,26 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const SelectPara
           acc = __dp2a_hi((int)w[s][2 * j + 1], (int)b[j], acc);
         }
       }
-#pragma unroll
-      for (int o = 1; o < LANES; o <<= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-      const int b = b0 + u * kWarps * PAGES + lp;
-      if (lc == 0 && b < hi) to[b] = (uint32_t)acc ^ 0x80000000u;
+      key[u] = (uint32_t)acc;
     }
+    fetch_bounds(b0 + UNROLL * STEP);
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+#pragma unroll
+      for (int o = 1; o < LANES; o <<= 1) key[u] += __shfl_xor_sync(0xffffffffu, key[u], o);
+      key[u] ^= 0x80000000u;  // in the order of the scores
+      if (b0 + u * STEP < hi) {
+        if (lc == 0) to[b0 + u * STEP] = key[u];
+        least = min(least, key[u]);
+        most = max(most, key[u]);
+      }
+    }
+  }
+  least = __reduce_min_sync(0xffffffffu, least);
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 0 && least <= most) {
+    atomicMin(C > 1 ? cluster.map_shared_rank(&sh.least, 0) : &sh.least, least);
+    atomicMax(C > 1 ? cluster.map_shared_rank(&sh.most, 0) : &sh.most, most);
   }
   if (C > 1) {
     cluster.sync();
@@ -204,149 +258,231 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const SelectPara
     __syncthreads();
   }
 
-  // ---- the m largest of nb keys ----
-  uint32_t least = 0xffffffffu, most = 0u;
-  for (int b = tid; b < nb; b += kThreads) {
-    least = min(least, keys[b]);
-    most = max(most, keys[b]);
-  }
-  least = __reduce_min_sync(0xffffffffu, least);
-  most = __reduce_max_sync(0xffffffffu, most);
-  if (lane == 0) {
-    sh.warp_lo[warp] = least;
-    sh.warp_hi[warp] = most;
-  }
-  for (int k = tid; k < kBins; k += kThreads) sh.hist[k] = 0u;
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < kWarps; ++k) {
-    least = min(least, sh.warp_lo[k]);
-    most = max(most, sh.warp_hi[k]);
-  }
-  // digits from the top of the range; `found`: the threshold's digits so far, keys >> shift compare with it
-  int bits = 32 - __clz((int)(most - least));
-  int shift = max(0, bits - kBinBits);
-  uint32_t found = 0, rest = (uint32_t)m, count = 0;
-  int above = 32;  // keys whose digits above bit `above` equal found's compete (all of them in the first pass)
+  // ---- the m largest of nb keys, equal ones from the front ----
+  // Keys (less the least of them) whose digits from bit `shift` on are above `found` stay, and `rest` of the `count` at it.
+  const int words = (nb + 31) / 32;
+  uint32_t rest = (uint32_t)m, count = 0, found = 0;
+  least = sh.least;
+  int shift = max(0, 32 - __clz((int)(sh.most - least)) - BIN_BITS);
+  int above = 32;  // keys whose digits from bit `above` on equal `found` compete (all of them in the first pass)
   while (true) {
-    for (int b = tid; b < nb; b += kThreads) {
-      const uint32_t k = keys[b] - least;
-      if (above == 32 || k >> above == found) atomicAdd(&sh.hist[(k >> shift) & (kBins - 1)], 1u);
+    for (int b = tid; b < nb; b += READ * THREADS) {
+      uint32_t k[READ];
+#pragma unroll
+      for (int r = 0; r < READ; ++r) k[r] = keys[min(b + r * THREADS, nb - 1)] - least;
+#pragma unroll
+      for (int r = 0; r < READ; ++r)
+        if (b + r * THREADS < nb && (above == 32 || k[r] >> above == found))
+          atomicAdd(&sh.hist[BINS - 1 - ((k[r] >> shift) & (BINS - 1))], 1u);
     }
     __syncthreads();
-    // the digit at which the count from the top reaches `rest`: each thread sums its bins from the top
-    constexpr int PER = kBins / kThreads;
-    uint32_t mine = 0;
+    // the digit at which the count from the top reaches `rest`
+    constexpr int PER = BINS / THREADS;
+    static_assert(PER == 1 || PER == 4, "one load per thread");
+    uint32_t n[PER], mine = 0;
+    if constexpr (PER == 4) {
+      const uint4 x4 = *reinterpret_cast<const uint4*>(&sh.hist[4 * tid]);
+      n[0] = x4.x, n[1] = x4.y, n[2] = x4.z, n[3] = x4.w;
+    } else {
+      n[0] = sh.hist[tid];
+    }
 #pragma unroll
-    for (int k = 0; k < PER; ++k) mine += sh.hist[kBins - 1 - (tid * PER + k)];
-    uint32_t total;
-    uint32_t before = block_prefix<uint32_t>(mine, sh.warp_sum, total);
+    for (int k = 0; k < PER; ++k) mine += n[k];
+    uint32_t before = block_prefix<WARPS>(mine, sh.warp_sum);
     if (before < rest && before + mine >= rest) {
 #pragma unroll
       for (int k = 0; k < PER; ++k) {
-        const uint32_t n = sh.hist[kBins - 1 - (tid * PER + k)];
-        if (before < rest && before + n >= rest) {
-          sh.digit = (uint32_t)(kBins - 1 - (tid * PER + k));
+        if (before < rest && before + n[k] >= rest) {
+          sh.digit = (uint32_t)(BINS - 1 - (tid * PER + k));
           sh.rest = rest - before;
-          sh.count = n;
+          sh.count = n[k];
         }
-        before += n;
+        before += n[k];
       }
     }
     __syncthreads();
-    const int width = min(kBinBits, above - shift);
+    const int width = min(BIN_BITS, above - shift);
     found = above == 32 ? sh.digit : (found << width) | (sh.digit & ((1u << width) - 1u));
     rest = sh.rest;
     count = sh.count;
-    if (rest == count || shift == 0) break;  // all of the digit's keys stay, or they are equal
+    if (rest == count || shift == 0 || count <= kCandidates) break;
     above = shift;
-    shift = max(0, shift - kBinBits);
-    for (int k = tid; k < kBins; k += kThreads) sh.hist[k] = 0u;
+    shift = max(0, shift - BIN_BITS);
+    for (int k = tid; k < BINS; k += THREADS) sh.hist[k] = 0u;
     __syncthreads();
   }
-
-  // ---- the survivors, in order ----
-  const int words = (nb + 31) / 32;
-  for (int wd = warp; wd < words; wd += kWarps) {
-    const int b = wd * 32 + lane;
-    const uint32_t k = b < nb ? (keys[b] - least) >> shift : 0u;
-    const uint32_t gt = __ballot_sync(0xffffffffu, b < nb && k > found);
-    const uint32_t eq = __ballot_sync(0xffffffffu, b < nb && k == found);
-    if (lane == 0) {
-      gtw[wd] = gt;
-      eqw[wd] = eq;
+  const bool all = rest == count;                    // of the digit's keys
+  const bool few = !all && count <= kCandidates;     // each is compared with all
+  if (all || few) {
+    const uint32_t stays = found + (all ? 0u : 1u);  // the lowest digit whose keys all do
+    for (int w0 = warp; w0 < words; w0 += READ * WARPS) {
+      uint32_t k[READ];
+#pragma unroll
+      for (int r = 0; r < READ; ++r) k[r] = keys[min((w0 + r * WARPS) * 32 + lane, nb - 1)] - least;
+      uint32_t here = 0;  // a bit per key that is a candidate
+#pragma unroll
+      for (int r = 0; r < READ; ++r) {
+        const int wd = w0 + r * WARPS;
+        const bool in = wd * 32 + lane < nb;
+        const uint32_t live = __ballot_sync(0xffffffffu, in && k[r] >> shift >= stays);
+        if (lane == 0 && wd < words) lives[wd] = live;
+        here |= (uint32_t)(few && in && k[r] >> shift == found) << r;
+      }
+      if (here) {
+#pragma unroll
+        for (int r = 0; r < READ; ++r)
+          if (here >> r & 1u)
+            sh.candidate[atomicAdd(&sh.candidates, 1u)] = make_uint2(k[r], (uint32_t)((w0 + r * WARPS) * 32 + lane));
+      }
+    }
+    __syncthreads();
+    if (few && tid < (int)count) {
+      const uint2 own = sh.candidate[tid];
+      uint32_t ahead = 0;
+#pragma unroll 4
+      for (uint32_t j = 0; j < count; ++j) {
+        const uint2 c = sh.candidate[j];
+        ahead += c.x > own.x || (c.x == own.x && c.y < own.y);
+      }
+      if (ahead < rest) atomicOr(&lives[own.y >> 5], 1u << (own.y & 31u));
+    }
+  } else if (warp == 0) {  // many equal keys: the first `rest` of them, counted by one warp
+    for (int wd = 0; wd < words; ++wd) {
+      const int b = wd * 32 + lane;
+      const uint32_t k = b < nb ? keys[b] - least : 0u;  // (shift is 0)
+      const uint32_t equal = __ballot_sync(0xffffffffu, b < nb && k == found);
+      const bool first = __popc(equal & ((1u << lane) - 1u)) < rest;
+      const uint32_t live = __ballot_sync(0xffffffffu, b < nb && (k > found || (k == found && first)));
+      if (lane == 0) lives[wd] = live;
+      rest -= min(rest, (uint32_t)__popc(equal));
     }
   }
   __syncthreads();
-  // counts before each word: above the threshold (high half) and at it (low half), a thread per run of words
-  const int run = (words + kThreads - 1) / kThreads;
-  uint64_t mine = 0;
-  for (int k = 0; k < run; ++k) {
-    const int wd = tid * run + k;
-    if (wd < words) mine += ((uint64_t)__popc(gtw[wd]) << 32) | (uint32_t)__popc(eqw[wd]);
-  }
-  uint64_t total;
-  uint64_t before = block_prefix<uint64_t>(mine, sh.warp_sum, total);
-  for (int k = 0; k < run; ++k) {
-    const int wd = tid * run + k;
-    if (wd >= words) break;
-    const uint32_t gt = gtw[wd], eq = eqw[wd];
-    uint32_t ties = (uint32_t)before;  // keys at the threshold before this word: the first `rest` of them stay
-    uint32_t at = (uint32_t)(before >> 32) + min(ties, rest);
-    for (uint32_t live = gt | eq; live; live &= live - 1u) {
-      const int bit = __ffs(live) - 1;
-      if (!(gt >> bit & 1u) && ties++ >= rest) continue;
-      out[S + at++] = S + wd * 32 + bit;
+
+  // ---- the survivors, in order ----
+  const int run = (words + WARPS - 1) / WARPS, first_word = warp * run, last_word = min(words, first_word + run);
+  // a warp's survivors, and those before it
+  uint32_t mine = 0;
+  for (int wd = first_word + lane; wd < last_word; wd += 32) mine += __popc(lives[wd]);
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  if (lane == 0) sh.warp_sum[warp] = mine;
+  __syncthreads();
+  uint32_t at = S;
+#pragma unroll
+  for (int k = 0; k < WARPS; ++k) at += k < warp ? sh.warp_sum[k] : 0u;
+  if (run < 8) {  // few words: a lane per bit
+    for (int wd = first_word; wd < last_word; ++wd) {
+      const uint32_t live = lives[wd];
+      if (live >> lane & 1u) out[at + __popc(live & ((1u << lane) - 1u))] = S + wd * 32 + lane;
+      at += __popc(live);
     }
-    before += ((uint64_t)__popc(gt) << 32) | (uint32_t)__popc(eq);
+  } else {  // a lane per word
+    for (int w0 = first_word; w0 < last_word; w0 += 32) {
+      const int wd = w0 + lane;
+      uint32_t live = wd < last_word ? lives[wd] : 0u, inc = __popc(live);
+      const uint32_t n = inc;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+      }
+      uint32_t to_at = at + inc - n;
+      at += __shfl_sync(0xffffffffu, inc, 31);
+      for (; live; live &= live - 1u) out[to_at++] = S + wd * 32 + __ffs(live) - 1;
+    }
   }
-  for (int j = tid; j < S; j += kThreads) out[j] = j;
-  for (int j = tid; j < R; j += kThreads) out[K - R + j] = N - R + j;
+  for (int j = tid; j < S; j += THREADS) out[j] = j;
+  for (int j = tid; j < R; j += THREADS) out[K - R + j] = N - R + j;
+}
+
+template <int D, bool WIDE>
+cudaError_t allow_shared_memory(int dev) {
+  static bool done[64] = {false};
+  if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(block_select_kernel<D, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+  return e;
+}
+
+template <int D, bool WIDE>
+void configure(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], const SelectParams& p, int64_t ctas, int C, cudaStream_t s) {
+  cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(Form<WIDE>::THREADS);
+  cfg.dynamicSmemBytes = sizeof(typename Form<WIDE>::Shared) + (size_t)p.key_cap * 4 + (size_t)p.key_cap / 32 * 4;
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+}
+
+// Clusters of c CTAs of the wide form that the device runs at once (fewer than its SMs alone would let it), for a
+// request whose scores take a quarter of the shared memory; longer ones take all of an SM's either way.
+template <int D>
+cudaError_t clusters_at_once(int dev, int c, int64_t* out) {
+  static std::atomic<int> known[64][kSelectMaxCluster + 1];  // 0: not asked yet, else the answer + 1
+  int v = dev >= 0 && dev < 64 ? known[dev][c].load(std::memory_order_relaxed) : 0;
+  if (v == 0) {
+    SelectParams p{};
+    p.key_cap = kSelectMaxBlocks / 4;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    configure<D, true>(cfg, attr, p, c, c, nullptr);
+    cfg.numAttrs = 1;
+    int n = 0;
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, block_select_kernel<D, true>, &cfg);
+    if (e != cudaSuccess) return e;
+    v = n + 1;
+    if (dev >= 0 && dev < 64) known[dev][c].store(v, std::memory_order_relaxed);
+  }
+  *out = v - 1;
+  return cudaSuccess;
 }
 
 template <int D>
-cudaError_t launch_form(const SelectParams& p, int64_t units, int C, cudaStream_t s) {
-  if (units * C > INT32_MAX) return cudaErrorInvalidValue;
-  static bool attr_set[64] = {false};
+cudaError_t launch_form(const SelectParams& p, int64_t units, int most, cudaStream_t s) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-    e = cudaFuncSetAttribute(block_select_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+  const bool wide = most > kFewPages;
+  e = wide ? allow_shared_memory<D, true>(dev) : allow_shared_memory<D, false>(dev);
+  if (e != cudaSuccess) return e;
+  int C = 1;
+  // clusters while all of them run at once and every warp of a slice has two loads to make
+  for (int c = kSelectMaxCluster; wide && c > 1 && C == 1; --c) {
+    if (most / c < 2 * Form<true>::WARPS * (512 / D)) continue;
+    int64_t at_once = 0;
+    e = clusters_at_once<D>(dev, c, &at_once);
     if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) attr_set[dev] = true;
+    if (units <= at_once) C = c;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(units * C));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = sizeof(SelectShared) + (size_t)p.key_cap * 4 + (size_t)p.key_cap / 32 * 8;
-  cfg.stream = s;
+  if (units * C > INT32_MAX) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)C;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, block_select_kernel<D>, p);
+  if (!wide) {
+    configure<D, false>(cfg, attr, p, units, 1, s);
+    return cudaLaunchKernelEx(&cfg, block_select_kernel<D, false>, p);
+  }
+  configure<D, true>(cfg, attr, p, units * C, C, s);
+  return cudaLaunchKernelEx(&cfg, block_select_kernel<D, true>, p);
 }
 
-static_assert(sizeof(SelectShared) + (size_t)kSelectMaxBlocks * 4 + (size_t)kSelectMaxBlocks / 32 * 8 <= 232448,
+static_assert(sizeof(Form<true>::Shared) + (size_t)kSelectMaxBlocks * 4 + (size_t)kSelectMaxBlocks / 32 * 4 <= 232448,
               "the scores of the longest request fit the shared memory of one CTA");
 
 }  // namespace
 
-cudaError_t launch_block_select(SelectParams p, int32_t batch, int32_t max_blocks, int num_sms, cudaStream_t s) {
+cudaError_t launch_block_select(SelectParams p, int32_t batch, int32_t max_blocks, cudaStream_t s) {
   const int64_t units = (int64_t)batch * p.num_kv_heads;
   const int32_t most = std::max(1, max_blocks - p.num_sink - p.num_recent);
   p.key_cap = (most + 31) / 32 * 32;
   p.by_page = divider(p.page_size);
-  // clusters while their CTAs all run at once and a slice keeps a load per warp in flight
-  int C = 1;
-  while (C < kSelectMaxCluster && units * C * 2 <= 2 * (int64_t)num_sms && most / (2 * C) >= 128) C *= 2;
-  return p.head_dim == 128 ? launch_form<128>(p, units, C, s) : launch_form<64>(p, units, C, s);
+  return p.head_dim == 128 ? launch_form<128>(p, units, most, s) : launch_form<64>(p, units, most, s);
 }
 
 }  // namespace pkv
