@@ -308,6 +308,7 @@ class Rotary:
         # whole turns are dropped: positions are integers
         steps = [round(math.fmod(x / (2 * math.pi), 1.0) * 2.0 ** 64) % 2 ** 64 for x in f.tolist()]
         self.phase_step = torch.from_numpy(np.array(steps, dtype=np.uint64).view(np.int64)).to(device)
+        self._phase_step, self._device_index = self.phase_step.data_ptr(), self.phase_step.get_device()
 
     @staticmethod
     def _frequencies(R, base, scaling, factor, original_positions, low_turns, high_turns):
@@ -346,34 +347,40 @@ def rope_store(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: tor
     Returns the turned q, contiguous (q_out, which may be q), or (q, k) with return_k=True or a k_out to
     write the turned keys to (for the ragged runs).  scores: as kv_store."""
     d = cache._device_index
-    T = q.shape[0]
-    D = cache._geometry[3]
-    if q.dim() != 3 or k.shape != (T, cache._geometry[2], D) or v.shape != k.shape or q.shape[2] != D:
+    _, _, H, D = cache._geometry
+    if q.dim() != 3:
+        raise ValueError("q must be [T, num_qo_heads, head_dim]")
+    T, Hq, width = q.shape
+    if width != D or k.shape != (T, H, D) or v.shape != (T, H, D):
         raise ValueError("q must be [T, num_qo_heads, head_dim], k and v [T, num_kv_heads, head_dim] of the cache's geometry")
     if rotary.head_dim != D:
         raise ValueError(f"the rotary is for head_dim {rotary.head_dim}, the cache has {D}")
-    for t in (q, k, v):
-        if t.dtype != torch.bfloat16 or t.stride(2) != 1 or t.get_device() != d:
-            raise ValueError("q, k and v must be bf16 tensors on the cache's device with a contiguous last dimension")
-    for t in (positions, slot_mapping):
-        if t.dtype != torch.int64 or t.shape != (T,) or not t.is_contiguous() or t.get_device() != d:
-            raise ValueError("positions and slot_mapping must be contiguous int64 tensors [T] on the cache's device")
-    if rotary.phase_step.get_device() != d:
+    qt, qh, qe = q.stride()
+    kt, kh, ke = k.stride()
+    vt, vh, ve = v.stride()
+    bf16, i64 = torch.bfloat16, torch.int64
+    if (q.dtype != bf16 or k.dtype != bf16 or v.dtype != bf16 or not qe == ke == ve == 1
+            or not q.get_device() == k.get_device() == v.get_device() == d):
+        raise ValueError("q, k and v must be bf16 tensors on the cache's device with a contiguous last dimension")
+    if (positions.dtype != i64 or slot_mapping.dtype != i64 or positions.shape != (T,) or slot_mapping.shape != (T,)
+            or not positions.is_contiguous() or not slot_mapping.is_contiguous()
+            or not positions.get_device() == slot_mapping.get_device() == d):
+        raise ValueError("positions and slot_mapping must be contiguous int64 tensors [T] on the cache's device")
+    if rotary._device_index != d:
         raise ValueError("the rotary must be on the cache's device")
     for t, like in ((q_out, q), (k_out, k)):
-        if t is not None and (t.dtype != torch.bfloat16 or t.shape != like.shape or not t.is_contiguous() or t.get_device() != d):
+        if t is not None and (t.dtype != bf16 or t.shape != like.shape or not t.is_contiguous() or t.get_device() != d):
             raise ValueError("q_out and k_out must be contiguous bf16 tensors like q and k")
     _check_device(cache)
     return_k = return_k or k_out is not None
     if q_out is None:
-        q_out = _new(q.shape, torch.bfloat16, q.device, stream)
+        q_out = _new((T, Hq, D), bf16, cache._device, stream)
     if k_out is None and return_k:
-        k_out = _new(k.shape, torch.bfloat16, k.device, stream)
+        k_out = _new((T, H, D), bf16, cache._device, stream)
     a = _lib.pkv_rope_args(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), k_out.data_ptr() if return_k else None, positions.data_ptr(),
-        slot_mapping.data_ptr(), rotary.phase_step.data_ptr(), _check_scores(scores, cache) if scores is not None else None, T,
-        q.stride(0), q.stride(1), k.stride(0), k.stride(1), v.stride(0), v.stride(1), q.shape[1], rotary.rotary_dim,
-        rotary.interleaved, rotary.amplitude)
+        slot_mapping.data_ptr(), rotary._phase_step, _check_scores(scores, cache) if scores is not None else None, T,
+        qt, qh, kt, kh, vt, vh, Hq, rotary.rotary_dim, rotary.interleaved, rotary.amplitude)
     check(lib().pkv_rope_kv_store(C.byref(a), C.byref(cache.struct), _stream_ptr(stream)))
     return (q_out, k_out) if return_k else q_out
 
@@ -702,8 +709,7 @@ class Plan:
         if offsets is not None and (offsets.dtype != torch.int64 or offsets.shape != (self.batch_size,) or not offsets.is_contiguous()
                                     or offsets.device != device):
             raise ValueError(f"offsets must be a contiguous int64 tensor [{self.batch_size}] on the plan's device")
-        out = _new((2, self.total_tokens), torch.int64, device, stream)
-        positions, slots = out.unbind(0)
+        positions, slots = (_new((self.total_tokens,), torch.int64, device, stream) for _ in range(2))
         check(lib().pkv_token_map(self._h, offsets.data_ptr() if offsets is not None else None, positions.data_ptr(),
                                   slots.data_ptr(), self._use(stream)))
         return positions, slots

@@ -221,7 +221,7 @@ struct DecodeCfg {
   static_assert(!PAIR || FP4, "the pair form is for 4-bit codes");
   static constexpr int KS = D / 16;  // k-steps of S^T
   static_assert(CH >= 8 || CH == 4, "the XOR swizzles below are for rows of 4 or at least 8 chunks");
-  static_assert(SMEM * CTAS <= 232448, "shared memory per SM");
+  static_assert((SMEM + 1024 + 4096) * CTAS <= 233472, "shared memory per SM, with 1 KB of the system's and a table of pages each");
   // Byte offset of 16-byte chunk c of a tile's row.  The 8 rows one ldmatrix phase reads at the same
   // chunk must fall in 8 different 16-byte columns of the 128-byte bank line: a row of 8 or more chunks
   // is XORed with its row number; of 4-chunk rows two share a line, so pairs of rows are XORed.
@@ -287,6 +287,7 @@ __device__ __forceinline__ void merge_accumulate(float4 (&acc)[NA], const int (&
 // p.lse2 (for the accumulated attention weights, decode_scored.cu).
 // BLOCKS: the unit's keys are those of the pages that p.blocks lists for its token row and KV head, in the list's
 // order; key positions (kv_begin, kv_end) count within them.
+constexpr int kPageTable = 1024;  // BLOCKS: pages of a unit that are looked up ahead
 template <int D, int KV, int NB, int HPB, bool SCORED, bool BLOCKS>
 __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB, HPB>::CTAS) decode_kernel(const RunParams p, int32_t* err) {
   using C = DecodeCfg<D, KV, NB, HPB>;
@@ -297,6 +298,35 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB, HPB>::CTAS) decode_k
 
   pdl_wait();  // the plan's metadata copy and the KV write before this run must be complete
   const WorkItem w = p.work[blockIdx.x];
+  const int ps = p.page_size;
+  const int ps_shift = (ps & (ps - 1)) == 0 ? __ffs(ps) - 1 : -1;  // page sizes are usually powers of 2
+  auto page_of = [&](int key) -> int { return ps_shift >= 0 ? key >> ps_shift : key / ps; };
+  // BLOCKS: the pool's pages of the unit, looked up once by the whole CTA (two dependent reads for all of
+  // them, instead of two before every tile), where they fit a table; -1: not a page of the request
+  __shared__ int32_t s_pages[BLOCKS ? kPageTable : 1];
+  const int32_t* blocks = nullptr;
+  unsigned num_pages = 0;  // of the request
+  bool tabled = false;
+  if constexpr (BLOCKS) {
+    blocks = p.blocks + ((int64_t)w.q_row * p.num_kv_heads + w.kv_head) * p.num_blocks;
+    num_pages = (unsigned)page_of(__ldg(&p.req[w.req].kv_len) - 1) + 1u;
+    const int listed = page_of(w.kv_end - 1) + 1;
+    tabled = listed <= kPageTable;
+    if (tabled) {
+      constexpr int READ = 4;
+      for (int e = threadIdx.x; e < listed; e += READ * 128) {
+        unsigned b[READ];
+#pragma unroll
+        for (int r = 0; r < READ; ++r) b[r] = e + r * 128 < listed ? (unsigned)__ldg(blocks + e + r * 128) : 0xffffffffu;
+        int32_t page[READ];
+#pragma unroll
+        for (int r = 0; r < READ; ++r) page[r] = b[r] < num_pages ? __ldg(p.kv_indices + w.page_base + b[r]) : -1;
+#pragma unroll
+        for (int r = 0; r < READ; ++r)
+          if (e + r * 128 < listed) s_pages[e + r * 128] = page[r];
+      }
+    }
+  }
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int g = lane >> 2;
@@ -340,9 +370,6 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB, HPB>::CTAS) decode_k
   constexpr int RPI = 32 / C::CH;  // rows per warp instruction
   const int lc = lane % C::CH;
   const int lsub = lane / C::CH;
-  const int ps = p.page_size;
-  const int ps_shift = (ps & (ps - 1)) == 0 ? __ffs(ps) - 1 : -1;  // page sizes are usually powers of 2
-  auto page_of = [&](int key) -> int { return ps_shift >= 0 ? key >> ps_shift : key / ps; };
   // NVFP4: tiles start on multiples of 16, pages are a power of two and hold whole 16-key halves, and the
   // byte strides fit 32 bits; narrow: so do all offsets into the pools
   const bool halves_paged = FP4 && ps_shift >= 4 && (w.kv_begin & 15) == 0 &&
@@ -383,16 +410,12 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB, HPB>::CTAS) decode_k
 
   // The page id of the row this lane resolves is fetched one tile ahead, so the index load never
   // stalls the issue of the copies.
-  const int32_t* blocks = nullptr;
-  unsigned num_pages = 0;  // of the request
-  if constexpr (BLOCKS) {
-    blocks = p.blocks + ((int64_t)w.q_row * p.num_kv_heads + w.kv_head) * p.num_blocks;
-    num_pages = (unsigned)page_of(__ldg(&p.req[w.req].kv_len) - 1) + 1u;
-  }
+  if constexpr (BLOCKS) __syncthreads();
   auto fetch_page = [&](int key) -> int {
     if (key >= w.kv_end) return 0;
     int at = page_of(key);
     if constexpr (BLOCKS) {
+      if (tabled) return s_pages[at];
       at = __ldg(blocks + at);
       if ((unsigned)at >= num_pages) return -1;  // (recorded where its rows are read)
     }
@@ -951,60 +974,59 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB, HPB>::CTAS) decode_k
     __syncthreads();
     if (!s_last) return;
     __threadfence();
-    if (rows * D <= 4 * 128) {
+    if (rows * D <= 4 * 128 || BLOCKS) {
       // One float4 column per thread (up to 4 rows of 128 dims): an online merge.  Each thread loads
       // the log2-sum-exp of its row and its column of U partials at once (as many as its registers
       // hold: 20 with 4 resident CTAs, 32 with 2) and folds them in under a running maximum, so 38
-      // partials cost two dependent L2 round trips and no shared-memory staging.
+      // partials cost two dependent L2 round trips and no shared-memory staging.  (BLOCKS: more rows too, 128
+      // columns at a time: few keys in many hands, so the merge is a large part of the time.)
       constexpr int U = C::CTAS >= 4 ? 20 : 32;
       const int ns = mi_.num_splits;
       const int n4 = rows * D / 4;
-      const int col = threadIdx.x;
-      const bool active = col < n4;
-      const int crow = active ? col * 4 / D : 0;
-      const float* lse_g = p.part_lse + (int64_t)mi_.first_slot * kDecodeRows + crow;
-      const float4* pm = reinterpret_cast<const float4*>(p.part_o + (int64_t)mi_.first_slot * kDecodeRows * D) + col;
-      constexpr int SLOT4 = kDecodeRows * D / 4;
-      float la[U];
-      float4 oa[U];
-      auto fetch = [&](float (&l)[U], float4 (&o)[U], int s0) {
+      for (int col = threadIdx.x; col < n4; col += 128) {
+        const int crow = col * 4 / D;
+        const float* lse_g = p.part_lse + (int64_t)mi_.first_slot * kDecodeRows + crow;
+        const float4* pm = reinterpret_cast<const float4*>(p.part_o + (int64_t)mi_.first_slot * kDecodeRows * D) + col;
+        constexpr int SLOT4 = kDecodeRows * D / 4;
+        float la[U];
+        float4 oa[U];
+        auto fetch = [&](float (&l)[U], float4 (&o)[U], int s0) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const bool in = active && s0 + u < ns;
-          l[u] = in ? __ldcg(lse_g + (int64_t)(s0 + u) * kDecodeRows) : -INFINITY;
-          o[u] = in ? __ldcg(pm + (int64_t)(s0 + u) * SLOT4) : make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int u = 0; u < U; ++u) {
+            const bool in = s0 + u < ns;
+            l[u] = in ? __ldcg(lse_g + (int64_t)(s0 + u) * kDecodeRows) : -INFINITY;
+            o[u] = in ? __ldcg(pm + (int64_t)(s0 + u) * SLOT4) : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+        };
+        float m = -INFINITY, W = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto fold = [&](const float (&l)[U], const float4 (&o)[U]) {
+          float mb = m;
+#pragma unroll
+          for (int u = 0; u < U; ++u) mb = fmaxf(mb, l[u]);
+          if (mb == -INFINITY) return;  // a partial without keys has lse -inf and weight 0
+          const float c = ex2(m - mb);  // 0 while nothing has been seen
+          W *= c;
+          acc.x *= c;
+          acc.y *= c;
+          acc.z *= c;
+          acc.w *= c;
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const float wv = ex2(l[u] - mb);
+            W += wv;
+            acc.x = fmaf(wv, o[u].x, acc.x);
+            acc.y = fmaf(wv, o[u].y, acc.y);
+            acc.z = fmaf(wv, o[u].z, acc.z);
+            acc.w = fmaf(wv, o[u].w, acc.w);
+          }
+          m = mb;
+        };
+        for (int s0 = 0; s0 < ns; s0 += U) {
+          fetch(la, oa, s0);
+          fold(la, oa);
         }
-      };
-      float m = -INFINITY, W = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      auto fold = [&](const float (&l)[U], const float4 (&o)[U]) {
-        float mb = m;
-#pragma unroll
-        for (int u = 0; u < U; ++u) mb = fmaxf(mb, l[u]);
-        if (mb == -INFINITY) return;  // a partial without keys has lse -inf and weight 0
-        const float c = ex2(m - mb);  // 0 while nothing has been seen
-        W *= c;
-        acc.x *= c;
-        acc.y *= c;
-        acc.z *= c;
-        acc.w *= c;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const float wv = ex2(l[u] - mb);
-          W += wv;
-          acc.x = fmaf(wv, o[u].x, acc.x);
-          acc.y = fmaf(wv, o[u].y, acc.y);
-          acc.z = fmaf(wv, o[u].z, acc.z);
-          acc.w = fmaf(wv, o[u].w, acc.w);
-        }
-        m = mb;
-      };
-      for (int s0 = 0; s0 < ns; s0 += U) {
-        fetch(la, oa, s0);
-        fold(la, oa);
-      }
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) + ((int64_t)mi_.q_row * p.num_qo_heads + qh0) * D;
-      if (active) {
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) + ((int64_t)mi_.q_row * p.num_qo_heads + qh0) * D;
         const float f = W > 0.f ? p.out_scale / W : 0.f;
         __nv_bfloat162* o2 = reinterpret_cast<__nv_bfloat162*>(out + col * 4);
         o2[0] = __floats2bfloat162_rn(acc.x * f, acc.y * f);
