@@ -1234,8 +1234,8 @@ int pkv_key_bounds_update(const pkv_plan* plan, const pkv_cache* cache, int8_t* 
   pkv::BoundsParams p{};
   p.last_only = plan->mode == PKV_MODE_DECODE && !all_pages;
   p.new_only = !all_pages;
-  p.units = (p.last_only ? (int64_t)plan->batch : (int64_t)plan->indices.size()) * plan->Hkv;
-  if (p.units == 0) return PKV_OK;
+  p.pages = p.last_only ? (int64_t)plan->batch : (int64_t)plan->indices.size();
+  if (p.pages == 0) return PKV_OK;
   p.req = (const ReqInfo*)((char*)plan->ws + plan->off_req);
   p.kv_indices = (const int32_t*)((char*)plan->ws + plan->off_idx);
   p.k_pool = rp.k_pool;

@@ -37,8 +37,8 @@ template <bool WIDE>
 struct Form {
   static constexpr int THREADS = WIDE ? 512 : 256;
   static constexpr int WARPS = THREADS / 32;
-  static constexpr int CTAS = WIDE ? 1 : 3;
-  static constexpr int UNROLL = WIDE ? 8 : 4;
+  static constexpr int CTAS = WIDE ? 1 : 4;
+  static constexpr int UNROLL = WIDE ? 8 : 2;
   static constexpr int BIN_BITS = WIDE ? 11 : 8;
   static constexpr int BINS = 1 << BIN_BITS;
   struct alignas(16) Shared {  // (packed and hist are read 16 bytes at a time)
@@ -142,8 +142,8 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, Form<WIDE>::CTAS) block_s
       x[u][0] = x[u][1] = make_uint4(0u, 0u, 0u, 0u);
       if (b + u * STEP < hi) {
         const uint4* at = reinterpret_cast<const uint4*>(codes + page[u] * page_bytes);
-        x[u][0] = __ldg(at);
-        x[u][1] = __ldg(at + LANES);
+        x[u][0] = ldg_once(at);
+        x[u][1] = ldg_once(at + LANES);
       }
     }
   };

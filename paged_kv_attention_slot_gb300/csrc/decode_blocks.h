@@ -20,7 +20,7 @@ struct BoundsParams {
   int8_t* codes;       // [num_pages, num_kv_heads, 2, head_dim]
   const float* scale;  // [num_kv_heads, head_dim]
   float k_scale;       // of the pool (1 for bf16)
-  int64_t units;       // (page, KV head) pairs to look at
+  int64_t pages;       // entries of the page list to look at (last_only: requests)
   int32_t batch, num_kv_heads, page_size;
   int32_t last_only;   // a page per request, its last one
   int32_t new_only;    // pages that hold a new token

@@ -68,42 +68,61 @@ __device__ __forceinline__ void widen(const uint4& x, uint32_t sf, uint32_t (&ou
   }
 }
 
-__device__ __forceinline__ uint32_t bound_code(float value, float scale, bool upper, bool nan) {
-  const float x = __fdiv_rn(value, scale);
-  float c = upper ? ceilf(x) : floorf(x);
-  c = fminf(fmaxf(c, -127.f), 127.f);
-  if (nan || x != x) c = upper ? 127.f : -127.f;  // (0 / 0 and infinity / infinity too)
-  return (uint32_t)(int)c & 0xffu;
-}
-
 template <int KV, int D>
-__global__ void __launch_bounds__(kBoundWarps * 32) key_bounds_kernel(const BoundsParams p) {
+__global__ void __launch_bounds__(kBoundWarps * 32, KV == PKV_BF16 ? 8 : 4) key_bounds_kernel(const BoundsParams p) {
   using C = BoundCfg<KV, D>;
+  constexpr uint32_t INF = KV == PKV_BF16 ? 0x7f807f80u : 0x7c007c00u, SIGNS = 0x80008000u;
+  static_assert(C::ROWS >= 2, "the first row's lanes write the lower bounds, the second's the upper ones");
   __shared__ uint32_t s_part[kBoundWarps - 1][2 * C::PAIRS][C::LANES];
   pdl_wait();
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int lane_c = lane % C::LANES, lane_r = lane / C::LANES;
+  const int ps = p.page_size;
+  const int stride = p.shared_page ? kBoundWarps * C::ROWS : C::ROWS;
+  const int start = (p.shared_page ? warp * C::ROWS : 0) + lane_r;
   const int64_t unit = p.shared_page ? (int64_t)blockIdx.x : blockIdx.x * (int64_t)kBoundWarps + warp;
-  if (unit >= p.units) return;  // (whole CTAs where they share a page)
   const int64_t u = unit / p.num_kv_heads;
   const int h = (int)(unit - u * p.num_kv_heads);
+  const bool upper = lane_r == 1;
+  if (u >= p.pages) return;  // (whole CTAs where they share a page)
+  const char* rows = nullptr;
+  const char* sfs = nullptr;
+  uint4 x[C::UNROLL];
+  uint32_t sf[C::UNROLL];
+  auto open_page = [&](int page) {
+    rows = p.k_pool + (int64_t)page * p.stride_page_b + (int64_t)h * p.stride_head_b + lane_c * 16;
+    if constexpr (KV == PKV_NVFP4) sfs = p.k_sf + (int64_t)page * p.sf_page_b + (int64_t)h * p.sf_head_b + lane_c * 2;
+  };
+  auto read = [&](int r0, int limit) {  // rows r0, r0 + stride, ... below the limit
+#pragma unroll
+    for (int k = 0; k < C::UNROLL; ++k) {
+      const int r = r0 + k * stride;
+      if (r < limit) {
+        x[k] = ldg_once(rows + r * p.stride_token_b);
+        if constexpr (KV == PKV_NVFP4) sf[k] = __ldg(reinterpret_cast<const unsigned short*>(sfs + r * p.sf_token_b));
+      }
+    }
+  };
 
-  // the request of the unit, and the page's place in the page list
-  int i;
-  int64_t entry;
+  // the request of the page, and the page's place in its list
+  int i, page = 0;
+  const bool early = !p.last_only && !p.new_only;  // every page is looked at: its first rows are read before its request is known
   if (p.last_only) {  // one page per request: its last one
     i = (int)u;
-    entry = -1;
   } else {
-    entry = u;
+    if (early) {
+      page = __ldg(p.kv_indices + u);
+      open_page(page);
+      read(start, ps);
+    }
     // the last request whose pages start at or before the entry, 32 probes at a time (requests without pages
     // share their successor's start)
     int lo = 0, n = p.batch;
     while (n > 1) {
       const int step = (n + 31) / 32;
       const int at = lane * step;
-      const bool below = at < n && __ldg(&p.req[lo + at].page_base) <= entry;
+      const bool below = at < n && __ldg(&p.req[lo + at].page_base) <= u;
       const int k = __popc(__ballot_sync(0xffffffffu, below)) - 1;  // (the first probe always is)
       lo += k * step;
       n = min(step, n - k * step);
@@ -111,46 +130,39 @@ __global__ void __launch_bounds__(kBoundWarps * 32) key_bounds_kernel(const Boun
     i = lo;
   }
   const int4 rq = __ldg(reinterpret_cast<const int4*>(p.req + i));  // page_base, kv_len, q_begin, q_len
-  const int ps = p.page_size, L = rq.y;
+  const int L = rq.y;
   const int N = (int)p.by_page.div((uint32_t)L + (uint32_t)ps - 1u);
-  const int block = p.last_only ? N - 1 : (int)(entry - rq.x);
+  const int block = p.last_only ? N - 1 : (int)(u - rq.x);
   if (p.last_only && (rq.w == 0 || N == 0)) return;
   const int valid = min(ps, L - block * ps);
-  if (p.new_only && (rq.w == 0 || block * ps + valid <= L - rq.w)) return;  // no new token in it
-  const int page = __ldg(p.kv_indices + rq.x + block);
-  const char* rows = p.k_pool + (int64_t)page * p.stride_page_b + (int64_t)h * p.stride_head_b + lane_c * 16;
-  const char* sfs = KV == PKV_NVFP4 ? p.k_sf + (int64_t)page * p.sf_page_b + (int64_t)h * p.sf_head_b + lane_c * 2 : nullptr;
+  if (!early) {
+    if (p.new_only && (rq.w == 0 || block * ps + valid <= L - rq.w)) return;  // no new token in it
+    page = __ldg(p.kv_indices + rq.x + block);
+    open_page(page);
+    read(start, valid);
+  }
 
+  // largest values, and largest negated ones (floor(x) = -ceil(-x): both bounds are rounded up)
   uint32_t mn[C::PAIRS], mx[C::PAIRS];
-  bool any = false;
-  const int stride = p.shared_page ? kBoundWarps * C::ROWS : C::ROWS;
-  for (int r0 = (p.shared_page ? warp * C::ROWS : 0) + lane_r; r0 < valid; r0 += C::UNROLL * stride) {
-    uint4 x[C::UNROLL];
-    uint32_t sf[C::UNROLL];
+#pragma unroll
+  for (int j = 0; j < C::PAIRS; ++j) mn[j] = INF, mx[j] = INF | SIGNS;
+  for (int r0 = start; r0 < valid;) {
 #pragma unroll
     for (int k = 0; k < C::UNROLL; ++k) {
-      const int r = min(r0 + k * stride, valid - 1);  // (a row read twice changes nothing)
-      x[k] = __ldg(reinterpret_cast<const uint4*>(rows + (int64_t)r * p.stride_token_b));
-      sf[k] = 0;
-      if constexpr (KV == PKV_NVFP4) sf[k] = __ldg(reinterpret_cast<const unsigned short*>(sfs + (int64_t)r * p.sf_token_b));
-    }
+      if (r0 + k * stride < valid) {
+        uint32_t v[C::PAIRS];
+        widen<KV>(x[k], sf[k], v);
 #pragma unroll
-    for (int k = 0; k < C::UNROLL; ++k) {
-      uint32_t v[C::PAIRS];
-      widen<KV>(x[k], sf[k], v);
-#pragma unroll
-      for (int j = 0; j < C::PAIRS; ++j) {
-        mn[j] = any ? pair_min<KV>(mn[j], v[j]) : v[j];
-        mx[j] = any ? pair_max<KV>(mx[j], v[j]) : v[j];
+        for (int j = 0; j < C::PAIRS; ++j) {
+          mn[j] = pair_min<KV>(mn[j], v[j]);
+          mx[j] = pair_max<KV>(mx[j], v[j]);
+        }
       }
-      any = true;
     }
+    r0 += C::UNROLL * stride;
+    if (r0 < valid) read(r0, valid);
   }
-  if (!any) {  // no row for this lane: infinities, which lose
-    constexpr uint32_t inf = KV == PKV_BF16 ? 0x7f807f80u : 0x7c007c00u;
-#pragma unroll
-    for (int j = 0; j < C::PAIRS; ++j) mn[j] = inf, mx[j] = inf | 0x80008000u;
-  }
+  __syncwarp();
 #pragma unroll
   for (int o = C::LANES; o < 32; o <<= 1)
 #pragma unroll
@@ -175,26 +187,25 @@ __global__ void __launch_bounds__(kBoundWarps * 32) key_bounds_kernel(const Boun
         mx[j] = pair_max<KV>(mx[j], s_part[k][C::PAIRS + j][lane_c]);
       }
   }
-  // the first row's lanes write the lower bounds, the second's the upper ones
-  static_assert(C::ROWS >= 2, "two rows to a load");
   if (lane_r > 1) return;
-  const bool upper = lane_r == 1;
-  const float* scale = p.scale + h * D + lane_c * 2 * C::PAIRS;
+  const float sign = upper ? 1.f : -1.f;
   uint32_t out[C::PAIRS / 2];
 #pragma unroll
   for (int j = 0; j < C::PAIRS; j += 2) {
-    const float4 s = __ldg(reinterpret_cast<const float4*>(scale + 2 * j));
-    uint32_t c4 = 0;
+    const float4 s4 = __ldg(reinterpret_cast<const float4*>(p.scale + h * D + lane_c * 2 * C::PAIRS + 2 * j));
+    const float scale[4] = {s4.x, s4.y, s4.z, s4.w};
+    uint32_t code[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const uint32_t w = upper ? mx[j + (e >> 1)] : mn[j + (e >> 1)];
-      const uint32_t bits = (e & 1) ? w >> 16 : w & 0xffffu;
+      const uint32_t w = upper ? mx[j + (e >> 1)] : mn[j + (e >> 1)] ^ SIGNS;
       float f;
-      if constexpr (KV == PKV_BF16) f = __uint_as_float(bits << 16);
-      else f = __half2float(__ushort_as_half((unsigned short)bits)) * p.k_scale;
-      c4 |= bound_code(f, e == 0 ? s.x : e == 1 ? s.y : e == 2 ? s.z : s.w, upper, f != f) << (8 * e);
+      if constexpr (KV == PKV_BF16) f = __uint_as_float((e & 1) ? w & 0xffff0000u : w << 16);
+      else f = __half2float(__ushort_as_half((unsigned short)((e & 1) ? w >> 16 : w & 0xffffu))) * p.k_scale;
+      const float c = ceilf(__fdiv_rn(f, scale[e]));
+      // (a NaN becomes 127; the code is the low byte of 1.5 * 2^23 + c)
+      code[e] = __float_as_uint(fmaf(fmaxf(fminf(c, 127.f), -127.f), sign, 12582912.f));
     }
-    out[j / 2] = c4;
+    out[j / 2] = __byte_perm(__byte_perm(code[0], code[1], 0x0040u), __byte_perm(code[2], code[3], 0x0040u), 0x5410u);
   }
   int8_t* dst = p.codes + (((int64_t)page * p.num_kv_heads + h) * 2 + (upper ? 1 : 0)) * D + lane_c * 2 * C::PAIRS;
   if constexpr (C::PAIRS == 4) {
@@ -208,7 +219,7 @@ __global__ void __launch_bounds__(kBoundWarps * 32) key_bounds_kernel(const Boun
 
 template <int KV, int D>
 cudaError_t launch_form(const BoundsParams& p, cudaStream_t s) {
-  const int64_t ctas = p.shared_page ? p.units : (p.units + kBoundWarps - 1) / kBoundWarps;
+  const int64_t units = p.pages * p.num_kv_heads, ctas = p.shared_page ? units : (units + kBoundWarps - 1) / kBoundWarps;
   if (ctas > INT32_MAX) return cudaErrorInvalidValue;
   return launch_pdl(key_bounds_kernel<KV, D>, dim3((unsigned)ctas), dim3(kBoundWarps * 32), 0, s, p);
 }
@@ -217,7 +228,7 @@ cudaError_t launch_form(const BoundsParams& p, cudaStream_t s) {
 
 cudaError_t launch_key_bounds(BoundsParams p, int dtype, int head_dim, int num_sms, cudaStream_t s) {
   // four warps to a page while that does not take more CTAs than run at once, and a page has rows for them
-  p.shared_page = p.page_size >= 32 && p.units <= (int64_t)num_sms * 8;
+  p.shared_page = p.page_size >= 32 && p.pages * p.num_kv_heads <= (int64_t)num_sms * 4;
   p.by_page = divider(p.page_size);
   if (dtype == PKV_NVFP4) return launch_form<PKV_NVFP4, 128>(p, s);
   if (dtype == PKV_FP8_E4M3) return launch_form<PKV_FP8_E4M3, 128>(p, s);

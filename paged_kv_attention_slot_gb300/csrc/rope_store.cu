@@ -27,6 +27,8 @@ int32_t* device_error_ptr();
 namespace {
 
 constexpr int kRopeMaxThreads = 512;
+constexpr int kRopeFewTokens = 152;    // a CTA per SM: latency counts, one round of row pieces where 512 threads allow it
+constexpr int kRopeManyThreads = 256;  // at most, where there are more tokens than run at once
 
 struct RopeParams {
   const char* q;
@@ -101,7 +103,7 @@ __device__ __forceinline__ uint4 row_vector(const uint4& a, const uint4& b, int 
 }
 
 template <int KV, int D, bool NEIGHBOURS>
-__global__ void __launch_bounds__(kRopeMaxThreads) rope_store_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeMaxThreads, KV == PKV_NVFP4 ? 2 : 3) rope_store_kernel(const RopeParams p) {
   constexpr int PIECES = D / 16;  // threads per row
   __shared__ __align__(16) float s_cos[D / 2], s_sin[D / 2];
   pdl_wait();
@@ -211,7 +213,8 @@ __global__ void __launch_bounds__(kRopeMaxThreads) rope_store_kernel(const RopeP
 template <int KV, int D>
 cudaError_t launch_form(const RopeParams& p, bool neighbours, int64_t tokens, cudaStream_t s) {
   const int tasks = (p.q_heads + 2 * p.heads) * (D / 16);
-  const int rounds = (tasks + kRopeMaxThreads - 1) / kRopeMaxThreads;
+  const int cap = tokens > kRopeFewTokens ? kRopeManyThreads : kRopeMaxThreads;
+  const int rounds = (tasks + cap - 1) / cap;
   const int threads = ((tasks + rounds - 1) / rounds + 31) / 32 * 32;
   const dim3 g((unsigned)tokens), b((unsigned)threads);
   return neighbours ? launch_pdl(rope_store_kernel<KV, D, true>, g, b, 0, s, p)
