@@ -1288,10 +1288,12 @@ int pkv_block_select(const pkv_plan* plan, const void* q, const int8_t* codes, c
   p.num_blocks = plan->num_blocks;
   p.num_sink = num_sink;
   p.num_recent = num_recent;
-  int32_t max_blocks = 0;
+  int32_t max_blocks = 0, sms = 0;
   for (const ReqInfo& r : plan->req)
     if (r.q_len) max_blocks = std::max(max_blocks, (int32_t)(((int64_t)r.kv_len + plan->ps - 1) / plan->ps));
-  PKV_CUDA(pkv::launch_block_select(p, plan->batch, max_blocks, (cudaStream_t)stream), "block_select launch");
+  st = query_num_sms(0, &sms);
+  if (st != PKV_OK) return st;
+  PKV_CUDA(pkv::launch_block_select(p, plan->batch, max_blocks, sms, (cudaStream_t)stream), "block_select launch");
   return PKV_OK;
 }
 

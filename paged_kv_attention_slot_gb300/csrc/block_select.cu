@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, Form<WIDE>::CTAS) block_s
   constexpr int STEP = WARPS * PAGES;    // pages between the loads of one thread
   constexpr int PARTS = THREADS / D;     // threads per channel
   constexpr int BINS = F::BINS, BIN_BITS = F::BIN_BITS;
-  constexpr int READ = WIDE ? 8 : 1;     // keys that a thread reads at once
+  constexpr int READ = WIDE ? 8 : 2;     // keys that a thread reads at once
   constexpr int HELD = 4;                // query values a thread keeps between the two looks at them
   extern __shared__ __align__(16) uint8_t smem[];
   typename F::Shared& sh = *reinterpret_cast<typename F::Shared*>(smem);
@@ -445,11 +445,12 @@ cudaError_t clusters_at_once(int dev, int c, int64_t* out) {
 }
 
 template <int D>
-cudaError_t launch_form(const SelectParams& p, int64_t units, int most, cudaStream_t s) {
+cudaError_t launch_form(const SelectParams& p, int64_t units, int most, int num_sms, cudaStream_t s) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const bool wide = most > kFewPages;
+  // The narrow form for few pages, or where two CTAs and more per SM have a unit each (NARROWRULE)
+  const bool wide = most > kFewPages && units < 2 * (int64_t)num_sms;
   e = wide ? allow_shared_memory<D, true>(dev) : allow_shared_memory<D, false>(dev);
   if (e != cudaSuccess) return e;
   int C = 1;
@@ -477,12 +478,12 @@ static_assert(sizeof(Form<true>::Shared) + (size_t)kSelectMaxBlocks * 4 + (size_
 
 }  // namespace
 
-cudaError_t launch_block_select(SelectParams p, int32_t batch, int32_t max_blocks, cudaStream_t s) {
+cudaError_t launch_block_select(SelectParams p, int32_t batch, int32_t max_blocks, int num_sms, cudaStream_t s) {
   const int64_t units = (int64_t)batch * p.num_kv_heads;
   const int32_t most = std::max(1, max_blocks - p.num_sink - p.num_recent);
   p.key_cap = (most + 31) / 32 * 32;
   p.by_page = divider(p.page_size);
-  return p.head_dim == 128 ? launch_form<128>(p, units, most, s) : launch_form<64>(p, units, most, s);
+  return p.head_dim == 128 ? launch_form<128>(p, units, most, num_sms, s) : launch_form<64>(p, units, most, num_sms, s);
 }
 
 }  // namespace pkv

@@ -42,7 +42,7 @@ struct SelectParams {
   Divider by_page;
 };
 // max_blocks: pages of the longest request
-cudaError_t launch_block_select(SelectParams p, int32_t batch, int32_t max_blocks, cudaStream_t s);
+cudaError_t launch_block_select(SelectParams p, int32_t batch, int32_t max_blocks, int num_sms, cudaStream_t s);
 
 cudaError_t launch_rope_store(const pkv_rope_args& a, const pkv_cache& c, float inv_k, float inv_v, cudaStream_t s);
 cudaError_t launch_token_map(const ReqInfo* req, const int32_t* kv_indices, int32_t batch, int64_t tokens, int32_t page_size,

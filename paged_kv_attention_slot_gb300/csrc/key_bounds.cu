@@ -12,6 +12,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "decode_blocks.h"
 #include "ptx.cuh"
 
@@ -23,11 +25,13 @@ constexpr int kBoundWarps = 4;
 
 template <int KV, int D>
 struct BoundCfg {
-  static constexpr int ROWB = KV == PKV_NVFP4 ? D / 2 : KV == PKV_FP8_E4M3 ? D : 2 * D;
-  static constexpr int LANES = ROWB / 16;                                              // per row
+  static constexpr int VECB = KV == PKV_NVFP4 ? 8 : 16;                                // bytes of a row that a lane reads
+  static constexpr int LANES = (KV == PKV_NVFP4 ? D / 2 : KV == PKV_FP8_E4M3 ? D : 2 * D) / VECB;  // per row
   static constexpr int ROWS = 32 / LANES;                                              // per warp-wide load
-  static constexpr int PAIRS = KV == PKV_NVFP4 ? 16 : KV == PKV_FP8_E4M3 ? 8 : 4;  // of elements per lane
-  static constexpr int UNROLL = 8;  // loads in flight: a 16-token page of bf16 rows at once
+  static constexpr int PAIRS = KV == PKV_BF16 ? 4 : 8;                                 // of elements per lane
+  static constexpr int MINE = D / 16;                                                  // channels of one bound that a lane ends with
+  static constexpr int UNROLL = 16 / ROWS;                                             // loads in flight: a 16-token page at once
+  using Vec = typename std::conditional<KV == PKV_NVFP4, uint2, uint4>::type;
 };
 
 // minimum and maximum of 16-bit float pairs; a NaN wins
@@ -46,34 +50,32 @@ __device__ __forceinline__ uint32_t pair_max(uint32_t a, uint32_t b) {
   return r;
 }
 
-// the pairs (element 2 j, 2 j + 1) of a 16-byte vector of a row; sf: the block scales of its two blocks (NVFP4)
-template <int KV>
-__device__ __forceinline__ void widen(const uint4& x, uint32_t sf, uint32_t (&out)[BoundCfg<KV, 128>::PAIRS]) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  if constexpr (KV == PKV_BF16) {
+// the pairs (element 2 j, 2 j + 1) of a lane's part of a row; sf: its block scale (NVFP4)
+__device__ __forceinline__ void widen(const uint4& x, uint32_t, uint32_t (&out)[4]) {  // bf16
+  out[0] = x.x, out[1] = x.y, out[2] = x.z, out[3] = x.w;
+}
+__device__ __forceinline__ void widen(const uint4& x, uint32_t, uint32_t (&out)[8]) {  // E4M3
+  e4m3x4_to_f16x2x2(x.x, out[0], out[1]);
+  e4m3x4_to_f16x2x2(x.y, out[2], out[3]);
+  e4m3x4_to_f16x2x2(x.z, out[4], out[5]);
+  e4m3x4_to_f16x2x2(x.w, out[6], out[7]);
+}
+__device__ __forceinline__ void widen(const uint2& x, uint32_t sf, uint32_t (&out)[8]) {  // E2M1 times its block's scale
+  const uint32_t s = e4m3x2_to_f16x2(sf);
+  uint32_t v[4];
+  e2m1x8_to_f16x2x4(x.x, v);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) out[j] = w[j];
-  } else if constexpr (KV == PKV_FP8_E4M3) {
+  for (int k = 0; k < 4; ++k) out[k] = hmul2_by(v[k], s, false);
+  e2m1x8_to_f16x2x4(x.y, v);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) e4m3x4_to_f16x2x2(w[j], out[2 * j], out[2 * j + 1]);
-  } else {
-    const uint32_t s = e4m3x2_to_f16x2(sf);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t v[4];
-      e2m1x8_to_f16x2x4(w[j], v);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) out[4 * j + k] = hmul2_by(v[k], s, j >= 2);
-    }
-  }
+  for (int k = 0; k < 4; ++k) out[4 + k] = hmul2_by(v[k], s, false);
 }
 
 template <int KV, int D>
-__global__ void __launch_bounds__(kBoundWarps * 32, KV == PKV_BF16 ? 8 : 4) key_bounds_kernel(const BoundsParams p) {
+__global__ void __launch_bounds__(kBoundWarps * 32, 8) key_bounds_kernel(const BoundsParams p) {
   using C = BoundCfg<KV, D>;
   constexpr uint32_t INF = KV == PKV_BF16 ? 0x7f807f80u : 0x7c007c00u, SIGNS = 0x80008000u;
-  static_assert(C::ROWS >= 2, "the first row's lanes write the lower bounds, the second's the upper ones");
-  __shared__ uint32_t s_part[kBoundWarps - 1][2 * C::PAIRS][C::LANES];
+  __shared__ uint32_t s_part[kBoundWarps - 1][C::MINE / 2][32];
   pdl_wait();
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -84,23 +86,26 @@ __global__ void __launch_bounds__(kBoundWarps * 32, KV == PKV_BF16 ? 8 : 4) key_
   const int64_t unit = p.shared_page ? (int64_t)blockIdx.x : blockIdx.x * (int64_t)kBoundWarps + warp;
   const int64_t u = unit / p.num_kv_heads;
   const int h = (int)(unit - u * p.num_kv_heads);
-  const bool upper = lane_r == 1;
   if (u >= p.pages) return;  // (whole CTAs where they share a page)
   const char* rows = nullptr;
   const char* sfs = nullptr;
-  uint4 x[C::UNROLL];
+  typename C::Vec x[C::UNROLL];
   uint32_t sf[C::UNROLL];
   auto open_page = [&](int page) {
-    rows = p.k_pool + (int64_t)page * p.stride_page_b + (int64_t)h * p.stride_head_b + lane_c * 16;
-    if constexpr (KV == PKV_NVFP4) sfs = p.k_sf + (int64_t)page * p.sf_page_b + (int64_t)h * p.sf_head_b + lane_c * 2;
+    rows = p.k_pool + (int64_t)page * p.stride_page_b + (int64_t)h * p.stride_head_b + lane_c * C::VECB;
+    if constexpr (KV == PKV_NVFP4) sfs = p.k_sf + (int64_t)page * p.sf_page_b + (int64_t)h * p.sf_head_b + lane_c;
   };
   auto read = [&](int r0, int limit) {  // rows r0, r0 + stride, ... below the limit
 #pragma unroll
     for (int k = 0; k < C::UNROLL; ++k) {
       const int r = r0 + k * stride;
       if (r < limit) {
-        x[k] = ldg_once(rows + r * p.stride_token_b);
-        if constexpr (KV == PKV_NVFP4) sf[k] = __ldg(reinterpret_cast<const unsigned short*>(sfs + r * p.sf_token_b));
+        if constexpr (KV == PKV_NVFP4) {
+          x[k] = ldg_once8(rows + r * p.stride_token_b);
+          sf[k] = __ldg(reinterpret_cast<const unsigned char*>(sfs + r * p.sf_token_b));
+        } else {
+          x[k] = ldg_once(rows + r * p.stride_token_b);
+        }
       }
     }
   };
@@ -151,7 +156,7 @@ __global__ void __launch_bounds__(kBoundWarps * 32, KV == PKV_BF16 ? 8 : 4) key_
     for (int k = 0; k < C::UNROLL; ++k) {
       if (r0 + k * stride < valid) {
         uint32_t v[C::PAIRS];
-        widen<KV>(x[k], sf[k], v);
+        widen(x[k], sf[k], v);
 #pragma unroll
         for (int j = 0; j < C::PAIRS; ++j) {
           mn[j] = pair_min<KV>(mn[j], v[j]);
@@ -163,41 +168,51 @@ __global__ void __launch_bounds__(kBoundWarps * 32, KV == PKV_BF16 ? 8 : 4) key_
     if (r0 < valid) read(r0, valid);
   }
   __syncwarp();
+  // Across the warp's rows: the upper half of the lanes takes the largest values, the lower half the largest negated
+  // ones, then each step halves the channels, so that every lane ends with C::MINE of one bound.
+  const bool upper = lane & 16;
+  uint32_t best[C::PAIRS];
 #pragma unroll
-  for (int o = C::LANES; o < 32; o <<= 1)
+  for (int j = 0; j < C::PAIRS; ++j) {
+    mn[j] ^= SIGNS;
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, upper ? mn[j] : mx[j], 16);
+    best[j] = pair_max<KV>(upper ? mx[j] : mn[j], other);
+  }
+  int held = C::PAIRS, first = 0;  // pairs of this lane's 16 bytes of a row that it still holds
 #pragma unroll
-    for (int j = 0; j < C::PAIRS; ++j) {
-      mn[j] = pair_min<KV>(mn[j], __shfl_xor_sync(0xffffffffu, mn[j], o));
-      mx[j] = pair_max<KV>(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], o));
-    }
-  if (p.shared_page) {
-    if (warp > 0 && lane < C::LANES)
+  for (int o = 8; o >= C::LANES; o >>= 1) {
+    held >>= 1;
+    const bool high = lane & o;
+    if (high) first += held;
 #pragma unroll
-      for (int j = 0; j < C::PAIRS; ++j) {
-        s_part[warp - 1][j][lane] = mn[j];
-        s_part[warp - 1][C::PAIRS + j][lane] = mx[j];
+    for (int j = 0; j < C::PAIRS / 2; ++j)
+      if (j < held) {
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, high ? best[j] : best[held + j], o);
+        best[j] = pair_max<KV>(high ? best[held + j] : best[j], other);
       }
+  }
+  if (p.shared_page) {
+    if (warp > 0)
+#pragma unroll
+      for (int j = 0; j < C::MINE / 2; ++j) s_part[warp - 1][j][lane] = best[j];
     __syncthreads();
     if (warp > 0) return;
 #pragma unroll
     for (int k = 0; k < kBoundWarps - 1; ++k)
 #pragma unroll
-      for (int j = 0; j < C::PAIRS; ++j) {
-        mn[j] = pair_min<KV>(mn[j], s_part[k][j][lane_c]);
-        mx[j] = pair_max<KV>(mx[j], s_part[k][C::PAIRS + j][lane_c]);
-      }
+      for (int j = 0; j < C::MINE / 2; ++j) best[j] = pair_max<KV>(best[j], s_part[k][j][lane]);
   }
-  if (lane_r > 1) return;
+  const int channel = lane_c * 2 * C::PAIRS + 2 * first;  // the first of this lane's
   const float sign = upper ? 1.f : -1.f;
-  uint32_t out[C::PAIRS / 2];
+  uint32_t out[C::MINE / 4];
 #pragma unroll
-  for (int j = 0; j < C::PAIRS; j += 2) {
-    const float4 s4 = __ldg(reinterpret_cast<const float4*>(p.scale + h * D + lane_c * 2 * C::PAIRS + 2 * j));
+  for (int j = 0; j < C::MINE / 4; ++j) {
+    const float4 s4 = __ldg(reinterpret_cast<const float4*>(p.scale + h * D + channel + 4 * j));
     const float scale[4] = {s4.x, s4.y, s4.z, s4.w};
     uint32_t code[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const uint32_t w = upper ? mx[j + (e >> 1)] : mn[j + (e >> 1)] ^ SIGNS;
+      const uint32_t w = best[2 * j + (e >> 1)];
       float f;
       if constexpr (KV == PKV_BF16) f = __uint_as_float((e & 1) ? w & 0xffff0000u : w << 16);
       else f = __half2float(__ushort_as_half((unsigned short)((e & 1) ? w >> 16 : w & 0xffffu))) * p.k_scale;
@@ -205,16 +220,11 @@ __global__ void __launch_bounds__(kBoundWarps * 32, KV == PKV_BF16 ? 8 : 4) key_
       // (a NaN becomes 127; the code is the low byte of 1.5 * 2^23 + c)
       code[e] = __float_as_uint(fmaf(fmaxf(fminf(c, 127.f), -127.f), sign, 12582912.f));
     }
-    out[j / 2] = __byte_perm(__byte_perm(code[0], code[1], 0x0040u), __byte_perm(code[2], code[3], 0x0040u), 0x5410u);
+    out[j] = __byte_perm(__byte_perm(code[0], code[1], 0x0040u), __byte_perm(code[2], code[3], 0x0040u), 0x5410u);
   }
-  int8_t* dst = p.codes + (((int64_t)page * p.num_kv_heads + h) * 2 + (upper ? 1 : 0)) * D + lane_c * 2 * C::PAIRS;
-  if constexpr (C::PAIRS == 4) {
-    *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < C::PAIRS / 2; j += 4)
-      *reinterpret_cast<uint4*>(dst + 4 * j) = make_uint4(out[j], out[j + 1], out[j + 2], out[j + 3]);
-  }
+  int8_t* dst = p.codes + (((int64_t)page * p.num_kv_heads + h) * 2 + (upper ? 1 : 0)) * D + channel;
+  if constexpr (C::MINE == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
+  else *reinterpret_cast<uint32_t*>(dst) = out[0];
 }
 
 template <int KV, int D>

@@ -64,6 +64,12 @@ __device__ __forceinline__ uint4 ldg_once(const void* p) {
   return r;
 }
 
+__device__ __forceinline__ uint2 ldg_once8(const void* p) {
+  uint2 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];\n" : "=r"(r.x), "=r"(r.y) : "l"(p));
+  return r;
+}
+
 // ---- ldmatrix ----
 __device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
