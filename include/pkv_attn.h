@@ -374,7 +374,8 @@ int pkv_token_map(const pkv_plan* plan, const int64_t* offsets, int64_t* positio
  * pair i being elements (i, i + rotary_dim / 2), or (2 i, 2 i + 1) where `interleaved`; elements from rotary_dim on
  * pass through, v is not turned.  Float32, rounded to bf16 once; the pool gets what pkv_kv_store makes of that key.
  *   q        device bf16 [num_tokens, num_qo_heads, head_dim], k and v device bf16 [num_tokens, num_kv_heads, head_dim], any token and
- *            head strides that are multiples of 8 elements (views of one projection's output), 16-byte aligned.
+ *            head strides that are multiples of 8 elements (views of one projection's output; that of a dimension of one is
+ *            not used), 16-byte aligned.
  *   q_out    device bf16, contiguous (out); may be q where q is contiguous.  k_out: the turned keys, contiguous, or NULL;
  *            may be k where k is contiguous.  No other overlap.
  *   positions     device int64 [num_tokens], any value.
@@ -425,7 +426,7 @@ int pkv_key_bounds_update(const pkv_plan* plan, const pkv_cache* cache, int8_t* 
 
 /*
  * pkv_attn_plan_blocks: pkv_attn_plan for decode over min(num_blocks, pages) selected pages of each request, its last page among
- * them.  PKV_MODE_DECODE without a sliding window.  The plan serves pkv_block_select and pkv_attn_decode_run_blocks, beside
+ * them.  PKV_MODE_DECODE without a sliding window.  The key positions of its work items count within the selection.  The plan serves pkv_block_select and pkv_attn_decode_run_blocks, beside
  * pkv_token_map, pkv_key_bounds_update and pkv_kv_evict; the runs over every page refuse it.
  */
 int pkv_attn_plan_blocks(pkv_plan* plan, const pkv_plan_args* args, int32_t num_blocks, void* workspace,

@@ -83,6 +83,13 @@ def _i32(a) -> np.ndarray:
     return np.ascontiguousarray(np.asarray(a, dtype=np.int32))
 
 
+def _int32(n) -> int:
+    n = int(n)
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError(f"{n} does not fit 32 bits")
+    return n
+
+
 _EMPTY_I32 = np.zeros(1, dtype=np.int32)  # a valid address for optional arrays that are absent
 
 
@@ -401,7 +408,7 @@ class KeyBounds:
             raise ValueError("codes and scale must be on one device")
         self.codes, self.scale = codes, scale
         self._pages, self._heads = codes.shape[0], (codes.shape[1], codes.shape[3])
-        self._device_index = codes.get_device()
+        self._device, self._device_index = codes.device, codes.get_device()
 
     @classmethod
     def of(cls, cache: KVCache, scale) -> "KeyBounds":
@@ -492,6 +499,7 @@ class Plan:
     def workspace_size(qo_indptr, kv_indptr, kv_indices, last_page_len, *, num_qo_heads, num_kv_heads, head_dim,
                        page_size=1, mode="decode", window_left=-1, sm_scale=0.0, kv_dtype="bf16", max_splits=0,
                        num_sms=0, causal=True, num_blocks=0) -> int:
+        num_blocks = _int32(num_blocks)
         a, keep = Plan._args(qo_indptr, kv_indptr, kv_indices, last_page_len, num_qo_heads, num_kv_heads,
                              head_dim, page_size, mode, window_left, sm_scale, kv_dtype, max_splits, num_sms, causal)
         return Plan._workspace_size(a, num_blocks)
@@ -524,7 +532,7 @@ class Plan:
 
         num_blocks > 0 (decode plans without a sliding window): the runs read that many selected pages of each
         request (select, then run(..., blocks=...)); requests with fewer pages all of theirs."""
-        num_blocks = int(num_blocks)
+        num_blocks = _int32(num_blocks)
         if scored and num_blocks:
             raise ValueError("accumulated scores need a plan over every page: scored and num_blocks exclude each other")
         a, keep = self._args(qo_indptr, kv_indptr, kv_indices, last_page_len, num_qo_heads, num_kv_heads, head_dim,
@@ -553,6 +561,7 @@ class Plan:
         self.total_tokens = int(keep[0][-1]) if len(keep[0]) else 0
         self.kv_rows = int(keep[1][-1]) if (mode == "ragged" and len(keep[1])) else 0
         self.num_kv_heads = num_kv_heads
+        self._blocks_shape = (self.total_tokens, num_kv_heads, num_blocks)
         self._keep = keep
         if scored:
             n = C.c_size_t(0)
@@ -660,7 +669,12 @@ class Plan:
             if not self.num_blocks or scores is not None or merge_into:
                 raise ValueError("blocks need a plan made with num_blocks, and no scores or merge_into")
             self._check_blocks(blocks, cache._device_index)
-            self._check_tensors(q, out, lse, cache)
+            if out is not None or lse is not None:
+                self._check_tensors(q, out, lse, cache)
+            elif q.get_device() != cache._device_index:
+                raise ValueError("q must be on the cache's device")
+            else:
+                _check_device(cache)
             out, lse = self._outputs(q, out, lse, return_lse, stream)
             check(lib().pkv_attn_decode_run_blocks(self._h, q.data_ptr(), C.byref(cache.struct), blocks.data_ptr(), out.data_ptr(),
                                                    lse.data_ptr() if lse is not None else None, self._use(stream)))
@@ -693,10 +707,9 @@ class Plan:
         return (out, lse) if (return_lse or lse is not None) else out
 
     def _check_blocks(self, blocks, device_index) -> None:
-        if (blocks.dtype != torch.int32 or blocks.shape != (self.total_tokens, self.num_kv_heads, self.num_blocks)
-                or not blocks.is_contiguous() or blocks.get_device() != device_index):
-            raise ValueError(f"blocks must be a contiguous int32 tensor {[self.total_tokens, self.num_kv_heads, self.num_blocks]} "
-                             "on the cache's device")
+        if (blocks.dtype != torch.int32 or blocks.shape != self._blocks_shape or not blocks.is_contiguous()
+                or blocks.get_device() != device_index):
+            raise ValueError(f"blocks must be a contiguous int32 tensor {list(self._blocks_shape)} on the cache's device")
 
     def token_map(self, offsets: torch.Tensor | None = None, stream=None):
         """Positions and slots of the planned new tokens: (positions, slot_mapping), int64 [total_tokens].
@@ -735,20 +748,19 @@ class Plan:
         if not self.num_blocks:
             raise ValueError("select needs a plan made with num_blocks")
         d = bounds._device_index
-        if q.dtype != torch.bfloat16 or q.shape != (self.total_tokens, self.num_qo_heads, self.head_dim) or not q.is_contiguous() \
-                or q.get_device() != d:
-            raise ValueError(f"q must be a contiguous bf16 tensor {[self.total_tokens, self.num_qo_heads, self.head_dim]} on the "
-                             "bounds' device")
+        shape = (self.total_tokens, self.num_qo_heads, self.head_dim)
+        if q.dtype != torch.bfloat16 or q.shape != shape or not q.is_contiguous() or q.get_device() != d:
+            raise ValueError(f"q must be a contiguous bf16 tensor {list(shape)} on the bounds' device")
         if bounds._heads != (self.num_kv_heads, self.head_dim):
             raise ValueError("the bounds do not match the plan's KV heads and head_dim")
         if d < 0 or d != _get_device():
             raise ValueError("the bounds must be on the current CUDA device")
         if blocks is None:
-            blocks = _new((self.total_tokens, self.num_kv_heads, self.num_blocks), torch.int32, q.device, stream)
+            blocks = _new(self._blocks_shape, torch.int32, bounds._device, stream)
         else:
             self._check_blocks(blocks, d)
         check(lib().pkv_block_select(self._h, q.data_ptr(), bounds.codes.data_ptr(), bounds.scale.data_ptr(), bounds._pages,
-                                     num_sink, num_recent, blocks.data_ptr(), self._use(stream)))
+                                     _int32(num_sink), _int32(num_recent), blocks.data_ptr(), self._use(stream)))
         return blocks
 
     def evict(self, cache: KVCache, scores: torch.Tensor, budget: int, num_sink: int = 0, num_recent: int = 0,

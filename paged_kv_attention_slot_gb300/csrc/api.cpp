@@ -1200,7 +1200,12 @@ int pkv_rope_kv_store(const pkv_rope_args* a, const pkv_cache* cache, void* stre
     return fail(PKV_EUNSUPPORTED, "rotary_dim must be a multiple of 16 in [16, head_dim]");
   if (a->interleaved != 0 && a->interleaved != 1) return fail(PKV_EINVAL, "interleaved must be 0 or 1");
   if (!std::isfinite(a->amplitude)) return fail(PKV_EINVAL, "amplitude is not finite");
-  const int64_t strides[6] = {a->q_stride_token, a->q_stride_head, a->k_stride_token, a->k_stride_head, a->v_stride_token, a->v_stride_head};
+  // (the stride of a dimension of one is not used)
+  pkv_rope_args used = *a;
+  if (a->num_tokens == 1) used.q_stride_token = used.k_stride_token = used.v_stride_token = 0;
+  if (a->num_qo_heads == 1) used.q_stride_head = 0;
+  if (cache->num_kv_heads == 1) used.k_stride_head = used.v_stride_head = 0;
+  const int64_t strides[6] = {used.q_stride_token, used.q_stride_head, used.k_stride_token, used.k_stride_head, used.v_stride_token, used.v_stride_head};
   for (int64_t x : strides)
     if (x < 0 || x % 8) return fail(PKV_EINVAL, "strides of q, k and v must be non-negative multiples of 8 elements");
   if (a->num_tokens == 0) return PKV_OK;
@@ -1216,7 +1221,7 @@ int pkv_rope_kv_store(const pkv_rope_args* a, const pkv_cache* cache, void* stre
     inv_k = 1.0f / cache->k_scale;
     inv_v = 1.0f / cache->v_scale;
   }
-  PKV_CUDA(pkv::launch_rope_store(*a, *cache, inv_k, inv_v, (cudaStream_t)stream), "rope_kv_store launch");
+  PKV_CUDA(pkv::launch_rope_store(used, *cache, inv_k, inv_v, (cudaStream_t)stream), "rope_kv_store launch");
   return PKV_OK;
 }
 

@@ -29,10 +29,11 @@ namespace pkv {
 namespace {
 
 constexpr int kSelectMaxCluster = 8;
-constexpr int kFewPages = 256;     // competing pages of the narrow form: a thread each
+constexpr int kFewPages = 256;     // competing pages that the narrow form takes in any case: a thread each
 constexpr int kCandidates = 256;   // keys of one digit that are compared with each other
 
-// WIDE: for more than kFewPages competing pages.  UNROLL: warp-wide loads in flight (of two vectors each).
+// WIDE: a cluster of CTAs that have an SM each, for few units of many pages; narrow: a CTA of four on an SM.
+// UNROLL: warp-wide loads in flight (of two vectors a lane each).
 template <bool WIDE>
 struct Form {
   static constexpr int THREADS = WIDE ? 512 : 256;
@@ -449,8 +450,10 @@ cudaError_t launch_form(const SelectParams& p, int64_t units, int most, int num_
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  // The narrow form for few pages, or where two CTAs and more per SM have a unit each (NARROWRULE)
-  const bool wide = most > kFewPages && units < 2 * (int64_t)num_sms;
+  // Narrow for few pages (64 x 8 units of up to 256: 7.3 us; wide 12.8), and where units outnumber the SMs, which hold one
+  // wide CTA each (512 units of 400 to 512 pages 13.8 us, wide 32.6; 256 of 768 to 1024 pages 16.8, wide 23.3; 152 of
+  // as many 14.8, wide 12.4; 192 of 3072 to 4096 pages 49.6, wide 47.3).
+  const bool wide = most > kFewPages && units <= num_sms;
   e = wide ? allow_shared_memory<D, true>(dev) : allow_shared_memory<D, false>(dev);
   if (e != cudaSuccess) return e;
   int C = 1;

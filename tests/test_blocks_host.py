@@ -213,6 +213,12 @@ def test_plan_refuses_scores_and_too_long_requests(pk):
     assert _plan(pk, [8 * 49152 + 1, 9], 4, ps=8, q_lens=[0, 1]).info()["kv_tokens"] == 9
 
 
+@pytest.mark.parametrize("n", [2 ** 32 + 5, -2 ** 33])
+def test_plan_refuses_counts_beyond_32_bits(pk, n):
+    with pytest.raises(ValueError, match="32 bits"):
+        _plan(pk, [100], n)
+
+
 def test_replanning_forgets_the_selection(pk):
     p = _plan(pk, [100], 4)
     assert p.num_blocks == 4

@@ -138,6 +138,11 @@ ROPE = [
     ("nvfp4", 128, 48, False, 40, 8, 11, 128, "head pools"),
     ("nvfp4", 128, 80, False, 4, 4, 6, 16, "hnd"),
     ("nvfp4", 128, 112, True, 128, 8, 4, 1, "hnd"),
+    # more tokens than SMs: several rounds of fewer threads
+    ("bf16", 128, 128, False, 32, 8, 200, 16, "nhd"),
+    ("bf16", 64, 32, True, 40, 8, 153, 16, "hnd"),
+    ("e4m3", 128, 96, False, 32, 8, 160, 64, "nhd"),
+    ("nvfp4", 128, 96, False, 28, 4, 170, 16, "hnd"),
 ]
 
 
@@ -187,6 +192,24 @@ def test_rope_store_in_place_and_broadcast_inputs():
     # one row for all tokens and heads
     one = q[:1, :1].expand(6, 8, 128)
     assert torch.equal(pk.rope_store(one, k, v, pos, slots, b, rot), pk.rope_store(one.contiguous(), k, v, pos, slots, b, rot))
+
+
+def test_rope_store_of_single_rows_of_any_stride():
+    # the stride of a dimension of one is not used
+    pk = _pk()
+    base = torch.randn(4096, generator=torch.Generator().manual_seed(4)).to(torch.bfloat16).cuda()
+    one = base[:512].view(4, 128)
+    rot = pk.Rotary(128)
+    pos, slot = torch.tensor([77], device="cuda"), torch.tensor([3], device="cuda")
+    a, pa = _cache("bf16", 1, 16, 1, 128, "nhd")
+    b, pb = _cache("bf16", 1, 16, 1, 128, "nhd")
+    want = pk.rope_store(one[None], one[None, :1], one[None, 1:2], pos, slot, a, rot)
+    got = pk.rope_store(torch.as_strided(base, (1, 4, 128), (13, 128, 1)), torch.as_strided(base, (1, 1, 128), (1, 3, 1)),
+                        torch.as_strided(base, (1, 1, 128), (5, 7, 1), 128), pos, slot, b, rot)
+    assert torch.equal(got, want) and torch.equal(pa[0], pb[0]) and torch.equal(pa[1], pb[1])
+    with pytest.raises(pk.PkvError, match="strides"):
+        pk.rope_store(torch.as_strided(base, (2, 4, 128), (516, 128, 1)), torch.zeros((2, 1, 128), dtype=torch.bfloat16, device="cuda"),
+                      torch.zeros((2, 1, 128), dtype=torch.bfloat16, device="cuda"), pos.expand(2).contiguous(), slot.expand(2).contiguous(), b, rot)
 
 
 def test_rope_store_of_far_and_negative_positions():
@@ -268,6 +291,11 @@ BOUNDS = [
     ("nvfp4", [1, 15, 16, 17, 500], 4, 2, 16, 128, "hnd", None, "decode"),
     ("nvfp4", [260, 128, 3], 2, 1, 128, 128, "padded", [1, 1, 0], "decode"),
     ("nvfp4", [31, 64], 4, 4, 32, 128, "head pools", None, "decode"),
+    # more pages than one CTA each takes, their rows in several rounds
+    ("bf16", [7000, 5001], 4, 4, 40, 64, "nhd", None, "decode"),
+    ("bf16", [9000, 1], 2, 2, 33, 128, "hnd", [3000, 1], "mixed"),
+    ("e4m3", [8000, 39], 4, 4, 40, 128, "nhd", None, "decode"),
+    ("nvfp4", [8000, 121], 4, 4, 40, 128, "hnd", None, "decode"),
 ]
 
 
@@ -368,6 +396,8 @@ class Selection:
             codes = codes[r.randint(0, 3, P)]
         if kind == "equal":
             codes[:] = codes[:1]
+        if kind == "outlier":  # one page far above the others: most scores share a digit
+            codes = np.where(np.arange(P)[:, None, None, None] == self.idx[2][-1], 127, codes * 0.05)
         if kind == "extreme":
             codes = np.where(r.rand(*codes.shape) < 0.5, -127, 127)
         self.codes = np.clip(np.rint(codes), -127, 127).astype(np.int8)
@@ -419,10 +449,13 @@ SELECT = [
     ([33000, 60000, 5], 8, 2, 16, 128, 200, 1, 4),    # several CTAs per unit
     ([131071], 4, 1, 8, 128, 700, 3, 5),
     ([300 + i for i in range(300)], 4, 2, 16, 64, 9, 1, 1),
+    ([5000] * 30 + [6001], 4, 2, 16, 128, 60, 1, 1),   # a CTA per unit, an SM each
+    ([4700 + 9 * i for i in range(80)], 4, 2, 16, 128, 40, 1, 2),  # more units than SMs
+    ([9000, 8000], 6, 2, 16, 64, 50, 0, 3),            # several CTAs per unit, head_dim 64
 ]
 
 
-@pytest.mark.parametrize("kind", ["random", "few", "equal", "extreme"])
+@pytest.mark.parametrize("kind", ["random", "few", "equal", "extreme", "outlier"])
 @pytest.mark.parametrize("lens, heads, kv_heads, ps, D, K, sink, recent", SELECT)
 def test_select(lens, heads, kv_heads, ps, D, K, sink, recent, kind):
     Selection(lens, heads, kv_heads, ps, D, K, kind=kind, seed=len(lens)).check(sink, recent)
@@ -464,6 +497,9 @@ def test_select_refusals():
     for sink, recent in ((-1, 1), (0, 0), (5, 2), (2 ** 31 - 1, 2 ** 31 - 1)):
         with pytest.raises(pk.PkvError, match="num_sink"):
             s.plan.select(q, s.b, num_sink=sink, num_recent=recent)
+    for kw in (dict(num_sink=2 ** 32), dict(num_recent=2 ** 32 + 1), dict(num_sink=-2 ** 31 - 1)):
+        with pytest.raises(ValueError, match="32 bits"):
+            s.plan.select(q, s.b, **kw)
     with pytest.raises(pk.PkvError, match="bounds have"):
         s.plan.select(q, pk.KeyBounds(s.b.codes[:20].clone(), s.b.scale))
     with pytest.raises(ValueError, match="blocks"):
@@ -517,6 +553,9 @@ ATTEND = [
     ("nvfp4", [3000, 17, 450], 32, 8, 16, 128, "hnd", 40, 4),
     ("nvfp4", [700, 1, 640], 16, 2, 24, 128, "padded", 6, 0),
     ("nvfp4", [6000, 8000], 20, 1, 128, 128, "hnd", 30, 16),
+    ("bf16", [12000, 8191], 4, 2, 8, 128, "nhd", 1025, 0),     # more pages than are looked up ahead
+    ("e4m3", [9000], 4, 1, 8, 128, "nhd", 1100, 4),
+    ("nvfp4", [33000], 8, 1, 16, 128, "hnd", 1500, 20),
 ]
 
 
