@@ -8,11 +8,20 @@
 // that 32 bits hold (2 D terms below 2^15 2^7), so neither the order of a sum nor the split of the work moves a page
 // across the border, and a border is where the definition puts it.
 //
-// What bounds it: reading 2 D bytes of bounds per page, and the latency of the steps behind (a selection from
-// numbers that a few thousand threads hold).  One launch: a cluster of C CTAs per (request, KV head) scores its pages in
-// C slices, 8 lanes to a page (head_dim 128) by two-way 16 x 8 bit dot products; the scores go to the first
-// CTA's shared memory, which selects: a radix select on the scores less their smallest, by the digits that their
-// range has, then ballots and prefix counts that list the survivors in order.
+// What bounds it: reading 2 D bytes of bounds per page, and the latency of the steps before and behind.  One launch,
+// a unit per (request, KV head), in one of two forms:
+//   * narrow: a CTA of 256 threads per unit, four to an SM.  64 x 8 units of up to 256 pages (17.8 MB): 7.4 us, of which
+//     reading takes 2.8 at the measured copy rate; the rest is the way to the first bounds (request, page ids: 0.6 us), the
+//     weights (1.4), the selection (1.8) and the launch;
+//   * wide, for few units of many pages: a cluster of C CTAs of 512 threads scores its pages in C slices; the scores go to
+//     the first CTA's shared memory, which selects.  2 x 8 units of 8192 pages (33.5 MB): 14.2 us, 5.1 at the copy rate; the
+//     slices stream for 7.9 us (16 clusters of 6: 96 SMs; of 7 or 8 no 16 run at once, and half-size CTAs in clusters
+//     of 12 to 16 take 15.5), the selection behind them takes 3.7.
+// A page takes 8 lanes (head_dim 128): two 16-byte loads each, past L1 (14.4 -> 14.2 us), 16 two-way 16 x 8 bit dot
+// products, three shuffles.  Loads through a ring in shared memory instead of registers: 15.5 us (4 to 8 in flight), 17.7 (12).
+// The selection is a radix select on the scores less their smallest, cut by the digits that their range has (a range
+// known before the scores, from the weights, is too coarse: 18.0 us); once a digit holds at most 256 keys they are
+// compared with each other; then ballots and prefix counts list the survivors in order.
 
 #include <cooperative_groups.h>
 
@@ -29,7 +38,7 @@ namespace pkv {
 namespace {
 
 constexpr int kSelectMaxCluster = 8;
-constexpr int kFewPages = 256;     // competing pages that the narrow form takes in any case: a thread each
+constexpr int kFewPages = 768;     // competing pages that the narrow form takes in any case
 constexpr int kCandidates = 256;   // keys of one digit that are compared with each other
 
 // WIDE: a cluster of CTAs that have an SM each, for few units of many pages; narrow: a CTA of four on an SM.
@@ -450,9 +459,10 @@ cudaError_t launch_form(const SelectParams& p, int64_t units, int most, int num_
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  // Narrow for few pages (64 x 8 units of up to 256: 7.3 us; wide 12.8), and where units outnumber the SMs, which hold one
-  // wide CTA each (512 units of 400 to 512 pages 13.8 us, wide 32.6; 256 of 768 to 1024 pages 16.8, wide 23.3; 152 of
-  // as many 14.8, wide 12.4; 192 of 3072 to 4096 pages 49.6, wide 47.3).
+  // Narrow for few pages (128 units of up to 512 pages 6.8 us, wide 8.2; of 768 8.9, wide 9.8; of 1024 14.0, wide 11.0;
+  // 8 units of 512 pages 6.6, wide 8.0; of 1024 9.1, wide 7.9), and where units outnumber the SMs, which hold one wide
+  // CTA each (512 units of 400 to 512 pages 13.8 us, wide 32.6; 256 of 768 to 1024 pages 16.8, wide 23.3; 152 of as
+  // many 14.8, wide 12.4; 192 of 3072 to 4096 pages 49.6, wide 47.3).
   const bool wide = most > kFewPages && units <= num_sms;
   e = wide ? allow_shared_memory<D, true>(dev) : allow_shared_memory<D, false>(dev);
   if (e != cudaSuccess) return e;
