@@ -283,11 +283,12 @@ __device__ __forceinline__ void merge_accumulate(float4 (&acc)[NA], const int (&
   }
 }
 
+constexpr int kPageTable = 1024;  // pages of a unit that a run over selected pages looks up ahead
+
 // SCORED: every visible key's scaled score (log2 units) goes to p.logits, each row's log2-sum-exp to
 // p.lse2 (for the accumulated attention weights, decode_scored.cu).
 // BLOCKS: the unit's keys are those of the pages that p.blocks lists for its token row and KV head, in the list's
 // order; key positions (kv_begin, kv_end) count within them.
-constexpr int kPageTable = 1024;  // BLOCKS: pages of a unit that are looked up ahead
 template <int D, int KV, int NB, int HPB, bool SCORED, bool BLOCKS>
 __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB, HPB>::CTAS) decode_kernel(const RunParams p, int32_t* err) {
   using C = DecodeCfg<D, KV, NB, HPB>;
@@ -298,9 +299,6 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB, HPB>::CTAS) decode_k
 
   pdl_wait();  // the plan's metadata copy and the KV write before this run must be complete
   const WorkItem w = p.work[blockIdx.x];
-  const int ps = p.page_size;
-  const int ps_shift = (ps & (ps - 1)) == 0 ? __ffs(ps) - 1 : -1;  // page sizes are usually powers of 2
-  auto page_of = [&](int key) -> int { return ps_shift >= 0 ? key >> ps_shift : key / ps; };
   // BLOCKS: the pool's pages of the unit, looked up once by the whole CTA (two dependent reads for all of
   // them, instead of two before every tile), where they fit a table; -1: not a page of the request
   __shared__ int32_t s_pages[BLOCKS ? kPageTable : 1];
@@ -308,6 +306,9 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB, HPB>::CTAS) decode_k
   unsigned num_pages = 0;  // of the request
   bool tabled = false;
   if constexpr (BLOCKS) {
+    const int ps_log2 = __ffs(p.page_size) - 1;
+    const bool pow2 = (p.page_size & (p.page_size - 1)) == 0;
+    auto page_of = [&](int key) -> int { return pow2 ? key >> ps_log2 : key / p.page_size; };
     blocks = p.blocks + ((int64_t)w.q_row * p.num_kv_heads + w.kv_head) * p.num_blocks;
     num_pages = (unsigned)page_of(__ldg(&p.req[w.req].kv_len) - 1) + 1u;
     const int listed = page_of(w.kv_end - 1) + 1;
@@ -370,6 +371,9 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB, HPB>::CTAS) decode_k
   constexpr int RPI = 32 / C::CH;  // rows per warp instruction
   const int lc = lane % C::CH;
   const int lsub = lane / C::CH;
+  const int ps = p.page_size;
+  const int ps_shift = (ps & (ps - 1)) == 0 ? __ffs(ps) - 1 : -1;  // page sizes are usually powers of 2
+  auto page_of = [&](int key) -> int { return ps_shift >= 0 ? key >> ps_shift : key / ps; };
   // NVFP4: tiles start on multiples of 16, pages are a power of two and hold whole 16-key halves, and the
   // byte strides fit 32 bits; narrow: so do all offsets into the pools
   const bool halves_paged = FP4 && ps_shift >= 4 && (w.kv_begin & 15) == 0 &&
@@ -983,8 +987,10 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB, HPB>::CTAS) decode_k
       constexpr int U = C::CTAS >= 4 ? 20 : 32;
       const int ns = mi_.num_splits;
       const int n4 = rows * D / 4;
-      for (int col = threadIdx.x; col < n4; col += 128) {
-        const int crow = col * 4 / D;
+      for (int col0 = 0; col0 < (BLOCKS ? n4 : 1); col0 += 128) {
+        const int col = col0 + threadIdx.x;
+        const bool active = col < n4;
+        const int crow = active ? col * 4 / D : 0;
         const float* lse_g = p.part_lse + (int64_t)mi_.first_slot * kDecodeRows + crow;
         const float4* pm = reinterpret_cast<const float4*>(p.part_o + (int64_t)mi_.first_slot * kDecodeRows * D) + col;
         constexpr int SLOT4 = kDecodeRows * D / 4;
@@ -993,7 +999,7 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB, HPB>::CTAS) decode_k
         auto fetch = [&](float (&l)[U], float4 (&o)[U], int s0) {
 #pragma unroll
           for (int u = 0; u < U; ++u) {
-            const bool in = s0 + u < ns;
+            const bool in = active && s0 + u < ns;
             l[u] = in ? __ldcg(lse_g + (int64_t)(s0 + u) * kDecodeRows) : -INFINITY;
             o[u] = in ? __ldcg(pm + (int64_t)(s0 + u) * SLOT4) : make_float4(0.f, 0.f, 0.f, 0.f);
           }
@@ -1027,14 +1033,16 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB, HPB>::CTAS) decode_k
           fold(la, oa);
         }
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) + ((int64_t)mi_.q_row * p.num_qo_heads + qh0) * D;
-        const float f = W > 0.f ? p.out_scale / W : 0.f;
-        __nv_bfloat162* o2 = reinterpret_cast<__nv_bfloat162*>(out + col * 4);
-        o2[0] = __floats2bfloat162_rn(acc.x * f, acc.y * f);
-        o2[1] = __floats2bfloat162_rn(acc.z * f, acc.w * f);
-        if (p.lse && (col * 4) % D == 0)  // the row's first column writes its log-sum-exp
-          p.lse[(int64_t)mi_.q_row * p.num_qo_heads + qh0 + crow] = (m + __log2f(W)) * 0.69314718055994531f;
-        if constexpr (SCORED)
-          if ((col * 4) % D == 0) p.lse2[(int64_t)mi_.q_row * p.num_qo_heads + qh0 + crow] = m + __log2f(W);
+        if (active) {
+          const float f = W > 0.f ? p.out_scale / W : 0.f;
+          __nv_bfloat162* o2 = reinterpret_cast<__nv_bfloat162*>(out + col * 4);
+          o2[0] = __floats2bfloat162_rn(acc.x * f, acc.y * f);
+          o2[1] = __floats2bfloat162_rn(acc.z * f, acc.w * f);
+          if (p.lse && (col * 4) % D == 0)  // the row's first column writes its log-sum-exp
+            p.lse[(int64_t)mi_.q_row * p.num_qo_heads + qh0 + crow] = (m + __log2f(W)) * 0.69314718055994531f;
+          if constexpr (SCORED)
+            if ((col * 4) % D == 0) p.lse2[(int64_t)mi_.q_row * p.num_qo_heads + qh0 + crow] = m + __log2f(W);
+        }
       }
       if (threadIdx.x == 0) {  // ready for the next run of this plan
         p.unit_count[unit] = 0;
