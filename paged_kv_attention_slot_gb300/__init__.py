@@ -655,6 +655,15 @@ class Plan:
 
         blocks (plans made with num_blocks): int32 [total_tokens, num_kv_heads, num_blocks], the pages that each token's query
         heads see, as select gives them (pkv_attn_decode_run_blocks)."""
+        if blocks is not None:
+            if not self.num_blocks or scores is not None or merge_into:
+                raise ValueError("blocks need a plan made with num_blocks, and no scores or merge_into")
+            self._check_blocks(blocks, cache._device_index)
+            self._check_tensors(q, out, lse, cache)
+            out, lse = self._outputs(q, out, lse, return_lse, stream)
+            check(lib().pkv_attn_decode_run_blocks(self._h, q.data_ptr(), C.byref(cache.struct), blocks.data_ptr(), out.data_ptr(),
+                                                   lse.data_ptr() if lse is not None else None, self._use(stream)))
+            return (out, lse) if (return_lse or lse is not None) else out
         if self.mode == "ragged":
             raise ValueError("a ragged plan runs with run_ragged(q, k, v)")
         if self.mode == "paged_ragged":
@@ -665,20 +674,6 @@ class Plan:
             addr = _check_scores(scores, cache)
             if self.scratch is None:
                 raise ValueError("a scored run needs a plan with a workspace")
-        if blocks is not None:
-            if not self.num_blocks or scores is not None or merge_into:
-                raise ValueError("blocks need a plan made with num_blocks, and no scores or merge_into")
-            self._check_blocks(blocks, cache._device_index)
-            if out is not None or lse is not None:
-                self._check_tensors(q, out, lse, cache)
-            elif q.get_device() != cache._device_index:
-                raise ValueError("q must be on the cache's device")
-            else:
-                _check_device(cache)
-            out, lse = self._outputs(q, out, lse, return_lse, stream)
-            check(lib().pkv_attn_decode_run_blocks(self._h, q.data_ptr(), C.byref(cache.struct), blocks.data_ptr(), out.data_ptr(),
-                                                   lse.data_ptr() if lse is not None else None, self._use(stream)))
-            return (out, lse) if (return_lse or lse is not None) else out
         if merge_into:
             if self.mode not in ("prefill", "extend") or out is None or lse is None:
                 raise ValueError("merge_into needs a prefill plan and the held state in out and lse")

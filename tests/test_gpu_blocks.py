@@ -632,7 +632,7 @@ def test_runs_over_every_page_refuse_a_plan_over_selected_pages():
     assert L.pkv_attn_decode_run_blocks(d._h, c.q.data_ptr(), C.byref(c.cache.struct), blocks.data_ptr(), out.data_ptr(), None, None) == -1
     assert L.pkv_attn_decode_run_blocks(p._h, c.q.data_ptr(), C.byref(c.cache.struct), None, out.data_ptr(), None, None) == -1
     assert L.pkv_block_select(d._h, c.q.data_ptr(), out.data_ptr(), out.data_ptr(), 100, 1, 1, blocks.data_ptr(), None) == -1
-    with pytest.raises(ValueError, match="scores need"):
+    with pytest.raises(ValueError, match="blocks need"):
         p.run(c.q, c.cache, blocks=blocks, scores=torch.zeros((c.cache.num_pages, 2, 16), device="cuda"))
     with pytest.raises(ValueError, match="out must"):
         p.run(c.q, c.cache, blocks=blocks, out=out[:1])
