@@ -462,7 +462,7 @@ cudaError_t launch_form(const SelectParams& p, int64_t units, int most, int num_
   // Narrow for few pages (128 units of up to 512 pages 6.8 us, wide 8.2; of 768 8.9, wide 9.8; of 1024 14.0, wide 11.0;
   // 8 units of 512 pages 6.6, wide 8.0; of 1024 9.1, wide 7.9), and where units outnumber the SMs, which hold one wide
   // CTA each (512 units of 400 to 512 pages 13.8 us, wide 32.6; 256 of 768 to 1024 pages 16.8, wide 23.3; 152 of as
-  // many 14.8, wide 12.4; 192 of 3072 to 4096 pages 49.6, wide 47.3).
+  // many 14.8, wide 12.4; 192 of up to 4096 pages 49.6, wide 47.3).
   const bool wide = most > kFewPages && units <= num_sms;
   e = wide ? allow_shared_memory<D, true>(dev) : allow_shared_memory<D, false>(dev);
   if (e != cudaSuccess) return e;
