@@ -743,10 +743,14 @@ namespace {
 
 int plan_workspace_size(const pkv_plan_args* args, int32_t num_blocks, size_t* bytes) {
   if (!bytes) return fail(PKV_EINVAL, "bytes is NULL");
-  pkv_plan tmp;
-  int st = build_plan(args, &tmp, num_blocks);
-  if (st != PKV_OK) return st;
-  *bytes = tmp.need_bytes;
+  try {
+    pkv_plan tmp;
+    int st = build_plan(args, &tmp, num_blocks);
+    if (st != PKV_OK) return st;
+    *bytes = tmp.need_bytes;
+  } catch (const std::bad_alloc&) {
+    return fail(PKV_EUNSUPPORTED, "out of host memory while planning");
+  }
   return PKV_OK;
 }
 
