@@ -52,7 +52,7 @@ import numpy as np
 import torch
 
 from . import _lib
-from ._lib import PkvError, check, lib
+from ._lib import PkvError, binding, check, lib
 
 __all__ = [
     "KVCache", "KeyBounds", "Rotary", "Plan", "CascadePlan", "PkvError", "kv_store", "kv_load", "rope_store", "merge_state", "device_error", "block_table_to_csr",
@@ -353,43 +353,14 @@ def rope_store(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: tor
     strides multiples of 8 (views of one projection's output).  positions, slot_mapping: [T] int64, device.
     Returns the turned q, contiguous (q_out, which may be q), or (q, k) with return_k=True or a k_out to
     write the turned keys to (for the ragged runs).  scores: as kv_store."""
-    d = cache._device_index
-    _, _, H, D = cache._geometry
-    if q.dim() != 3:
-        raise ValueError("q must be [T, num_qo_heads, head_dim]")
-    T, Hq, width = q.shape
-    if width != D or k.shape != (T, H, D) or v.shape != (T, H, D):
-        raise ValueError("q must be [T, num_qo_heads, head_dim], k and v [T, num_kv_heads, head_dim] of the cache's geometry")
-    if rotary.head_dim != D:
-        raise ValueError(f"the rotary is for head_dim {rotary.head_dim}, the cache has {D}")
-    qt, qh, qe = q.stride()
-    kt, kh, ke = k.stride()
-    vt, vh, ve = v.stride()
-    bf16, i64 = torch.bfloat16, torch.int64
-    if (q.dtype != bf16 or k.dtype != bf16 or v.dtype != bf16 or not qe == ke == ve == 1
-            or not q.get_device() == k.get_device() == v.get_device() == d):
-        raise ValueError("q, k and v must be bf16 tensors on the cache's device with a contiguous last dimension")
-    if (positions.dtype != i64 or slot_mapping.dtype != i64 or positions.shape != (T,) or slot_mapping.shape != (T,)
-            or not positions.is_contiguous() or not slot_mapping.is_contiguous()
-            or not positions.get_device() == slot_mapping.get_device() == d):
-        raise ValueError("positions and slot_mapping must be contiguous int64 tensors [T] on the cache's device")
-    if rotary._device_index != d:
-        raise ValueError("the rotary must be on the cache's device")
-    for t, like in ((q_out, q), (k_out, k)):
-        if t is not None and (t.dtype != bf16 or t.shape != like.shape or not t.is_contiguous() or t.get_device() != d):
-            raise ValueError("q_out and k_out must be contiguous bf16 tensors like q and k")
-    _check_device(cache)
-    return_k = return_k or k_out is not None
-    if q_out is None:
-        q_out = _new((T, Hq, D), bf16, cache._device, stream)
-    if k_out is None and return_k:
-        k_out = _new((T, H, D), bf16, cache._device, stream)
-    a = _lib.pkv_rope_args(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), k_out.data_ptr() if return_k else None, positions.data_ptr(),
-        slot_mapping.data_ptr(), rotary._phase_step, _check_scores(scores, cache) if scores is not None else None, T,
-        qt, qh, kt, kh, vt, vh, Hq, rotary.rotary_dim, rotary.interleaved, rotary.amplitude)
-    check(lib().pkv_rope_kv_store(C.byref(a), C.byref(cache.struct), _stream_ptr(stream)))
-    return (q_out, k_out) if return_k else q_out
+    if stream is not None:
+        return_k = return_k or k_out is not None
+        q_out = _new(q.shape, torch.bfloat16, cache._device, stream) if q_out is None else q_out
+        k_out = _new(k.shape, torch.bfloat16, cache._device, stream) if k_out is None and return_k else k_out
+    return binding().rope_store(
+        C.addressof(cache.struct), cache._device_index, stream, q, k, v, positions, slot_mapping, rotary._phase_step,
+        rotary._device_index, rotary.head_dim, rotary.rotary_dim, rotary.interleaved, rotary.amplitude,
+        0 if scores is None else _check_scores(scores, cache), q_out, k_out, return_k)
 
 
 class KeyBounds:
@@ -407,8 +378,6 @@ class KeyBounds:
         if scale.device != codes.device:
             raise ValueError("codes and scale must be on one device")
         self.codes, self.scale = codes, scale
-        self._pages, self._heads = codes.shape[0], (codes.shape[1], codes.shape[3])
-        self._device, self._device_index = codes.device, codes.get_device()
 
     @classmethod
     def of(cls, cache: KVCache, scale) -> "KeyBounds":
@@ -658,12 +627,13 @@ class Plan:
         if blocks is not None:
             if not self.num_blocks or scores is not None or merge_into:
                 raise ValueError("blocks need a plan made with num_blocks, and no scores or merge_into")
-            self._check_blocks(blocks, cache._device_index)
-            self._check_tensors(q, out, lse, cache)
-            out, lse = self._outputs(q, out, lse, return_lse, stream)
-            check(lib().pkv_attn_decode_run_blocks(self._h, q.data_ptr(), C.byref(cache.struct), blocks.data_ptr(), out.data_ptr(),
-                                                   lse.data_ptr() if lse is not None else None, self._use(stream)))
-            return (out, lse) if (return_lse or lse is not None) else out
+            if stream is not None:
+                rows = (self.total_tokens, self.num_qo_heads)
+                out = _new((*rows, self.head_dim), torch.bfloat16, cache._device, stream) if out is None else out
+                lse = _new(rows, torch.float32, cache._device, stream) if lse is None and return_lse else lse
+            return binding().run_blocks(
+                self._h.value, self, self._streams, stream, C.addressof(cache.struct), cache._device_index, self._blocks_shape,
+                self.num_qo_heads, self.head_dim, q, blocks, out, lse, return_lse)
         if self.mode == "ragged":
             raise ValueError("a ragged plan runs with run_ragged(q, k, v)")
         if self.mode == "paged_ragged":
@@ -701,11 +671,6 @@ class Plan:
                      lse.data_ptr() if lse is not None else None, s))
         return (out, lse) if (return_lse or lse is not None) else out
 
-    def _check_blocks(self, blocks, device_index) -> None:
-        if (blocks.dtype != torch.int32 or blocks.shape != self._blocks_shape or not blocks.is_contiguous()
-                or blocks.get_device() != device_index):
-            raise ValueError(f"blocks must be a contiguous int32 tensor {list(self._blocks_shape)} on the cache's device")
-
     def token_map(self, offsets: torch.Tensor | None = None, stream=None):
         """Positions and slots of the planned new tokens: (positions, slot_mapping), int64 [total_tokens].
 
@@ -713,25 +678,17 @@ class Plan:
         [batch_size], added to the positions of each request's tokens, e.g. the keys that evict dropped."""
         if self.workspace is None:
             raise ValueError("token_map needs a plan with a workspace")
-        device = self.workspace.device
-        if offsets is not None and (offsets.dtype != torch.int64 or offsets.shape != (self.batch_size,) or not offsets.is_contiguous()
-                                    or offsets.device != device):
-            raise ValueError(f"offsets must be a contiguous int64 tensor [{self.batch_size}] on the plan's device")
-        positions, slots = (_new((self.total_tokens,), torch.int64, device, stream) for _ in range(2))
-        check(lib().pkv_token_map(self._h, offsets.data_ptr() if offsets is not None else None, positions.data_ptr(),
-                                  slots.data_ptr(), self._use(stream)))
-        return positions, slots
+        positions = slots = None
+        if stream is not None:
+            positions, slots = (_new((self.total_tokens,), torch.int64, self.workspace.device, stream) for _ in range(2))
+        return binding().token_map(self._h.value, self, self._streams, stream, self.total_tokens, self.batch_size, self.workspace,
+                                   offsets, positions, slots)
 
     def bound_keys(self, cache: KVCache, bounds: KeyBounds, all_pages: bool = False, stream=None) -> None:
         """Write the bounds of the keys of the planned requests' pages: of those that hold a new token (every step,
         after the KV write), or of all of them (a cache without bounds, or after evict)."""
-        if bounds._pages != cache._geometry[0] or bounds._heads != cache._geometry[2:]:
-            raise ValueError("the bounds do not match the cache's geometry")
-        if bounds._device_index != cache._device_index:
-            raise ValueError("the bounds must be on the cache's device")
-        _check_device(cache)
-        check(lib().pkv_key_bounds_update(self._h, C.byref(cache.struct), bounds.codes.data_ptr(), bounds.scale.data_ptr(),
-                                          1 if all_pages else 0, self._use(stream)))
+        binding().bound_keys(self._h.value, self, self._streams, stream, C.addressof(cache.struct), cache._device_index,
+                             bounds.codes, bounds.scale, all_pages)
 
     def select(self, q: torch.Tensor, bounds: KeyBounds, num_sink: int = 1, num_recent: int = 1,
                blocks: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -742,21 +699,10 @@ class Plan:
         largest upper bound of q.k, summed over the query heads of the KV head (pkv_block_select)."""
         if not self.num_blocks:
             raise ValueError("select needs a plan made with num_blocks")
-        d = bounds._device_index
-        shape = (self.total_tokens, self.num_qo_heads, self.head_dim)
-        if q.dtype != torch.bfloat16 or q.shape != shape or not q.is_contiguous() or q.get_device() != d:
-            raise ValueError(f"q must be a contiguous bf16 tensor {list(shape)} on the bounds' device")
-        if bounds._heads != (self.num_kv_heads, self.head_dim):
-            raise ValueError("the bounds do not match the plan's KV heads and head_dim")
-        if d < 0 or d != _get_device():
-            raise ValueError("the bounds must be on the current CUDA device")
-        if blocks is None:
-            blocks = _new(self._blocks_shape, torch.int32, bounds._device, stream)
-        else:
-            self._check_blocks(blocks, d)
-        check(lib().pkv_block_select(self._h, q.data_ptr(), bounds.codes.data_ptr(), bounds.scale.data_ptr(), bounds._pages,
-                                     _int32(num_sink), _int32(num_recent), blocks.data_ptr(), self._use(stream)))
-        return blocks
+        if stream is not None and blocks is None:
+            blocks = _new(self._blocks_shape, torch.int32, bounds.codes.device, stream)
+        return binding().select(self._h.value, self, self._streams, stream, self._blocks_shape, self.num_qo_heads, self.head_dim,
+                                q, bounds.codes, bounds.scale, num_sink, num_recent, blocks)
 
     def evict(self, cache: KVCache, scores: torch.Tensor, budget: int, num_sink: int = 0, num_recent: int = 0,
               kept: torch.Tensor | None = None, stream=None) -> torch.Tensor:

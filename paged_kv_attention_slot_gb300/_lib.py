@@ -1,6 +1,7 @@
 """ctypes declarations for libpkv_attn.so (the C ABI declared in include/pkv_attn.h).
 
-Argument marshalling only.  The library is loaded lazily on first use; if it is missing the call
+Argument marshalling only; the calls of a decode step over selected pages go through a compiled
+module instead (binding()).  The library is loaded lazily on first use; if it is missing the call
 fails loudly (there is no other implementation to fall back to).
 """
 
@@ -12,6 +13,7 @@ import threading
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libpkv_attn.so")
+BINDING_PATH = os.path.join(HERE, "_binding.so")
 
 PKV_OK = 0
 PKV_EINVAL = -1
@@ -179,7 +181,9 @@ _SIGS = {
 }
 
 _lib = None
+_binding = None
 _lock = threading.Lock()
+_BINDING_CALLS = ("pkv_token_map", "pkv_rope_kv_store", "pkv_key_bounds_update", "pkv_block_select", "pkv_attn_decode_run_blocks")
 
 
 def lib():
@@ -200,6 +204,25 @@ def lib():
                 f.argtypes = args
             _lib = L
     return _lib
+
+
+def binding():
+    """The compiled calls of a step over selected pages (csrc/python/binding.cpp), attached to the library."""
+    global _binding
+    if _binding is not None:
+        return _binding
+    L = lib()
+    with _lock:
+        if _binding is None:
+            try:
+                from . import _binding as B
+            except ImportError as e:
+                raise RuntimeError(
+                    f"{BINDING_PATH} is missing or does not fit this Python and torch: build it with "
+                    "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+            B.attach(check, *(C.cast(getattr(L, name), C.c_void_p).value for name in _BINDING_CALLS))
+            _binding = B
+    return _binding
 
 
 def check(status: int) -> None:

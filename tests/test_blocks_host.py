@@ -3,6 +3,7 @@ phase steps of Rotary, the plans over selected pages, and every refusal of the e
 
 import ctypes as C
 import math
+import sys
 
 import numpy as np
 import pytest
@@ -325,3 +326,34 @@ def test_calls_on_host_plans_and_mismatched_bounds_are_refused(pk):
         p.select(q, pk.KeyBounds.of(_cache(pk, H=1), 1.0))
     with pytest.raises(ValueError, match="CUDA device"):
         p.select(q, b)
+
+
+# ---- the compiled calls ----
+def test_compiled_calls_refuse_other_kinds_and_keep_no_reference(pk):
+    p, cache = _plan(pk, [100, 50], 4), _cache(pk, P=11)
+    b, q = pk.KeyBounds.of(cache, 0.03), torch.zeros((2, 8, 128), dtype=torch.bfloat16)
+    i32 = torch.zeros((2, 2, 4), dtype=torch.int32)
+    refused = [lambda: p.select([1], b), lambda: p.select(None, b),
+               lambda: p.select(q, b, num_sink=1.5), lambda: p.select(q, b, num_recent="1"), lambda: p.run("q", cache, blocks=i32),
+               lambda: p.run(q, cache, blocks=i32, out=3), lambda: pk._lib.binding().select(1, 2),
+               lambda: pk._lib.binding().select(*[None] * 13), lambda: pk._lib.binding().attach()]
+    held = [q, i32, b.codes, b.scale, p, p._streams, p._blocks_shape, p._blocks_shape[2]]
+    before = [sys.getrefcount(x) for x in held]
+    for _ in range(50):
+        for f in refused:
+            with pytest.raises(TypeError):
+                f()
+        for f in (lambda: p.select(q, b), lambda: p.run(q, cache, blocks=i32), lambda: p.run(q, cache, blocks=i32, out=q),
+                  lambda: p.select(q, b, blocks=i32), lambda: p.select(q, b, num_sink=2 ** 31), lambda: p.select(q, b, num_recent=-2 ** 40)):
+            with pytest.raises(ValueError):
+                f()
+    assert [sys.getrefcount(x) for x in held] == before
+
+
+def test_a_missing_binding_fails_loudly(pk, monkeypatch):
+    pk._lib.binding()
+    monkeypatch.setattr(pk._lib, "_binding", None)
+    monkeypatch.delattr(pk, "_binding")
+    monkeypatch.setitem(sys.modules, pk.__name__ + "._binding", None)
+    with pytest.raises(RuntimeError, match="_binding.so"):
+        pk._lib.binding()

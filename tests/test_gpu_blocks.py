@@ -11,6 +11,8 @@ Tolerances:
 
 import ctypes as C
 import math
+import sys
+import threading
 
 import numpy as np
 import pytest
@@ -814,3 +816,74 @@ def test_memory_of_results_on_another_stream():
     b2 = p.select(qo2, s.bounds)
     assert torch.equal(pos, pos2) and torch.equal(slots, slots2) and torch.equal(qo, qo2) and torch.equal(blocks, b2)
     assert torch.equal(a, p.run(qo2, s.cache, blocks=b2))
+
+
+def test_calls_return_the_given_outputs_and_keep_nothing():
+    s = Server([700, 45], 8, 2, 16, "bf16", 8, seed=7)
+    s.lens = [700, 45]
+    p = s.plan([1, 1], "decode", num_blocks=8)
+    q, k, v = s.tokens(2)
+    p.bound_keys(s.cache, s.bounds, all_pages=True)
+    given = [torch.empty_like(q), torch.empty_like(k), torch.empty((2, 2, 8), dtype=torch.int32, device="cuda"), torch.empty_like(q),
+             torch.empty((2, 8), device="cuda")]
+    qo, ko, blocks, out, lse = given
+
+    def step(give):
+        pos, slots = p.token_map()
+        r = s.pk.rope_store(q, k, v, pos, slots, s.cache, s.rot, *((qo, ko) if give else ()), return_k=True)
+        p.bound_keys(s.cache, s.bounds)
+        b = p.select(r[0], s.bounds, blocks=blocks if give else None)
+        return (*r, b, *p.run(r[0], s.cache, *((out, lse) if give else ()), return_lse=True, blocks=b))
+
+    assert all(a is b for a, b in zip(step(True), given))
+    assert all(torch.equal(a, b) for a, b in zip(step(False)[:3], given))
+    everything = [*given, q, k, v, p, p.workspace, p._streams, s.cache, s.cache.struct, s.bounds.codes, s.rot.phase_step]
+    before, memory = [sys.getrefcount(x) for x in everything], torch.cuda.memory_allocated()
+    for i in range(60):
+        step(i % 2 == 0)
+    assert [sys.getrefcount(x) for x in everything] == before and torch.cuda.memory_allocated() == memory
+
+
+def test_steps_from_several_threads_and_streams():
+    servers = [Server([700 + 16 * i, 45], 8, 2, 16, "bf16", 8, seed=8 + i) for i in range(4)]
+    work = []
+    for i, s in enumerate(servers):
+        for x in s.pools:
+            x.copy_(torch.randn(x.shape, generator=torch.Generator(device="cuda").manual_seed(i), device="cuda"))
+        s.lens = [700 + 16 * i, 45]
+        p, stream = s.plan([1, 1], "decode", num_blocks=8), torch.cuda.Stream()
+        p.bound_keys(s.cache, s.bounds, all_pages=True)
+        work.append((s, p, stream, s.tokens(2)))
+
+    def step(s, p, t):
+        pos, slots = p.token_map()
+        qo = s.pk.rope_store(*t, pos, slots, s.cache, s.rot)
+        p.bound_keys(s.cache, s.bounds)
+        blocks = p.select(qo, s.bounds)
+        return pos, slots, qo, blocks, p.run(qo, s.cache, blocks=blocks)
+
+    want = [[x.clone() for x in step(s, p, t)] for s, p, _, t in work]
+    torch.cuda.synchronize()
+    got, failed = [None] * 4, []
+
+    def run(i):
+        try:
+            s, p, stream, t = work[i]
+            with torch.cuda.stream(stream):
+                for _ in range(100):
+                    got[i] = step(s, p, t)
+                stream.synchronize()
+                assert stream.cuda_stream in p._streams  # the plan's workspace is recorded on it
+        except BaseException as e:
+            failed.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    for a, b in zip(got, want):
+        assert all(torch.equal(x, y) for x, y in zip(a[:4], b[:4]))
+        # (shared units claim their keys at run time: float32 sums in another order, one rounding)
+        assert torch.allclose(a[4].float(), b[4].float(), rtol=2.0 ** -6, atol=2.0 ** -10)
