@@ -208,7 +208,8 @@ def _new(shape, dtype, device, stream) -> torch.Tensor:
         stream = torch.cuda.ExternalStream(int(stream.cuda_stream))
     with torch.cuda.stream(stream):
         t = torch.empty(shape, dtype=dtype, device=device)
-    t.record_stream(reader)
+    if t.is_cuda:  # (a tensor elsewhere: the call is about to be refused)
+        t.record_stream(reader)
     return t
 
 

@@ -887,3 +887,19 @@ def test_steps_from_several_threads_and_streams():
         assert all(torch.equal(x, y) for x, y in zip(a[:4], b[:4]))
         # (shared units claim their keys at run time: float32 sums in another order, one rounding)
         assert torch.allclose(a[4].float(), b[4].float(), rtol=2.0 ** -6, atol=2.0 ** -10)
+
+
+def test_host_tensors_with_a_stream_are_refused():
+    pk = _pk()
+    k = torch.zeros((11, 16, 2, 128), dtype=torch.bfloat16)
+    cache, side = pk.KVCache(k, k.clone()), torch.cuda.Stream()
+    p = pk.Plan().plan(*_batch([100, 50], [1, 1], 16)[0], num_qo_heads=8, num_kv_heads=2, head_dim=128, page_size=16, mode="decode",
+                       num_blocks=4)
+    q, kv, i = torch.zeros((2, 8, 128), dtype=torch.bfloat16), torch.zeros((2, 2, 128), dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int64)
+    b, blocks = pk.KeyBounds.of(cache, 1.0), torch.zeros((2, 2, 4), dtype=torch.int32)
+    for f in (lambda: pk.rope_store(q, kv, kv, i, i, cache, pk.Rotary(128, device="cpu"), stream=side), lambda: p.bound_keys(cache, b, stream=side),
+              lambda: p.select(q, b, stream=side), lambda: p.run(q, cache, blocks=blocks, stream=side, return_lse=True)):
+        with pytest.raises(ValueError, match="current CUDA device"):
+            f()
+    with pytest.raises(ValueError, match="offsets"):
+        p.token_map(i, stream=side)
