@@ -84,7 +84,9 @@ enum {
   PKV_DEVERR_NONE = 0,
   PKV_DEVERR_SLOT_RANGE = 1,   /* kv_store, kv_load: slot_mapping entry >= num_pages * page_size  */
   PKV_DEVERR_PAGE_RANGE = 2,   /* attention: a page id outside [0, num_pages)                     */
-  PKV_DEVERR_TIMEOUT = 3       /* a bounded wait inside a kernel ran out; the kernel returned     */
+  PKV_DEVERR_TIMEOUT = 3,      /* a bounded wait inside a kernel ran out; the kernel returned     */
+  PKV_DEVERR_CAPACITY = 4      /* block_select: a captured call's plan was made anew for a request
+                                * of more pages than the call was captured for                    */
 };
 
 /* ---------------------------------------------------------------------------------------------- */
@@ -354,6 +356,9 @@ int pkv_kv_evict(const pkv_plan* plan, const pkv_cache* cache, float* scores, in
  *   once per layer      pkv_rope_kv_store, pkv_key_bounds_update, pkv_block_select, pkv_attn_decode_run_blocks
  * "Block" b of a request is the b-th page of its page list.  Pages of at least 8 tokens; requests of up to 49152
  * pages; at most 128 query heads per KV head.
+ * A call captured in a graph keeps what the plan held on the host then (counts of requests, tokens, work items and pages,
+ * the longest request, num_blocks): like the runs', its replays serve the plan made anew in place for the same
+ * lengths and num_blocks, over any pages.
  */
 
 /*
@@ -445,6 +450,8 @@ int pkv_plan_blocks_workspace_size(const pkv_plan_args* args, int32_t num_blocks
  *   codes, scale  as pkv_key_bounds_update; num_pages: pages that codes has.
  *   num_sink >= 0, num_recent >= 1, num_sink + num_recent <= num_blocks.
  *   blocks   device int32 [total_tokens, num_kv_heads, num_blocks] (out): ascending blocks of the request, -1 behind them.
+ * A captured call has room for the scores of the longest request it was captured with: a longer one is recorded as
+ * PKV_DEVERR_CAPACITY and gets a row of -1.
  */
 int pkv_block_select(const pkv_plan* plan, const void* q, const int8_t* codes, const float* scale, int64_t num_pages,
                      int32_t num_sink, int32_t num_recent, int32_t* blocks, void* stream);

@@ -497,8 +497,9 @@ class Plan:
         mode "ragged": kv_indptr holds row offsets into contiguous k / v tensors (run with
         run_ragged); kv_indices, last_page_len and page_size are ignored.  causal=False: every query
         sees all keys of its request (prefill / ragged plans).  scored=True (decode and mixed plans):
-        reserve the scratch of run(..., scores=...) and check that no page is listed twice.  A workspace
-        or scratch that a captured graph uses must not grow: plan the largest batch first.
+        reserve the scratch of run(..., scores=...) and check that no page is listed twice.  A captured
+        graph's replays serve this plan made anew for the same lengths (any pages, new values) in the same workspace;
+        a workspace or scratch that a captured graph uses must not grow: plan the largest batch first.
 
         num_blocks > 0 (decode plans without a sliding window): the runs read that many selected pages of each
         request (select, then run(..., blocks=...)); requests with fewer pages all of theirs."""
@@ -697,7 +698,8 @@ class Plan:
         num_blocks], ascending page numbers within the request, -1 behind them.
 
         Of a request with more than num_blocks pages the first num_sink and the last num_recent (at least 1), and the others with the
-        largest upper bound of q.k, summed over the query heads of the KV head (pkv_block_select)."""
+        largest upper bound of q.k, summed over the query heads of the KV head (pkv_block_select).  A captured call has room for
+        the longest request it was captured with: a longer one gets a row of -1, and device_error() tells."""
         if not self.num_blocks:
             raise ValueError("select needs a plan made with num_blocks")
         if stream is not None and blocks is None:

@@ -35,6 +35,8 @@ namespace cg = cooperative_groups;
 
 namespace pkv {
 
+int32_t* device_error_ptr();
+
 namespace {
 
 constexpr int kSelectMaxCluster = 8;
@@ -122,6 +124,13 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, Form<WIDE>::CTAS) block_s
     return;
   }
   const int nb = N - S - R;  // competing pages S .. N - R - 1
+  if (nb > p.key_cap) {     // (the whole cluster) a captured call whose plan was made anew for longer requests
+    if (rank == 0) {
+      if (tid == 0) record_error(p.err, PKV_DEVERR_CAPACITY);
+      for (int j = tid; j < K; j += THREADS) out[j] = -1;
+    }
+    return;
+  }
   if (rank == 0) {
     for (int k = tid; k < BINS; k += THREADS) sh.hist[k] = 0u;
     if (tid == 0) {
@@ -496,6 +505,8 @@ cudaError_t launch_block_select(SelectParams p, int32_t batch, int32_t max_block
   const int32_t most = std::max(1, max_blocks - p.num_sink - p.num_recent);
   p.key_cap = (most + 31) / 32 * 32;
   p.by_page = divider(p.page_size);
+  p.err = device_error_ptr();
+  if (!p.err) return cudaErrorInvalidDevice;
   return p.head_dim == 128 ? launch_form<128>(p, units, most, num_sms, s) : launch_form<64>(p, units, most, num_sms, s);
 }
 

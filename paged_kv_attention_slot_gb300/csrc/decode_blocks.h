@@ -38,8 +38,9 @@ struct SelectParams {
   int32_t* blocks;  // [total_tokens, num_kv_heads, num_blocks]
   int32_t num_kv_heads, group, head_dim, page_size;
   int32_t num_blocks, num_sink, num_recent;
-  int32_t key_cap;  // set by the launcher, as by_page
+  int32_t key_cap;  // competing pages that the launch has room for (set by the launcher, as the members behind it)
   Divider by_page;
+  int32_t* err;
 };
 // max_blocks: pages of the longest request
 cudaError_t launch_block_select(SelectParams p, int32_t batch, int32_t max_blocks, int num_sms, cudaStream_t s);

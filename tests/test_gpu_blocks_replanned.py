@@ -1,0 +1,85 @@
+"""Captured calls of a decode step over selected pages whose plan is made anew in place: for the same lengths over other
+pages, as documented, and for anything else that leaves the workspace's layout alone, which must end in a recorded error
+or in rows that say so, never in an access out of range."""
+
+import numpy as np
+import pytest
+import torch
+
+from tests.test_gpu_blocks import Selection, _batch, _np
+
+pytestmark = pytest.mark.gpu
+
+SLOT_RANGE, PAGE_RANGE, CAPACITY = 1, 2, 4
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    import paged_kv_attention_slot_gb300 as pk
+
+    pk._lib.lib()
+    assert pk.device_error() == 0
+    yield
+    assert pk.device_error() == 0
+
+
+def _pk():
+    import paged_kv_attention_slot_gb300 as pk
+
+    return pk
+
+
+def _capture(fn):
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        fn()
+    return graph
+
+
+# ---- selection ----
+@pytest.mark.parametrize("heads, kv_heads, D, short, long", [
+    (8, 8, 128, 60, 63),       # within the same 32 pages of scores: served
+    (8, 8, 128, 60, 200),      # one CTA per unit
+    (4, 2, 64, 700, 769),
+    (4, 2, 128, 2000, 2600),   # clusters
+    (2, 1, 64, 2000, 9000),
+    (2, 1, 128, 40000, 49152)])
+def test_a_captured_selection_refuses_longer_requests(heads, kv_heads, D, short, long):
+    # request 1 grows from `short` to `long` pages; the other, as long as it was, is served beside it
+    ps, K, keep = 8, 8, 30
+    s = Selection([keep * ps - 3, short * ps - 5], heads, kv_heads, ps, D, K, seed=1)
+    t = Selection([keep * ps - 3, long * ps - 5], heads, kv_heads, ps, D, K, seed=2)
+    pk = _pk()
+    P = len(t.codes)
+    codes = torch.zeros((P, kv_heads, 2, D), dtype=torch.int8, device="cuda")
+    codes[:len(s.codes)] = s.b.codes
+    b, q = pk.KeyBounds(codes, s.b.scale.clone()), s.q.cuda()
+    blocks = torch.empty((2, kv_heads, K), dtype=torch.int32, device="cuda")
+    kw = dict(num_qo_heads=heads, num_kv_heads=kv_heads, head_dim=D, page_size=ps, mode="decode", num_blocks=K)
+    at = s.plan.workspace.data_ptr()
+    graph = _capture(lambda: s.plan.select(q, b, num_sink=1, num_recent=2, blocks=blocks))
+    want = s.want(1, 2)
+    for _ in range(2):
+        s.plan.plan(*s.idx, **kw)
+        codes[:len(s.codes)] = s.b.codes
+        b.scale.copy_(s.b.scale)
+        q.copy_(s.q)
+        blocks.fill_(99)
+        graph.replay()
+        assert pk.device_error() == 0 and np.array_equal(_np(blocks), want)
+        s.plan.plan(*t.idx, **kw)
+        assert s.plan.workspace.data_ptr() == at
+        codes.copy_(t.b.codes)
+        b.scale.copy_(t.b.scale)
+        q.copy_(t.q)
+        blocks.fill_(99)
+        graph.replay()
+        other = t.want(1, 2)
+        if long - 3 > -(-(short - 3) // 32) * 32:
+            assert pk.device_error() == CAPACITY
+            other[1] = -1
+        else:
+            assert pk.device_error() == 0
+        assert np.array_equal(_np(blocks), other)
