@@ -83,7 +83,8 @@ typedef enum {
 enum {
   PKV_DEVERR_NONE = 0,
   PKV_DEVERR_SLOT_RANGE = 1,   /* kv_store, kv_load: slot_mapping entry >= num_pages * page_size  */
-  PKV_DEVERR_PAGE_RANGE = 2,   /* attention: a page id outside [0, num_pages)                     */
+  PKV_DEVERR_PAGE_RANGE = 2,   /* attention, block_select: a page id outside
+                                * [0, num_pages)                                                  */
   PKV_DEVERR_TIMEOUT = 3,      /* a bounded wait inside a kernel ran out; the kernel returned     */
   PKV_DEVERR_CAPACITY = 4      /* block_select: a captured call's plan was made anew for a request
                                 * of more pages than the call was captured for                    */
@@ -358,7 +359,8 @@ int pkv_kv_evict(const pkv_plan* plan, const pkv_cache* cache, float* scores, in
  * pages; at most 128 query heads per KV head.
  * A call captured in a graph keeps what the plan held on the host then (counts of requests, tokens, work items and pages,
  * the longest request, num_blocks): like the runs', its replays serve the plan made anew in place for the same
- * lengths and num_blocks, over any pages.
+ * lengths and num_blocks, over any pages; one that the pool or the bounds do not have (which a call outside a graph
+ * refuses) is recorded as PKV_DEVERR_PAGE_RANGE and nothing out of bounds is read or written.
  */
 
 /*

@@ -569,14 +569,14 @@ int build_plan(const pkv_plan_args* a, pkv_plan* P, int32_t num_blocks = 0) {
   if (kPrefillGroupOrder) order_by_group(P->work, (size_t)P->num_decode_work, P->work.size(), a->num_kv_heads);
   if ((int64_t)P->work.size() > INT32_MAX) return fail(PKV_EUNSUPPORTED, "too many CTAs");
 
-  // workspace layout: [work][merge][req][kv_indices] | [partial lse][partial o]
+  // workspace layout: [work][merge][req, max_page_id][kv_indices] | [partial lse][partial o]
   size_t off = 0;
   P->off_work = off;
   off = align_up(off + P->work.size() * sizeof(WorkItem), 256);
   P->off_merge = off;
   off = align_up(off + P->merge.size() * sizeof(MergeItem), 256);
   P->off_req = off;
-  off = align_up(off + P->req.size() * sizeof(ReqInfo), 256);
+  off = align_up(off + P->req.size() * sizeof(ReqInfo) + sizeof(int32_t), 256);
   P->off_idx = off;
   off = align_up(off + P->indices.size() * sizeof(int32_t), 256);
   P->off_count = off;  // [unit_count | claim lines], zero-filled by the metadata copy; zero again after each run
@@ -822,6 +822,8 @@ int make_plan(pkv_plan* plan, const pkv_plan_args* args, int32_t num_blocks, voi
   std::memcpy(h + plan->off_work, plan->work.data(), plan->work.size() * sizeof(WorkItem));
   std::memcpy(h + plan->off_merge, plan->merge.data(), plan->merge.size() * sizeof(MergeItem));
   std::memcpy(h + plan->off_req, plan->req.data(), plan->req.size() * sizeof(ReqInfo));
+  const int32_t max_page = (int32_t)std::min<int64_t>(plan->max_page_id, INT32_MAX);
+  std::memcpy(h + plan->off_req + plan->req.size() * sizeof(ReqInfo), &max_page, sizeof(max_page));
   std::memcpy(h + plan->off_idx, plan->indices.data(), plan->indices.size() * sizeof(int32_t));
   cudaStream_t s = (cudaStream_t)stream;
   // a small kernel reading the mapped staging buffer: a DMA copy of this size spends most of its
@@ -1166,6 +1168,11 @@ int check_paged_plan(const pkv_plan* P, const char* what) {
   return PKV_OK;
 }
 
+// The plan's largest page id on the device.
+const int32_t* max_page_ptr(const pkv_plan* P) {
+  return (const int32_t*)((const char*)P->ws + P->off_req + P->req.size() * sizeof(ReqInfo));
+}
+
 int check_bounds(const int8_t* codes, const float* scale) {
   if (!codes || !scale) return fail(PKV_EINVAL, "codes and scale must be non-NULL");
   if (((uintptr_t)codes | (uintptr_t)scale) & 15) return fail(PKV_EINVAL, "codes and scale must be 16-byte aligned");
@@ -1297,6 +1304,8 @@ int pkv_block_select(const pkv_plan* plan, const void* q, const int8_t* codes, c
   p.num_blocks = plan->num_blocks;
   p.num_sink = num_sink;
   p.num_recent = num_recent;
+  p.last_page = (uint32_t)std::min<int64_t>(num_pages - 1, INT32_MAX);
+  p.max_page = max_page_ptr(plan);
   int32_t max_blocks = 0, sms = 0;
   for (const ReqInfo& r : plan->req)
     if (r.q_len) max_blocks = std::max(max_blocks, (int32_t)(((int64_t)r.kv_len + plan->ps - 1) / plan->ps));

@@ -113,21 +113,20 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, Form<WIDE>::CTAS) block_s
   pdl_wait();
   pdl_launch_dependents();
   const int4 rq = __ldg(reinterpret_cast<const int4*>(p.req + i));  // page_base, kv_len, q_begin, q_len
+  // (a captured call's plan may have been made anew over pages that the bounds do not have: they count as the last one.
+  // A flag from where the pages are read cost 0.3 us; one read beside the request's costs nothing)
+  if (blockIdx.x == 0 && tid == 0 && __ldg(p.max_page) > (int)p.last_page) record_error(p.err, PKV_DEVERR_PAGE_RANGE);
   if (rq.w == 0) return;  // (the whole cluster)
   const int N = (int)p.by_page.div((uint32_t)rq.y + (uint32_t)p.page_size - 1u);
   const int K = p.num_blocks, S = p.num_sink, R = p.num_recent;
   int32_t* out = p.blocks + ((int64_t)rq.z * p.num_kv_heads + h) * K;
   const int m = K - S - R;  // pages to find
-  if (N <= K || m == 0) {   // (the whole cluster) nothing competes
-    if (rank == 0)
-      for (int j = tid; j < K; j += THREADS) out[j] = N <= K ? (j < N ? j : -1) : (j < S ? j : N - K + j);
-    return;
-  }
   const int nb = N - S - R;  // competing pages S .. N - R - 1
-  if (nb > p.key_cap) {     // (the whole cluster) a captured call whose plan was made anew for longer requests
-    if (rank == 0) {
-      if (tid == 0) record_error(p.err, PKV_DEVERR_CAPACITY);
-      for (int j = tid; j < K; j += THREADS) out[j] = -1;
+  if (N <= K || m == 0 || nb > p.key_cap) {  // (the whole cluster) nothing competes; or a captured call's plan was made anew
+    if (rank == 0) {                         // for longer requests than it has room for
+      const bool fits = N <= K || m == 0;
+      if (!fits && tid == 0) record_error(p.err, PKV_DEVERR_CAPACITY);
+      for (int j = tid; j < K; j += THREADS) out[j] = !fits ? -1 : N <= K ? (j < N ? j : -1) : (j < S ? j : N - K + j);
     }
     return;
   }
@@ -153,7 +152,10 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, Form<WIDE>::CTAS) block_s
   uint4 x[UNROLL][2];
   auto fetch_pages = [&](int b) {
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u) page[u] = b + u * STEP < hi ? __ldg(pages + b + u * STEP) : 0;
+    for (int u = 0; u < UNROLL; ++u) {
+      page[u] = b + u * STEP < hi ? __ldg(pages + b + u * STEP) : 0;
+      page[u] = (int)min((uint32_t)page[u], p.last_page);
+    }
   };
   auto fetch_bounds = [&](int b) {
 #pragma unroll

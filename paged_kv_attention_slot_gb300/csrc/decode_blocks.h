@@ -31,6 +31,7 @@ cudaError_t launch_key_bounds(BoundsParams p, int dtype, int head_dim, int num_s
 
 struct SelectParams {
   const ReqInfo* req;
+  const int32_t* max_page;  // largest entry of kv_indices
   const int32_t* kv_indices;
   const void* q;
   const int8_t* codes;
@@ -38,6 +39,7 @@ struct SelectParams {
   int32_t* blocks;  // [total_tokens, num_kv_heads, num_blocks]
   int32_t num_kv_heads, group, head_dim, page_size;
   int32_t num_blocks, num_sink, num_recent;
+  uint32_t last_page;  // that codes has
   int32_t key_cap;  // competing pages that the launch has room for (set by the launcher, as the members behind it)
   Divider by_page;
   int32_t* err;

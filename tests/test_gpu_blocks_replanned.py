@@ -83,3 +83,36 @@ def test_a_captured_selection_refuses_longer_requests(heads, kv_heads, D, short,
         else:
             assert pk.device_error() == 0
         assert np.array_equal(_np(blocks), other)
+
+
+# ---- pages ----
+def _batch_kw(heads, kv_heads, D, ps, **kw):
+    return dict(num_qo_heads=heads, num_kv_heads=kv_heads, head_dim=D, page_size=ps, **kw)
+
+
+@pytest.mark.parametrize("lens, D", [([300, 45], 128), ([9000, 500], 64), ([9000, 500], 128)])
+def test_a_captured_selection_serves_other_pages_and_records_those_it_has_no_bounds_of(lens, D):
+    pk, ps, H, K = _pk(), 8, 2, 9
+    s = Selection(lens, 4, H, ps, D, K, seed=3)
+    q, blocks = s.q.cuda(), torch.empty((2, H, K), dtype=torch.int32, device="cuda")
+    graph = _capture(lambda: s.plan.select(q, s.b, num_sink=1, num_recent=1, blocks=blocks))
+    P, first = len(s.codes), s.idx
+    for seed in (4, 5):
+        idx = np.random.RandomState(seed).permutation(P)[:len(first[2])].astype(np.int32)
+        s.idx = (first[0], first[1], idx, first[3])
+        s.plan.plan(*s.idx, **_batch_kw(4, H, D, ps, mode="decode", num_blocks=K))
+        blocks.fill_(99)
+        graph.replay()
+        assert pk.device_error() == 0 and np.array_equal(_np(blocks), s.want(1, 1))
+    # pages of request 0 that the bounds do not have, competing ones and the last one, which is selected in any case
+    for page in (P, 2 ** 31 - 1):
+        for at in (1, len(first[2]) // 2, first[1][1] - 1):
+            bad = idx.copy()
+            bad[at] = page
+            s.plan.plan(first[0], first[1], bad, first[3], **_batch_kw(4, H, D, ps, mode="decode", num_blocks=K))
+            blocks.fill_(99)
+            graph.replay()
+            assert pk.device_error() == PAGE_RANGE
+            got = _np(blocks)
+            assert np.array_equal(got[1], s.want(1, 1)[1])
+            assert np.all((got[0] >= 0) & (got[0] < first[1][1])) and np.all(np.diff(got[0]) > 0)
