@@ -83,7 +83,7 @@ typedef enum {
 enum {
   PKV_DEVERR_NONE = 0,
   PKV_DEVERR_SLOT_RANGE = 1,   /* kv_store, kv_load: slot_mapping entry >= num_pages * page_size  */
-  PKV_DEVERR_PAGE_RANGE = 2,   /* attention, block_select: a page id outside
+  PKV_DEVERR_PAGE_RANGE = 2,   /* attention, key bounds, block_select: a page id outside
                                 * [0, num_pages)                                                  */
   PKV_DEVERR_TIMEOUT = 3,      /* a bounded wait inside a kernel ran out; the kernel returned     */
   PKV_DEVERR_CAPACITY = 4      /* block_select: a captured call's plan was made anew for a request

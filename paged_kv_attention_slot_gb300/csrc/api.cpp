@@ -1252,6 +1252,8 @@ int pkv_key_bounds_update(const pkv_plan* plan, const pkv_cache* cache, int8_t* 
   p.new_only = !all_pages;
   p.pages = p.last_only ? (int64_t)plan->batch : (int64_t)plan->indices.size();
   if (p.pages == 0) return PKV_OK;
+  p.last_page = (uint32_t)std::min<int64_t>(cache->num_pages - 1, INT32_MAX);
+  p.max_page = max_page_ptr(plan);
   p.req = (const ReqInfo*)((char*)plan->ws + plan->off_req);
   p.kv_indices = (const int32_t*)((char*)plan->ws + plan->off_idx);
   p.k_pool = rp.k_pool;

@@ -12,6 +12,7 @@ constexpr int32_t kSelectMaxGroup = 128;      // query heads per KV head: codes 
 
 struct BoundsParams {
   const ReqInfo* req;
+  const int32_t* max_page;  // largest entry of kv_indices
   const int32_t* kv_indices;
   const char* k_pool;
   const char* k_sf;  // null unless NVFP4
@@ -21,6 +22,8 @@ struct BoundsParams {
   const float* scale;  // [num_kv_heads, head_dim]
   float k_scale;       // of the pool (1 for bf16)
   int64_t pages;       // entries of the page list to look at (last_only: requests)
+  uint32_t last_page;  // of the pool
+  int32_t* err;        // set by the launcher
   int32_t batch, num_kv_heads, page_size;
   int32_t last_only;   // a page per request, its last one
   int32_t new_only;    // pages that hold a new token

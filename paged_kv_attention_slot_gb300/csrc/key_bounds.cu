@@ -24,6 +24,8 @@
 
 namespace pkv {
 
+int32_t* device_error_ptr();
+
 namespace {
 
 constexpr int kBoundWarps = 4;
@@ -123,7 +125,7 @@ __global__ void __launch_bounds__(kBoundWarps * 32, 8) key_bounds_kernel(const B
   } else {
     if (early) {
       page = __ldg(p.kv_indices + u);
-      open_page(page);
+      open_page((int)min((uint32_t)page, p.last_page));
       read(start, ps);
     }
     // the last request whose pages start at or before the entry, 32 probes at a time (requests without pages
@@ -140,14 +142,19 @@ __global__ void __launch_bounds__(kBoundWarps * 32, 8) key_bounds_kernel(const B
     i = lo;
   }
   const int4 rq = __ldg(reinterpret_cast<const int4*>(p.req + i));  // page_base, kv_len, q_begin, q_len
+  if (unit == 0 && lane == 0 && warp == 0 && __ldg(p.max_page) > (int)p.last_page) record_error(p.err, PKV_DEVERR_PAGE_RANGE);
   const int L = rq.y;
   const int N = (int)p.by_page.div((uint32_t)L + (uint32_t)ps - 1u);
   const int block = p.last_only ? N - 1 : (int)(u - rq.x);
   if (p.last_only && (rq.w == 0 || N == 0)) return;
+  if (block >= N) return;  // (a captured call whose plan was made anew for fewer pages: an entry behind the last request)
   const int valid = min(ps, L - block * ps);
   if (!early) {
     if (p.new_only && (rq.w == 0 || block * ps + valid <= L - rq.w)) return;  // no new token in it
     page = __ldg(p.kv_indices + rq.x + block);
+  }
+  if ((uint32_t)page > p.last_page) return;  // (and over pages that the pool does not have: recorded above)
+  if (!early) {
     open_page(page);
     read(start, valid);
   }
@@ -247,6 +254,8 @@ cudaError_t launch_key_bounds(BoundsParams p, int dtype, int head_dim, int num_s
   // warp each 3.0), 1024 3.4 -> 3.6, 2048 4.7 -> 6.2.
   p.shared_page = p.page_size >= 32 && p.pages * p.num_kv_heads <= (int64_t)num_sms * p.page_size / 8;
   p.by_page = divider(p.page_size);
+  p.err = device_error_ptr();
+  if (!p.err) return cudaErrorInvalidDevice;
   if (dtype == PKV_NVFP4) return launch_form<PKV_NVFP4, 128>(p, s);
   if (dtype == PKV_FP8_E4M3) return launch_form<PKV_FP8_E4M3, 128>(p, s);
   return head_dim == 128 ? launch_form<PKV_BF16, 128>(p, s) : launch_form<PKV_BF16, 64>(p, s);

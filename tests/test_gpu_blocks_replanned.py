@@ -116,3 +116,62 @@ def test_a_captured_selection_serves_other_pages_and_records_those_it_has_no_bou
             got = _np(blocks)
             assert np.array_equal(got[1], s.want(1, 1)[1])
             assert np.all((got[0] >= 0) & (got[0] < first[1][1])) and np.all(np.diff(got[0]) > 0)
+
+
+@pytest.mark.parametrize("dtype, mode, every, ps", [
+    *((d, "decode", e, ps) for d in ("bf16", "e4m3", "nvfp4") for e, ps in ((False, 16), (True, 16), (True, 64))),
+    ("bf16", "prefill", False, 16), ("bf16", "prefill", True, 64)])
+def test_captured_bounds_serve_other_pages_and_record_those_outside_the_pool(dtype, mode, every, ps):
+    pk, H, P = _pk(), 2, 40
+    g = torch.Generator(device="cuda").manual_seed(1)
+    if dtype == "bf16":
+        k = torch.randn((P, ps, H, 128), generator=g, device="cuda").to(torch.bfloat16)
+        cache = pk.KVCache(k, k.clone())
+    elif dtype == "e4m3":
+        k = torch.randn((P, ps, H, 128), generator=g, device="cuda").to(torch.float8_e4m3fn).view(torch.uint8)
+        cache = pk.KVCache(k, k.clone(), 0.7, 0.7)
+    else:
+        cache = pk.KVCache.nvfp4(P, ps, H, 128, 0.01, 0.01)
+        cache.k.random_(0, 256, generator=g)
+        cache.k_sf.random_(0x30, 0x50, generator=g)
+    lens, q_lens = ([5 * ps - 3, 9 * ps, 17], [1, 1, 0]) if mode == "decode" else ([5 * ps - 3, 9 * ps, 17], [ps + 2, 3, 17])
+    idx, _ = _batch(lens, q_lens, ps)
+    kw = _batch_kw(2, H, 128, ps, mode=mode, kv_dtype=dtype, max_splits=1)
+    room = torch.full((P + 2, H, 2, 128), 99, dtype=torch.int8, device="cuda")  # (a page before and one behind the bounds)
+    b = pk.KeyBounds(room[1:P + 1], torch.full((H, 128), 0.03, device="cuda"))
+    plan, other = pk.Plan().plan(*idx, **kw), pk.Plan()
+    graph = _capture(lambda: plan.bound_keys(cache, b, all_pages=every))
+
+    def replayed():
+        room.fill_(99)
+        graph.replay()
+        return pk.device_error(), room.clone()
+
+    def eager(*batch):
+        want = torch.full_like(room, 99)
+        other.plan(*batch, **kw).bound_keys(cache, pk.KeyBounds(want[1:P + 1], b.scale), all_pages=every)
+        assert pk.device_error() == 0
+        return want
+
+    for seed in (2, 3):
+        pages = np.random.RandomState(seed).permutation(P)[:len(idx[2])].astype(np.int32)
+        plan.plan(idx[0], idx[1], pages, idx[3], **kw)
+        code, got = replayed()
+        assert code == 0 and torch.equal(got, eager(idx[0], idx[1], pages, idx[3]))
+    want = eager(idx[0], idx[1], pages, idx[3])
+    for page in (P, 2 ** 31 - 1):
+        at = int(idx[1][1]) - 1  # request 0's last page
+        bad = pages.copy()
+        bad[at] = page
+        plan.plan(idx[0], idx[1], bad, idx[3], **kw)
+        code, got = replayed()
+        assert code == PAGE_RANGE
+        rest = want.clone()
+        rest[1 + pages[at]] = 99
+        assert torch.equal(got, rest)
+    # a shorter request 1: the entries of the captured call behind the list's end are nobody's pages
+    lens[1] = 6 * ps
+    short, _ = _batch(lens, q_lens, ps)
+    plan.plan(*short, **kw)
+    code, got = replayed()
+    assert code == 0 and torch.equal(got, eager(*short))
