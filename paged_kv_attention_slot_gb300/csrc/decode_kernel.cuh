@@ -300,7 +300,8 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB, HPB>::CTAS) decode_k
   pdl_wait();  // the plan's metadata copy and the KV write before this run must be complete
   const WorkItem w = p.work[blockIdx.x];
   // BLOCKS: the pool's pages of the unit, looked up once by the whole CTA (two dependent reads for all of
-  // them, instead of two before every tile), where they fit a table; -1: not a page of the request
+  // them, instead of two before every tile), where they fit a table; -1: not a page of the request, or behind the
+  // row's selection (a captured run whose plan was made anew for more blocks)
   __shared__ int32_t s_pages[BLOCKS ? kPageTable : 1];
   const int32_t* blocks = nullptr;
   unsigned num_pages = 0;  // of the request
@@ -318,7 +319,7 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB, HPB>::CTAS) decode_k
       for (int e = threadIdx.x; e < listed; e += READ * 128) {
         unsigned b[READ];
 #pragma unroll
-        for (int r = 0; r < READ; ++r) b[r] = e + r * 128 < listed ? (unsigned)__ldg(blocks + e + r * 128) : 0xffffffffu;
+        for (int r = 0; r < READ; ++r) b[r] = e + r * 128 < min(listed, p.num_blocks) ? (unsigned)__ldg(blocks + e + r * 128) : 0xffffffffu;
         int32_t page[READ];
 #pragma unroll
         for (int r = 0; r < READ; ++r) page[r] = b[r] < num_pages ? __ldg(p.kv_indices + w.page_base + b[r]) : -1;
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__(128, DecodeCfg<D, KV, NB, HPB>::CTAS) decode_k
     int at = page_of(key);
     if constexpr (BLOCKS) {
       if (tabled) return s_pages[at];
-      at = __ldg(blocks + at);
+      at = at < p.num_blocks ? __ldg(blocks + at) : -1;
       if ((unsigned)at >= num_pages) return -1;  // (recorded where its rows are read)
     }
     return __ldg(p.kv_indices + w.page_base + at);

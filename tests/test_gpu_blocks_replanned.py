@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_blocks import Selection, _batch, _np
+from tests.test_gpu_blocks import Chosen, Selection, _batch, _np
 
 pytestmark = pytest.mark.gpu
 
@@ -175,3 +175,29 @@ def test_captured_bounds_serve_other_pages_and_record_those_outside_the_pool(dty
     plan.plan(*short, **kw)
     code, got = replayed()
     assert code == 0 and torch.equal(got, eager(*short))
+
+
+# ---- attention ----
+@pytest.mark.parametrize("dtype, keys, ps, K, more", [("bf16", 200, 16, 4, 8), ("nvfp4", 200, 16, 4, 8), ("e4m3", 12000, 8, 1100, 1300),
+                                                      ("bf16", 12000, 8, 1000, 1300)])
+def test_a_captured_run_records_a_plan_made_anew_for_more_blocks(dtype, keys, ps, K, more):
+    pk = _pk()
+    c = Chosen([keys], 4, 2, ps, dtype, layout="hnd", seed=2)
+    p, chosen = c.plan(num_blocks=K, max_splits=1), c.choose(K)
+    # blocks that the rows behind the selection would give, were they read
+    room = torch.zeros((1, 4, K), dtype=torch.int32, device="cuda")
+    blocks, out = room[:, :2], torch.empty_like(c.q)
+    blocks.copy_(chosen)
+    want = p.run(c.q, c.cache, blocks=blocks)
+    graph = _capture(lambda: p.run(c.q, c.cache, blocks=blocks, out=out))
+    graph.replay()
+    assert pk.device_error() == 0 and torch.equal(out, want)
+    b = c.b
+    kw = _batch_kw(4, 2, 128, ps, mode="decode", kv_dtype=dtype, max_splits=1)
+    p.plan(b.qo_indptr, b.kv_indptr, b.kv_indices, b.last_page_len, num_blocks=more, **kw)
+    graph.replay()
+    assert pk.device_error() == PAGE_RANGE
+    p.plan(b.qo_indptr, b.kv_indptr, b.kv_indices, b.last_page_len, num_blocks=K, **kw)
+    out.zero_()
+    graph.replay()
+    assert pk.device_error() == 0 and torch.equal(out, want)
