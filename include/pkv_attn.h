@@ -371,6 +371,8 @@ int pkv_kv_evict(const pkv_plan* plan, const pkv_cache* cache, float* scores, in
  *   offsets   device int64 [batch_size] or NULL (0): what a request's positions are ahead of its keys, e.g. the keys
  *             that pkv_kv_evict dropped.
  *   positions, slot_mapping  device int64 [total_tokens] (out).
+ * A captured call whose plan was made anew for fewer tokens gives the rows behind them slot -1 (nothing is written
+ * there) and position 0.
  */
 int pkv_token_map(const pkv_plan* plan, const int64_t* offsets, int64_t* positions, int64_t* slot_mapping, void* stream);
 

@@ -299,6 +299,11 @@ __global__ void __launch_bounds__(256) token_map_kernel(const ReqInfo* req, cons
     else hi = mid;
   }
   const int4 r = __ldg(reinterpret_cast<const int4*>(req + lo));  // page_base, kv_len, q_begin, q_len
+  if (row - r.z >= r.w) {  // (a captured call whose plan was made anew for fewer tokens: a row behind the last one)
+    slots[row] = -1;
+    positions[row] = 0;
+    return;
+  }
   const int32_t key = r.y - r.w + (int32_t)(row - r.z);
   const int32_t page = (int32_t)by_page.div((uint32_t)key);
   slots[row] = (int64_t)__ldg(kv_indices + r.x + page) * ps + (key - page * ps);

@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import blocks as OB
 from tests.test_gpu_blocks import Chosen, Selection, _batch, _np
 
 pytestmark = pytest.mark.gpu
@@ -38,6 +39,13 @@ def _capture(fn):
     return graph
 
 
+def _front(plan):
+    """What stands in front of the request table and the page list in a plan's workspace: where it differs, a captured call
+    would read something else in their place, and is not replayed."""
+    i = plan.info()
+    return i["num_work"], i["num_merge"], i["batch_size"]
+
+
 # ---- selection ----
 @pytest.mark.parametrize("heads, kv_heads, D, short, long", [
     (8, 8, 128, 60, 63),       # within the same 32 pages of scores: served
@@ -58,7 +66,7 @@ def test_a_captured_selection_refuses_longer_requests(heads, kv_heads, D, short,
     b, q = pk.KeyBounds(codes, s.b.scale.clone()), s.q.cuda()
     blocks = torch.empty((2, kv_heads, K), dtype=torch.int32, device="cuda")
     kw = dict(num_qo_heads=heads, num_kv_heads=kv_heads, head_dim=D, page_size=ps, mode="decode", num_blocks=K)
-    at = s.plan.workspace.data_ptr()
+    at, front = s.plan.workspace.data_ptr(), _front(s.plan)
     graph = _capture(lambda: s.plan.select(q, b, num_sink=1, num_recent=2, blocks=blocks))
     want = s.want(1, 2)
     for _ in range(2):
@@ -70,7 +78,7 @@ def test_a_captured_selection_refuses_longer_requests(heads, kv_heads, D, short,
         graph.replay()
         assert pk.device_error() == 0 and np.array_equal(_np(blocks), want)
         s.plan.plan(*t.idx, **kw)
-        assert s.plan.workspace.data_ptr() == at
+        assert s.plan.workspace.data_ptr() == at and _front(s.plan) == front
         codes.copy_(t.b.codes)
         b.scale.copy_(t.b.scale)
         q.copy_(t.q)
@@ -172,7 +180,9 @@ def test_captured_bounds_serve_other_pages_and_record_those_outside_the_pool(dty
     # a shorter request 1: the entries of the captured call behind the list's end are nobody's pages
     lens[1] = 6 * ps
     short, _ = _batch(lens, q_lens, ps)
+    front = _front(plan)
     plan.plan(*short, **kw)
+    assert _front(plan) == front
     code, got = replayed()
     assert code == 0 and torch.equal(got, eager(*short))
 
@@ -194,10 +204,40 @@ def test_a_captured_run_records_a_plan_made_anew_for_more_blocks(dtype, keys, ps
     assert pk.device_error() == 0 and torch.equal(out, want)
     b = c.b
     kw = _batch_kw(4, 2, 128, ps, mode="decode", kv_dtype=dtype, max_splits=1)
+    front = _front(p)
     p.plan(b.qo_indptr, b.kv_indptr, b.kv_indices, b.last_page_len, num_blocks=more, **kw)
+    assert _front(p) == front
     graph.replay()
     assert pk.device_error() == PAGE_RANGE
     p.plan(b.qo_indptr, b.kv_indptr, b.kv_indices, b.last_page_len, num_blocks=K, **kw)
     out.zero_()
     graph.replay()
     assert pk.device_error() == 0 and torch.equal(out, want)
+
+
+# ---- token map ----
+@pytest.mark.parametrize("mode, lens, first, then", [
+    ("decode", [40, 9, 700, 33], [1, 1, 1, 1], [1, 1, 0, 0]), ("decode", [40, 9, 700, 33], [1, 1, 1, 1], [0, 1, 0, 0]),
+    ("prefill", [300, 41], [100, 41], [90, 3])])
+def test_rows_of_a_captured_token_map_behind_the_last_token_are_padding(mode, lens, first, then):
+    pk = _pk()
+    kw = _batch_kw(4, 1, 128, 16, mode=mode, max_splits=1, num_sms=152)
+    # (the lists in front of the request table take as many 256-byte lines: it stays where the captured call reads it)
+    size = [pk.Plan.workspace_size(*_batch(lens, n, 16)[0], **kw) for n in (first, then)]
+    assert size[0] == size[1]
+    p = pk.Plan().plan(*_batch(lens, first, 16)[0], **kw)
+    off = torch.arange(len(lens), device="cuda") * 1000
+    at = p.workspace.data_ptr()
+    kept = []
+    graph = _capture(lambda: kept.extend(p.token_map(off)))
+    for q_lens in (first, then, first):
+        idx, _ = _batch(lens, q_lens, 16)
+        p.plan(*idx, **kw)
+        assert p.workspace.data_ptr() == at
+        for x in kept:
+            x.fill_(77)
+        graph.replay()
+        n = sum(q_lens)
+        pos, slots = OB.token_map(*idx, 16, _np(off))
+        assert np.array_equal(_np(kept[0]), np.concatenate([pos, np.zeros(sum(first) - n, np.int64)]))
+        assert np.array_equal(_np(kept[1]), np.concatenate([slots, np.full(sum(first) - n, -1)]))
