@@ -3,7 +3,8 @@
 Every translation unit under csrc/ is compiled in parallel into _build/, then linked into
 libpkv_attn.so next to this file.  Rebuilds only what changed (source or header newer than the
 object).  No cmake, no torch extension machinery: the library is a plain C-ABI shared object, and
-csrc/python/binding.cpp one host file that is compiled against the headers of Python and torch.
+csrc/python/binding.cpp one host file that is compiled against the headers of Python and torch
+(where there is no torch, the library is built alone, for users of its C ABI).
 """
 
 from __future__ import annotations
@@ -50,9 +51,13 @@ def _stale(src, obj, hdr_mtime):
 
 
 def _binding_job(nvcc, force):
-    """The command that makes _binding.so; None: it is up to date."""
+    """The command that makes _binding.so; None: it is up to date, or there is no torch, without which nothing could
+    import it (the library needs none)."""
     src = os.path.join(CSRC, "python", "binding.cpp")
-    torch = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    torch = list(spec.submodule_search_locations)[0]
     newest = max(os.path.getmtime(f) for f in (os.path.join(INCLUDE, "pkv_attn.h"), os.path.join(torch, "version.py")))
     if not (force or _stale(src, BINDING, newest)):
         return None
