@@ -213,6 +213,23 @@ def _new(shape, dtype, device, stream) -> torch.Tensor:
     return t
 
 
+def _record(stream, streams: set, *buffers) -> int:
+    """Handle of the stream, on which an object's own buffers are about to be used: their memory is not given away
+    before that work is done.  streams: the handles that they are recorded on.  (Not for a captured call: a
+    graph's replays are the caller's to keep the object for.  Nor on a stream that is not torch's, which may be gone when
+    the memory is given back.)"""
+    handle = _stream_ptr(stream)
+    if handle not in streams and not torch.cuda.is_current_stream_capturing():
+        streams.add(handle)
+        s = torch.cuda.current_stream() if stream is None else stream
+        # (the id of a stream from elsewhere is its handle)
+        if isinstance(s, torch.cuda.Stream) and (s.stream_id != handle or handle == 0):
+            for t in buffers:
+                if t is not None:
+                    t.record_stream(s)
+    return handle
+
+
 def _check_scores(scores: torch.Tensor, cache: KVCache) -> int:
     """Address of an accumulated-weight tensor of the cache's slots."""
     if scores.dtype != torch.float32 or not scores.is_contiguous():
@@ -316,7 +333,10 @@ class Rotary:
         # whole turns are dropped: positions are integers
         steps = [round(math.fmod(x / (2 * math.pi), 1.0) * 2.0 ** 64) % 2 ** 64 for x in f.tolist()]
         self.phase_step = torch.from_numpy(np.array(steps, dtype=np.uint64).view(np.int64)).to(device)
-        self._phase_step, self._device_index = self.phase_step.data_ptr(), self.phase_step.get_device()
+        self._streams = set()  # handles of the streams it is recorded on
+
+    def _use(self, stream) -> int:
+        return _record(stream, self._streams, self.phase_step)
 
     @staticmethod
     def _frequencies(R, base, scaling, factor, original_positions, low_turns, high_turns):
@@ -359,8 +379,8 @@ def rope_store(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: tor
         q_out = _new(q.shape, torch.bfloat16, cache._device, stream) if q_out is None else q_out
         k_out = _new(k.shape, torch.bfloat16, cache._device, stream) if k_out is None and return_k else k_out
     return binding().rope_store(
-        C.addressof(cache.struct), cache._device_index, stream, q, k, v, positions, slot_mapping, rotary._phase_step,
-        rotary._device_index, rotary.head_dim, rotary.rotary_dim, rotary.interleaved, rotary.amplitude,
+        C.addressof(cache.struct), cache._device_index, rotary, rotary._streams, stream, q, k, v, positions, slot_mapping,
+        rotary.phase_step, rotary.head_dim, rotary.rotary_dim, rotary.interleaved, rotary.amplitude,
         0 if scores is None else _check_scores(scores, cache), q_out, k_out, return_k)
 
 
@@ -439,19 +459,8 @@ class Plan:
         return _new((num_bytes,), torch.uint8, device, stream)
 
     def _use(self, stream) -> int:
-        """Handle of the stream, on which the plan's own buffers are about to be used: their memory is not given
-        away before that work is done.  (Not for a captured run: a graph's replays are the caller's to keep the
-        plan for.  Nor on a stream that is not torch's, which may be gone when the memory is given back.)"""
-        handle = _stream_ptr(stream)
-        if handle not in self._streams and not torch.cuda.is_current_stream_capturing():
-            self._streams.add(handle)
-            s = torch.cuda.current_stream() if stream is None else stream
-            # (the id of a stream from elsewhere is its handle)
-            if isinstance(s, torch.cuda.Stream) and (s.stream_id != handle or handle == 0):
-                for t in (self.workspace if self._own_workspace else None, self.scratch):
-                    if t is not None:
-                        t.record_stream(s)
-        return handle
+        """Handle of the stream, on which the plan's own buffers are about to be used."""
+        return _record(stream, self._streams, self.workspace if self._own_workspace else None, self.scratch)
 
     @staticmethod
     def _args(qo_indptr, kv_indptr, kv_indices, last_page_len, num_qo_heads, num_kv_heads, head_dim, page_size,

@@ -8,8 +8,8 @@
 // addresses attach() receives.
 //
 // Conventions: a tensor argument that may be absent is None; `stream` is what the caller was given, None for torch's current
-// stream, to which outputs made here belong (for another stream the caller passes outputs); `owner` is the Plan whose buffers
-// the call uses and `streams` its set of the handles that they are recorded on.  A wrong argument raises ValueError (one of
+// stream, to which outputs made here belong (for another stream the caller passes outputs); `owner` is the Plan or Rotary whose
+// buffers the call uses and `streams` its set of the handles that they are recorded on.  A wrong argument raises ValueError (one of
 // a wrong kind TypeError), an error status of the library what `check` raises.  Memory is asked for and kernels are launched
 // without the interpreter's lock: the allocator's own lock may be held by a thread that waits for it.
 
@@ -142,10 +142,10 @@ bool handle_of(PyObject* stream, int64_t device, void*& handle) {
   return handle || !PyErr_Occurred();
 }
 
-// The same for a call that uses a plan's own buffers, which are recorded on the stream the first time it is seen.
-struct PlanStream {
+// The same for a call that uses an owner's buffers, which are recorded on the stream the first time it is seen.
+struct OwnedStream {
   PyObject *owner, *streams, *stream;
-  explicit PlanStream(Args& a) : owner(a.object()), streams(a.object()), stream(a.object()) {}
+  explicit OwnedStream(Args& a) : owner(a.object()), streams(a.object()), stream(a.object()) {}
   bool use(int64_t device, void*& handle) const {
     if (!handle_of(stream, device, handle)) return false;
     PyObject* h = PyLong_FromVoidPtr(handle);
@@ -224,7 +224,7 @@ PyObject* token_map(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   Args a(args, n, 10);
   auto* plan = a.pointer<const pkv_plan>();
-  const PlanStream on(a);
+  const OwnedStream on(a);
   const int64_t tokens = a.integer(), batch = a.integer();
   const at::Tensor* workspace = a.tensor();
   const at::Tensor* offsets = a.tensor(true);
@@ -249,18 +249,18 @@ PyObject* token_map(PyObject*, PyObject* const* args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// rope_store(cache, device, stream, q, k, v, positions, slots, phase_step, rotary_device, rotary_head_dim, rotary_dim,
+// rope_store(cache, device, owner, streams, stream, q, k, v, positions, slots, phase_step, rotary_head_dim, rotary_dim,
 //            interleaved, amplitude, scores, q_out, k_out, return_k) -> q or (q, k)
 PyObject* rope_store(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  Args a(args, n, 18);
+  Args a(args, n, 19);
   auto* cache = a.pointer<const pkv_cache>();
   const int64_t device = a.integer();
-  PyObject* given = a.object();
+  const OwnedStream on(a);
   const at::Tensor *q = a.tensor(), *k = a.tensor(), *v = a.tensor(), *positions = a.tensor(), *slots = a.tensor();
+  const at::Tensor* step = a.tensor();
   pkv_rope_args r{};
-  r.phase_step = a.pointer<const uint64_t>();
-  const int64_t rotary_device = a.integer(), rotary_head_dim = a.integer();
+  const int64_t rotary_head_dim = a.integer();
   r.rotary_dim = a.int32();
   r.interleaved = a.int32();
   r.amplitude = (float)a.real();
@@ -281,7 +281,9 @@ PyObject* rope_store(PyObject*, PyObject* const* args, Py_ssize_t n) {
   for (const at::Tensor* t : {positions, slots})
     REQUIRE(is(*t, at::kLong, device) && t->dim() == 1 && t->size(0) == T,
             "positions and slot_mapping must be contiguous int64 tensors [T] on the cache's device");
-  REQUIRE(rotary_device == device, "the rotary must be on the cache's device");
+  REQUIRE(step->get_device() == device, "the rotary must be on the cache's device");
+  REQUIRE(is(*step, at::kLong, device) && step->dim() == 1 && step->size(0) == r.rotary_dim / 2,
+          "the rotary's phase_step must be a contiguous int64 tensor [rotary_dim / 2]");
   REQUIRE((!q_out || (is(*q_out, at::kBFloat16, device) && shape3(*q_out, T, Hq, D))) &&
               (!k_out || (is(*k_out, at::kBFloat16, device) && shape3(*k_out, T, H, D))),
           "q_out and k_out must be contiguous bf16 tensors like q and k");
@@ -295,9 +297,10 @@ PyObject* rope_store(PyObject*, PyObject* const* args, Py_ssize_t n) {
   r.q_stride_token = q->stride(0), r.q_stride_head = q->stride(1);
   r.k_stride_token = k->stride(0), r.k_stride_head = k->stride(1);
   r.v_stride_token = v->stride(0), r.v_stride_head = v->stride(1);
+  r.phase_step = static_cast<const uint64_t*>(step->data_ptr());
   r.num_qo_heads = (int32_t)Hq;
   void* stream;
-  if (!handle_of(given, device, stream)) return nullptr;
+  if (!on.use(device, stream)) return nullptr;
   at::Tensor qo, ko;
   if (!call([&] {
         qo = q_out ? *q_out : make({T, Hq, D}, at::kBFloat16, device);
@@ -309,8 +312,8 @@ PyObject* rope_store(PyObject*, PyObject* const* args, Py_ssize_t n) {
         return api.rope_kv_store(&r, cache, stream);
       }))
     return nullptr;
-  PyObject* first = result(args[15], qo);
-  return return_k ? pair(first, result(args[16], ko)) : first;
+  PyObject* first = result(args[16], qo);
+  return return_k ? pair(first, result(args[17], ko)) : first;
   END_HANDLE_TH_ERRORS
 }
 
@@ -319,7 +322,7 @@ PyObject* bound_keys(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   Args a(args, n, 9);
   auto* plan = a.pointer<const pkv_plan>();
-  const PlanStream on(a);
+  const OwnedStream on(a);
   auto* cache = a.pointer<const pkv_cache>();
   const int64_t device = a.integer();
   const at::Tensor *codes = a.tensor(), *scale = a.tensor();
@@ -346,7 +349,7 @@ PyObject* block_select(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   Args a(args, n, 13);
   auto* plan = a.pointer<const pkv_plan>();
-  const PlanStream on(a);
+  const OwnedStream on(a);
   const Shape3 shape = a.shape3();
   const auto [T, H, K] = shape;
   const int64_t Hq = a.integer(), D = a.integer();
@@ -381,7 +384,7 @@ PyObject* run_blocks(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   Args a(args, n, 14);
   auto* plan = a.pointer<const pkv_plan>();
-  const PlanStream on(a);
+  const OwnedStream on(a);
   auto* cache = a.pointer<const pkv_cache>();
   const int64_t device = a.integer();
   const Shape3 shape = a.shape3();
