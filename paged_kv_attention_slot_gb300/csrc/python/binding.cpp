@@ -129,6 +129,16 @@ at::Tensor make(at::IntArrayRef shape, at::ScalarType type, int64_t device) {
   return at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, (c10::DeviceIndex)device));
 }
 
+// The tensors of a KeyBounds, whose attributes a program may have exchanged since it was made
+bool are_bounds(const at::Tensor& codes, const at::Tensor& scale) {
+  if (codes.scalar_type() == at::kChar && codes.dim() == 4 && codes.size(2) == 2 && codes.is_contiguous() &&
+      is(scale, at::kFloat, codes.get_device()) && scale.dim() == 2 && scale.size(0) == codes.size(1) && scale.size(1) == codes.size(3))
+    return true;
+  PyErr_SetString(PyExc_ValueError, "bounds.codes must be a contiguous int8 tensor [num_pages, num_kv_heads, 2, head_dim], bounds.scale a "
+                                    "contiguous float32 tensor [num_kv_heads, head_dim] on its device");
+  return false;
+}
+
 // The handle of the stream to launch on; false: a Python error is set.
 bool handle_of(PyObject* stream, int64_t device, void*& handle) {
   if (stream == Py_None) {
@@ -328,6 +338,7 @@ PyObject* bound_keys(PyObject*, PyObject* const* args, Py_ssize_t n) {
   const at::Tensor *codes = a.tensor(), *scale = a.tensor();
   const int32_t all_pages = a.integer() != 0;
   if (!a.ok()) return nullptr;
+  if (!are_bounds(*codes, *scale)) return nullptr;
   REQUIRE(codes->size(0) == cache->num_pages && codes->size(1) == cache->num_kv_heads && codes->size(3) == cache->head_dim,
           "the bounds do not match the cache's geometry");
   REQUIRE(codes->get_device() == device, "the bounds must be on the cache's device");
@@ -360,6 +371,7 @@ PyObject* block_select(PyObject*, PyObject* const* args, Py_ssize_t n) {
   const int64_t device = codes->get_device();
   REQUIRE(is(*q, at::kBFloat16, device) && shape3(*q, T, Hq, D),
           "q must be a contiguous bf16 tensor [%lld, %lld, %lld] on the bounds' device", (long long)T, (long long)Hq, (long long)D);
+  if (!are_bounds(*codes, *scale)) return nullptr;
   REQUIRE(codes->size(1) == H && codes->size(3) == D, "the bounds do not match the plan's KV heads and head_dim");
   REQUIRE(on_current_device(device), "the bounds must be on the current CUDA device");
   REQUIRE(!blocks || (is(*blocks, at::kInt, device) && shape3(*blocks, T, H, K)),

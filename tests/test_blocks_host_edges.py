@@ -28,3 +28,20 @@ def test_rope_store_refuses_another_phase_step(pk, other):
     rot.phase_step = other
     with pytest.raises(ValueError, match="phase_step"):
         pk.rope_store(q, k, k, i, i, _cache(pk), rot)
+
+
+@pytest.mark.parametrize("name, other", [
+    ("codes", torch.zeros((11, 2, 2, 128), dtype=torch.int16)), ("codes", torch.zeros((11, 2, 2, 128), dtype=torch.uint8)),
+    ("codes", torch.zeros((1, 2, 2, 128), dtype=torch.int8).expand(11, 2, 2, 128)), ("codes", torch.zeros((11, 2, 1, 128), dtype=torch.int8)),
+    ("codes", torch.zeros((11, 2, 2, 256), dtype=torch.int8)[..., ::2]), ("codes", torch.zeros((11, 2, 256), dtype=torch.int8)),
+    ("scale", torch.ones((2, 128), dtype=torch.bfloat16)), ("scale", torch.ones(())), ("scale", torch.ones(128)),
+    ("scale", torch.ones((1, 128)).expand(2, 128)), ("scale", torch.ones((2, 64)))])
+def test_bounds_whose_tensors_were_exchanged_are_refused(pk, name, other):
+    b, cache = pk.KeyBounds.of(_cache(pk), 0.03), _cache(pk)
+    setattr(b, name, other)
+    plan = pk.Plan().plan([0, 1, 2], [0, 7, 11], list(range(11)), [4, 2], num_qo_heads=8, num_kv_heads=2, head_dim=128, page_size=16,
+                          mode="decode", num_sms=152, host_only=True, num_blocks=4)
+    with pytest.raises(ValueError, match="contiguous"):
+        plan.bound_keys(cache, b)
+    with pytest.raises(ValueError, match="contiguous"):
+        plan.select(torch.zeros((2, 8, 128), dtype=torch.bfloat16), b)
