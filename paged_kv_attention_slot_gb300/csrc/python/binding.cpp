@@ -80,6 +80,12 @@ class Args {
     }
     return ok_ ? (int32_t)v : 0;
   }
+  bool truth() {
+    PyObject* o = next();
+    const int v = o ? PyObject_IsTrue(o) : 0;
+    if (v < 0) ok_ = false;
+    return v > 0;
+  }
   double real() {
     PyObject* o = next();
     if (!o) return 0;
@@ -276,7 +282,7 @@ PyObject* rope_store(PyObject*, PyObject* const* args, Py_ssize_t n) {
   r.amplitude = (float)a.real();
   r.scores = a.pointer<float>();
   const at::Tensor *q_out = a.tensor(true), *k_out = a.tensor(true);
-  const bool return_k = a.integer() != 0 || k_out;
+  const bool return_k = a.truth() || k_out;
   if (!a.ok()) return nullptr;
   const int64_t H = cache->num_kv_heads, D = cache->head_dim;
   REQUIRE(q->dim() == 3, "q must be [T, num_qo_heads, head_dim]");
@@ -336,7 +342,7 @@ PyObject* bound_keys(PyObject*, PyObject* const* args, Py_ssize_t n) {
   auto* cache = a.pointer<const pkv_cache>();
   const int64_t device = a.integer();
   const at::Tensor *codes = a.tensor(), *scale = a.tensor();
-  const int32_t all_pages = a.integer() != 0;
+  const int32_t all_pages = a.truth();
   if (!a.ok()) return nullptr;
   if (!are_bounds(*codes, *scale)) return nullptr;
   REQUIRE(codes->size(0) == cache->num_pages && codes->size(1) == cache->num_kv_heads && codes->size(3) == cache->head_dim,
@@ -403,7 +409,7 @@ PyObject* run_blocks(PyObject*, PyObject* const* args, Py_ssize_t n) {
   const auto [T, H, K] = shape;
   const int64_t Hq = a.integer(), D = a.integer();
   const at::Tensor *q = a.tensor(), *blocks = a.tensor(), *out = a.tensor(true), *lse = a.tensor(true);
-  const bool return_lse = a.integer() != 0 || lse;
+  const bool return_lse = a.truth() || lse;
   if (!a.ok()) return nullptr;
   REQUIRE(is(*blocks, at::kInt, device) && shape3(*blocks, T, H, K),
           "blocks must be a contiguous int32 tensor [%lld, %lld, %lld] on the cache's device", (long long)T, (long long)H, (long long)K);

@@ -1,5 +1,6 @@
 """Refusals of the calls of a decode step over selected pages that need no GPU: objects whose tensors were exchanged."""
 
+import numpy as np
 import pytest
 import torch
 
@@ -45,3 +46,17 @@ def test_bounds_whose_tensors_were_exchanged_are_refused(pk, name, other):
         plan.bound_keys(cache, b)
     with pytest.raises(ValueError, match="contiguous"):
         plan.select(torch.zeros((2, 8, 128), dtype=torch.bfloat16), b)
+
+
+@pytest.mark.parametrize("yes", [np.True_, [1], "yes", torch.tensor(True)])
+def test_flags_are_truth_values(pk, yes):
+    # (as in the calls over every page; on host tensors everything but the device is accepted)
+    cache, rot = _cache(pk), pk.Rotary(128, device="cpu")
+    b, q = pk.KeyBounds.of(cache, 0.03), torch.zeros((2, 8, 128), dtype=torch.bfloat16)
+    k, i = torch.zeros((2, 2, 128), dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int64)
+    plan = pk.Plan().plan([0, 1, 2], [0, 7, 11], list(range(11)), [4, 2], num_qo_heads=8, num_kv_heads=2, head_dim=128, page_size=16,
+                          mode="decode", num_sms=152, host_only=True, num_blocks=4)
+    for f in (lambda: plan.bound_keys(cache, b, all_pages=yes), lambda: pk.rope_store(q, k, k, i, i, cache, rot, return_k=yes),
+              lambda: plan.run(q, cache, blocks=torch.zeros((2, 2, 4), dtype=torch.int32), return_lse=yes)):
+        with pytest.raises(ValueError, match="CUDA device"):
+            f()
