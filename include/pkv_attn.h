@@ -367,7 +367,9 @@ int pkv_kv_evict(const pkv_plan* plan, const pkv_cache* cache, float* scores, in
  * pkv_token_map: positions and slots of the planned new tokens, from the plan's own metadata on the device.  Token t of
  * request i sits at key P = L_i - n_i + t:  slot_mapping = page(P / page_size) * page_size + P % page_size,
  * positions = P + offsets[i].
- *   plan      PKV_MODE_DECODE, PKV_MODE_PREFILL or PKV_MODE_MIXED, causal.
+ *   plan      PKV_MODE_DECODE, PKV_MODE_PREFILL or PKV_MODE_MIXED, causal.  The map reads no pool: for the chunks of a
+ *             batch whose pool is FP8 or NVFP4 (which plans with more than one new token per request do not take) plan
+ *             them for PKV_BF16.
  *   offsets   device int64 [batch_size] or NULL (0): what a request's positions are ahead of its keys, e.g. the keys
  *             that pkv_kv_evict dropped.
  *   positions, slot_mapping  device int64 [total_tokens] (out).
@@ -391,7 +393,7 @@ int pkv_token_map(const pkv_plan* plan, const int64_t* offsets, int64_t* positio
  *   slot_mapping  as pkv_kv_store: negative = not written to the pool (q_out and k_out are), out of range = not written
  *                 and recorded as PKV_DEVERR_SLOT_RANGE; no slot twice.
  *   phase_step    device uint64 [rotary_dim / 2]: f_i / (2 pi) as a fraction of 2^64, so that phase = position *
- *                 step modulo 2^64 is exact; its top 32 bits are used (2^-32 of a turn).
+ *                 step modulo 2^64 is exact; its top 32 bits are used, as a float32: at most 2^-26 of a turn off.
  *   amplitude     factor of the turned elements (1 without a scaling that asks for another).
  *   scores        as pkv_kv_store_scored, or NULL.
  * rotary_dim: a multiple of 16 up to head_dim.  num_tokens == 0 is a no-op.
@@ -422,7 +424,9 @@ int pkv_rope_kv_store(const pkv_rope_args* args, const pkv_cache* cache, void* s
  * pkv_key_bounds_update: bounds of the keys of the planned requests' pages, per KV head h and channel d, over the page's
  * valid keys j:  lo = floor(min_j k_jd / scale[h, d]),  hi = ceil(max_j k_jd / scale[h, d]), both clamped to [-127, 127]
  * (quotients in float32; a NaN key element gives -127 and 127).  Keys are the values that attention reads (codes times scales).
- *   plan       PKV_MODE_DECODE, PKV_MODE_PREFILL or PKV_MODE_MIXED; page_size >= 8.
+ *   plan       PKV_MODE_DECODE, PKV_MODE_PREFILL or PKV_MODE_MIXED; page_size >= 8.  Plans with more than one new token
+ *              per request are for bf16 pools of head_dim 128: after a chunk for another pool use a PKV_MODE_DECODE plan
+ *              and all_pages.
  *   codes      device int8 [num_pages, num_kv_heads, 2, head_dim] (lower, upper), contiguous, 16-byte aligned (out).
  *   scale      device float32 [num_kv_heads, head_dim], > 0, 16-byte aligned: about max |k| / 127 of the channel.  What
  *              lies beyond 127 steps is bounded by 127 only.
@@ -448,8 +452,10 @@ int pkv_plan_blocks_workspace_size(const pkv_plan_args* args, int32_t num_blocks
  *   score_b = sum_d w+_d hi_bd + w-_d lo_bd    (equal scores: the lower page),
  *   w+_d, w-_d = sums over the G query heads g of h of max(c_gd, 0), min(c_gd, 0),
  *   c_gd = rint(a_gd / max |a| * floor(32767 / G)),  a_gd = q_gd * scale[h, d]  (float32; a non-finite a_gd counts as 0),
- * which, up to the rounding of c, bounds sum_g q_g.k over the page's keys from above.  c and everything behind it are whole
- * numbers: the result does not depend on an order of additions.
+ * which bounds sum_g q_g.k over the page's keys from above, up to the rounding of c (32767 / G levels for the largest value:
+ * 255 with 128 query heads) and for keys within 127 steps of scale (a bound is clamped there, so a key beyond
+ * counts for less than it is).  c and everything behind it are whole numbers: the result does not depend on an order
+ * of additions.
  *   q        device bf16 [total_tokens, num_qo_heads, head_dim], contiguous.
  *   codes, scale  as pkv_key_bounds_update; num_pages: pages that codes has.
  *   num_sink >= 0, num_recent >= 1, num_sink + num_recent <= num_blocks.

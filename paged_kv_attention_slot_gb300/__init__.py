@@ -308,6 +308,7 @@ class Rotary:
                     least high_turns times not at all, those between in proportion to their turns;
       "ramp"        the same, in proportion to the pair's index (the borders rounded outwards to whole
                     indices), and turned elements times amplitude, 0.1 ln(factor) + 1 unless given.
+    low_turns and high_turns are the model's: 1 and 4 is usual for "wavelength" (and the default here), 1 and 32 for "ramp".
     inv_freq: the f_i themselves, rotary_dim / 2 of them, instead of base and scaling.  rotary_dim is a multiple of 16."""
 
     def __init__(self, head_dim: int, rotary_dim: int | None = None, base: float = 10000.0, interleaved: bool = False,
@@ -388,8 +389,8 @@ class KeyBounds:
     """8-bit bounds of the keys of one layer's pages, per KV head and channel, in steps of scale.
 
     codes: int8 [num_pages, num_kv_heads, 2, head_dim] (lower, upper), contiguous; scale: float32 [num_kv_heads, head_dim],
-    positive, about max |k| / 127 of each channel (keys beyond 127 steps are bounded by 127 only).  Plan.bound_keys
-    writes the codes, Plan.select reads them."""
+    positive, about max |k| / 127 of each channel, e.g. over a prompt's keys with some room (a key beyond 127 steps is
+    bounded by 127 only, so that its page may be passed over).  Plan.bound_keys writes the codes, Plan.select reads them."""
 
     def __init__(self, codes: torch.Tensor, scale: torch.Tensor):
         if codes.dtype != torch.int8 or codes.dim() != 4 or codes.shape[2] != 2 or not codes.is_contiguous():
@@ -685,8 +686,9 @@ class Plan:
     def token_map(self, offsets: torch.Tensor | None = None, stream=None):
         """Positions and slots of the planned new tokens: (positions, slot_mapping), int64 [total_tokens].
 
-        Computed on the device from the plan's lengths and page table (decode, prefill and mixed plans).  offsets: int64
-        [batch_size], added to the positions of each request's tokens, e.g. the keys that evict dropped."""
+        Computed on the device from the plan's lengths and page table (decode, prefill and mixed plans; for the chunks of
+        an FP8 or 4-bit cache a plan with kv_dtype="bf16": the pool is not read).  offsets: int64 [batch_size], added to
+        the positions of each request's tokens, e.g. the keys that evict dropped."""
         if self.workspace is None:
             raise ValueError("token_map needs a plan with a workspace")
         positions = slots = None
@@ -697,7 +699,8 @@ class Plan:
 
     def bound_keys(self, cache: KVCache, bounds: KeyBounds, all_pages: bool = False, stream=None) -> None:
         """Write the bounds of the keys of the planned requests' pages: of those that hold a new token (every step,
-        after the KV write), or of all of them (a cache without bounds, or after evict)."""
+        after the KV write), or of all of them (a cache without bounds, after evict, or after a chunk for an FP8 or 4-bit
+        cache: plans with chunks are over bf16 ones)."""
         binding().bound_keys(self._h.value, self, self._streams, stream, C.addressof(cache.struct), cache._device_index,
                              bounds.codes, bounds.scale, all_pages)
 
@@ -707,7 +710,8 @@ class Plan:
         num_blocks], ascending page numbers within the request, -1 behind them.
 
         Of a request with more than num_blocks pages the first num_sink and the last num_recent (at least 1), and the others with the
-        largest upper bound of q.k, summed over the query heads of the KV head (pkv_block_select).  A captured call has room for
+        largest upper bound of q.k, summed over the query heads of the KV head, as 15-bit queries and 8-bit bounds have it
+        (pkv_block_select).  A captured call has room for
         the longest request it was captured with: a longer one gets a row of -1, and device_error() tells."""
         if not self.num_blocks:
             raise ValueError("select needs a plan made with num_blocks")

@@ -14,10 +14,10 @@
 //     reading takes 2.8 at the measured copy rate; the rest is the way to the first bounds (request, page ids: 0.6 us), the
 //     weights (1.4), the selection (1.8) and the launch;
 //   * wide, for few units of many pages: a cluster of C CTAs of 512 threads scores its pages in C slices; the scores go to
-//     the first CTA's shared memory, which selects.  2 x 8 units of 8192 pages (33.5 MB): 14.2 us, 5.1 at the copy rate; the
+//     the first CTA's shared memory, which selects.  2 x 8 units of 8192 pages (33.5 MB): 14.3 us, 5.1 at the copy rate; the
 //     slices stream for 7.9 us (16 clusters of 6: 96 SMs; of 7 or 8 no 16 run at once, and half-size CTAs in clusters
 //     of 12 to 16 take 15.5), the selection behind them takes 3.7.
-// A page takes 8 lanes (head_dim 128): two 16-byte loads each, past L1 (14.4 -> 14.2 us), 16 two-way 16 x 8 bit dot
+// A page takes 8 lanes (head_dim 128): two 16-byte loads each, past L1 (0.2 us of the 14.3), 16 two-way 16 x 8 bit dot
 // products, three shuffles.  Loads through a ring in shared memory instead of registers: 15.5 us (4 to 8 in flight), 17.7 (12).
 // The selection is a radix select on the scores less their smallest, cut by the digits that their range has (a range
 // known before the scores, from the weights, is too coarse: 18.0 us); once a digit holds at most 256 keys they are
@@ -367,7 +367,8 @@ __global__ void __launch_bounds__(Form<WIDE>::THREADS, Form<WIDE>::CTAS) block_s
       }
       if (ahead < rest) atomicOr(&lives[own.y >> 5], 1u << (own.y & 31u));
     }
-  } else if (warp == 0) {  // many equal keys: the first `rest` of them, counted by one warp
+  } else if (warp == 0) {  // many equal keys: the first `rest` of them, counted by one warp (2 x 8 units of 8192 equal scores
+                           // 30 us, unequal ones 14.3; 8 units of 49152: 150 and 60)
     for (int wd = 0; wd < words; ++wd) {
       const int b = wd * 32 + lane;
       const uint32_t k = b < nb ? keys[b] - least : 0u;  // (shift is 0)

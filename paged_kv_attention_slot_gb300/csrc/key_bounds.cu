@@ -9,9 +9,10 @@
 // they are; E4M3 values and E2M1 values times their block scale are f16 values), so the divisions come after the
 // last key.  The rows of every page are read before its request is known (which only says how many are valid).  At
 // the end the channels are shared out over the lanes before they are divided and rounded: small pages are bound by
-// those instructions, not by memory.  64 x 512 to 4096 keys x 8 heads, pages of 16: bf16 46 us for 287 MB, 93 % of the
-// measured copy rate (kept in L1: 48.8; 66 registers instead of 64: 51.3); 64 x 2048 to 4096 keys: E4M3 62 us, 55 % (128-token
-// pages 37), NVFP4 67 us, 31 % (33).  A decode step's one page per request: 2.5 us.
+// those instructions, not by memory.  64 x 512 to 4096 keys x 8 heads, pages of 16: bf16 47 us for 287 MB, 91 % of the
+// measured copy rate (kept in L1: 2.5 more; 66 registers instead of 64: 5); 64 x 2048 to 4096 keys: E4M3 62 us, 55 % (128-token
+// pages 36), NVFP4 66 us, 31 % (32).  A decode step's one page per request: 2.6 us.  Not writing what a captured call's new
+// plan lists beyond the pool, or behind its last request, is 0.8 of the 47 us.
 // A call for few large pages shares a page's rows among the four warps of a CTA.
 
 #include <cuda_bf16.h>

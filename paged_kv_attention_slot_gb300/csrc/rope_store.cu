@@ -14,7 +14,8 @@
 // compute the token's sines and cosines once for all heads, while every thread's row pieces are on their
 // way.  A thread takes 16 elements of a row as two 16-byte vectors that hold both halves of 8 pairs.  8191 tokens of
 // 32 + 8 + 8 heads, bf16 (201 MB): 31.8 us, 95 % of the measured copy rate; 2047 tokens of 64 + 8 + 8 heads into an E4M3
-// pool (80 MB): 13.9 us, 86 %; 64 tokens: 1.9 us, one chain of dependent reads.
+// pool (80 MB): 13.9 us, 86 %; 64 tokens: 1.9 us, one chain of dependent reads.  An NVFP4 pool takes 39.0 us for the 8191
+// tokens (177 MB, 68 %) and 2.5 for the 64: its quantisation needs up to 64 registers, so fewer CTAs hide each other's chain.
 // Many small CTAs hide each other's chain (position -> angle -> barrier): of up to 256 threads, at 40 registers, for more
 // tokens than SMs (8191 tokens: 384 threads 38.2 us, at 50 registers 41.8, at 32 with spills 43.1); up to
 // that many tokens all pieces in one round, where 512 threads do (64 tokens: 256 threads 2.2 us).
